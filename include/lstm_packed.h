@@ -688,6 +688,212 @@ lstm_status lstm_md_bwd(const lstm_md_plan* plan, const lstm_md_shape* shape, co
                         const float* x, void* workspace, const float* dy, float* dx, const lstm_md_grads* grads,
                         void* scratch, void* stream);
 
+/* ======================================================================
+ * Gated linear recurrence over the packed rows
+ *
+ * The cell without the recurrent product: every gate depends on the frame
+ * alone, so the state of a unit is a chain of affine maps and is found by a
+ * scan over time instead of a step-by-step recurrence ("Single Stream
+ * Parallelization of Generalized LSTM-Like RNNs on a GPU", Sec. 3: only the
+ * recurrent part of the graph is sequential; here it is linear).  Per
+ * direction, unit and sequence, with sig the logistic function:
+ *     LSTM_GLR_TIED   h_t = sig(f_t) h_{t-1} + (1 - sig(f_t)) z_t
+ *     LSTM_GLR_GATED  h_t = sig(f_t) h_{t-1} + sig(i_t) z_t
+ * f, z, i are pre-activations that the caller's projection made (z enters as
+ * it is); h_0 = 0 unless given.  The reverse direction runs from the last
+ * frame to the first.  Works on every plan: packed, segments, windows, and
+ * the padded comparator (whose masked rows read nothing; their outputs and
+ * gradients are set to zero).
+ *
+ * Arithmetic: the state, the gates and every product are fp32 whatever the
+ * dtype; outputs are rounded once.  The order of every sum is fixed by the
+ * plan and the shape: repeated calls agree bitwise.
+ *
+ * Device pointers of this section need the alignment of their element type
+ * only, workspaces 16 bytes; rows whose pointers, strides and widths allow
+ * 8- or 16-byte accesses are read and written that way.
+ * ====================================================================== */
+
+typedef enum { LSTM_GLR_TIED = 0, LSTM_GLR_GATED = 1 } lstm_glr_cell;
+
+typedef struct {
+    int32_t hidden_size;     /* H: units per direction, 1..65536 */
+    int32_t num_directions;  /* 1 (forward only) or 2 (forward and reverse) */
+    int32_t dtype;           /* lstm_dtype of the gates, y, and their gradients */
+    int32_t cell;            /* lstm_glr_cell */
+} lstm_glr_shape;
+
+/* Pre-activations, device: unit u of direction d in row r at
+ * f[r * row_stride + d * dir_stride + u] (elements), the same for z and i, so
+ * they may be blocks of one projection's output.  i: gated cell only, else
+ * NULL.  row_stride >= H; dir_stride >= H when there are two directions. */
+typedef struct {
+    const void* f;
+    const void* z;
+    const void* i;
+    int64_t row_stride;
+    int64_t dir_stride;
+} lstm_glr_gates;
+
+/* Gradients in the same form (they may be blocks of one buffer, with strides
+ * of its own); overwritten. */
+typedef struct {
+    void* f;
+    void* z;
+    void* i;
+    int64_t row_stride;
+    int64_t dir_stride;
+} lstm_glr_gate_grads;
+
+/* Bytes of the workspace that lstm_glr_fwd leaves for lstm_glr_bwd: the state
+ * before every 64th step of each sequence and direction, fp32 (1/64 of a
+ * state per frame).  0 on a bad argument. */
+size_t lstm_glr_workspace_bytes(const lstm_plan* plan, const lstm_glr_shape* shape);
+
+/*
+ * Forward pass.
+ *   h0         [ndir][B][H] fp32, caller order; NULL = zero
+ *   y          [rows][ndir*H] dtype: h of every row
+ *   h_n        [ndir][B][H] fp32: the states after each sequence's last step
+ *              (h0 for a sequence of length 0); NULL to skip
+ *   workspace  lstm_glr_workspace_bytes, kept for lstm_glr_bwd; NULL when no
+ *              backward pass follows
+ * The plan's device must be the current one (else LSTM_ERR_INVALID_ARG).
+ */
+lstm_status lstm_glr_fwd(const lstm_plan* plan, const lstm_glr_shape* shape, const lstm_glr_gates* gates,
+                         const float* h0, void* y, float* h_n, void* workspace, void* stream);
+
+/*
+ * Backward pass of the loss L = sum <y, dy> + <h_n, dh_n>.
+ *   gates, workspace  as given to and left by lstm_glr_fwd (read only: the
+ *                     same workspace may serve several backward passes)
+ *   dy         [rows][ndir*H] dtype
+ *   dh_n       [ndir][B][H] fp32, caller order; NULL = zero
+ *   grads      dL/df, dL/dz and (gated cell) dL/di
+ *   dh0        [ndir][B][H] fp32: dL/dh0 (dh_n for a sequence of length 0);
+ *              NULL to skip
+ */
+lstm_status lstm_glr_bwd(const lstm_plan* plan, const lstm_glr_shape* shape, const lstm_glr_gates* gates,
+                         const void* workspace, const void* dy, const float* dh_n,
+                         const lstm_glr_gate_grads* grads, float* dh0, void* stream);
+
+/*
+ * One new frame of each of `rows` streams (num_directions must be 1): the
+ * recurrence's step for streaming use, without a plan.
+ *   gates      `rows` rows
+ *   slots      [rows] int32, device: the state row of each stream in a cache
+ *              of num_slots states; NULL = stream r has state r.  A row whose
+ *              slot is outside 0..num_slots-1 is idle: its y is zero and no
+ *              state is read or written.  Two live rows must not name the
+ *              same slot.
+ *   state_in, state_out  [num_slots][H] fp32; may be the same array.  Slots
+ *              that no row names are not written.
+ *   y          [rows][H] dtype
+ */
+lstm_status lstm_glr_step(const lstm_glr_shape* shape, const lstm_glr_gates* gates, int32_t rows,
+                          const int32_t* slots, int32_t num_slots, const float* state_in, float* state_out,
+                          void* y, void* stream);
+
+/* ======================================================================
+ * Norms before and after a block, with its gate and residual scale
+ *
+ * A block (a recurrent layer, a projection) of a deep stack reads a
+ * normalised row and adds its own normalised, gated and scaled output to the
+ * residual stream.  One call does what stands between two blocks, row by row:
+ *     v  = norm_post(y) w_post + b_post          the norm after the block
+ *     x' = x + scale * v * act(gate)             gate and residual scale
+ *     n  = norm_pre(x') w_pre + b_pre            the norm before the next one
+ * with act = 1, sig(g) or g sig(g), and per row of D values
+ *     LSTM_NORM_RMS    norm(v) = v / sqrt(mean(v^2) + eps)
+ *     LSTM_NORM_LAYER  norm(v) = (v - mean v) / sqrt(mean((v - mean v)^2) + eps)
+ *     LSTM_NORM_NONE   norm(v) = v
+ * All arithmetic is fp32; x' and n are each rounded once (n is the norm of the
+ * unrounded x').  Column sums of the backward pass are added in a fixed order.
+ * ====================================================================== */
+
+typedef enum { LSTM_NORM_NONE = 0, LSTM_NORM_RMS = 1, LSTM_NORM_LAYER = 2 } lstm_norm_kind;
+typedef enum { LSTM_GATE_NONE = 0, LSTM_GATE_SIGMOID = 1, LSTM_GATE_SILU = 2 } lstm_gate_kind;
+
+typedef struct {
+    int32_t width;         /* D, 1..16384 */
+    int32_t post_kind;     /* lstm_norm_kind after the block */
+    int32_t pre_kind;      /* lstm_norm_kind before the next block; NONE: no n */
+    int32_t gate;          /* lstm_gate_kind */
+    int32_t branch_dtype;  /* lstm_dtype of y, gate and their gradients */
+    int32_t stream_dtype;  /* lstm_dtype of x, x' and their gradients */
+    int32_t norm_dtype;    /* lstm_dtype of n (forward) or dn (backward) */
+    float eps;             /* > 0 */
+} lstm_block_norm_shape;
+
+/* fp32 [D] each; a NULL weight or scale counts as 1, a NULL bias as 0.  With
+ * post_kind NONE w_post and b_post must be NULL, with pre_kind NONE w_pre and
+ * b_pre. */
+typedef struct {
+    const float* w_post;
+    const float* b_post;
+    const float* scale;
+    const float* w_pre;
+    const float* b_pre;
+} lstm_block_norm_params;
+
+/* Their gradients, [D] fp32, overwritten; any may be NULL (not wanted). */
+typedef struct {
+    float* w_post;
+    float* b_post;
+    float* scale;
+    float* w_pre;
+    float* b_pre;
+} lstm_block_norm_grads;
+
+/* Rows in: x [rows][D]; y and gate with row strides in elements (>= D).
+ * y NULL: there is no block yet, only the first pre-norm, n = norm_pre(x)
+ * (post_kind and gate must be NONE then). */
+typedef struct {
+    const void* x;
+    const void* y;
+    const void* gate;
+    int64_t y_stride;
+    int64_t gate_stride;
+} lstm_block_norm_inputs;
+
+typedef struct {
+    void* dx;
+    void* dy;
+    void* dgate;
+    int64_t dy_stride;
+    int64_t dgate_stride;
+} lstm_block_norm_input_grads;
+
+/*
+ * Forward pass over `rows` rows.
+ *   x_out   [rows][D] stream dtype: x'; may be x itself; NULL with y NULL
+ *   n       [rows][D] norm dtype; NULL with pre_kind NONE
+ *   stats   [rows][4] fp32 (mean and 1/deviation of both norms), kept for
+ *           lstm_block_norm_bwd; NULL when no backward pass follows
+ */
+lstm_status lstm_block_norm_fwd(const lstm_block_norm_shape* shape, const lstm_block_norm_params* params,
+                                const lstm_block_norm_inputs* in, int64_t rows, void* x_out, void* n,
+                                float* stats, void* stream);
+
+/* Bytes of lstm_block_norm_bwd's scratch: partial column sums, a size that
+ * depends on the shape and rows only.  0 on a bad argument. */
+size_t lstm_block_norm_scratch_bytes(const lstm_block_norm_shape* shape, int64_t rows);
+
+/*
+ * Backward pass.
+ *   in      as given to lstm_block_norm_fwd (x is the stream before the block:
+ *           not overwritten in between); stats as left by it
+ *   dx_out  [rows][D] stream dtype: dL/dx' from beyond this call; NULL = zero
+ *   dn      [rows][D] norm dtype; NULL = zero
+ *   din     dx [rows][D] stream dtype (may be dx_out itself), dy and (with a
+ *           gate) dgate with their own strides
+ *   grads   the parameters' gradients
+ */
+lstm_status lstm_block_norm_bwd(const lstm_block_norm_shape* shape, const lstm_block_norm_params* params,
+                                const lstm_block_norm_inputs* in, int64_t rows, const float* stats,
+                                const void* dx_out, const void* dn, const lstm_block_norm_input_grads* din,
+                                const lstm_block_norm_grads* grads, void* scratch, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -37,9 +37,14 @@ EXPORTED = (
     "lstm_md_plan_placement", "lstm_md_plan_step_cells", "lstm_md_plan_set_wait_limit", "lstm_md_status_poll",
     "lstm_md_plan_launch_count", "lstm_md_workspace_bytes", "lstm_md_scratch_bytes", "lstm_md_fwd", "lstm_md_bwd",
     "lstm_md_plan_enable_timing", "lstm_md_plan_read_timing", "lstm_md_debug_skip_arrival",
+    "lstm_glr_workspace_bytes", "lstm_glr_fwd", "lstm_glr_bwd", "lstm_glr_step",
+    "lstm_block_norm_fwd", "lstm_block_norm_scratch_bytes", "lstm_block_norm_bwd",
 )
 
 KERNEL_KINDS = ("pack", "unpack", "input_gemm", "rec_fwd", "rec_bwd", "gemm_dx", "gemm_dw", "gemm_dr", "convert")
+GLR_CELLS = ("tied", "gated")
+NORM_KINDS = ("none", "rms", "layer")
+GATE_KINDS = ("none", "sigmoid", "silu")
 MD_KINDS = ("md_input", "md_fwd", "md_bwd", "md_grads")
 
 
@@ -80,6 +85,33 @@ class MdParams(ctypes.Structure):
 class MdGrads(ctypes.Structure):
     _fields_ = [("W", ctypes.c_void_p), ("U1", ctypes.c_void_p), ("U2", ctypes.c_void_p), ("b", ctypes.c_void_p),
                 ("peep", ctypes.c_void_p)]
+
+
+class GlrShape(ctypes.Structure):
+    _fields_ = [("hidden_size", ctypes.c_int32), ("num_directions", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("cell", ctypes.c_int32)]
+
+
+class GlrGates(ctypes.Structure):
+    """lstm_glr_gates and lstm_glr_gate_grads."""
+    _fields_ = [("f", ctypes.c_void_p), ("z", ctypes.c_void_p), ("i", ctypes.c_void_p),
+                ("row_stride", ctypes.c_int64), ("dir_stride", ctypes.c_int64)]
+
+
+class BlockNormShape(ctypes.Structure):
+    _fields_ = [(k, ctypes.c_int32) for k in ("width", "post_kind", "pre_kind", "gate", "branch_dtype", "stream_dtype",
+                                              "norm_dtype")] + [("eps", ctypes.c_float)]
+
+
+class BlockNormParams(ctypes.Structure):
+    """lstm_block_norm_params and lstm_block_norm_grads."""
+    _fields_ = [(k, ctypes.c_void_p) for k in ("w_post", "b_post", "scale", "w_pre", "b_pre")]
+
+
+class BlockNormInputs(ctypes.Structure):
+    """lstm_block_norm_inputs and lstm_block_norm_input_grads."""
+    _fields_ = [("x", ctypes.c_void_p), ("y", ctypes.c_void_p), ("gate", ctypes.c_void_p),
+                ("y_stride", ctypes.c_int64), ("gate_stride", ctypes.c_int64)]
 
 
 class LSTMError(RuntimeError):
@@ -163,6 +195,17 @@ def _declare(lib):
                                             vp]),
         "lstm_bwd_noalloc": (c, [vp, ctypes.POINTER(LayerShape), ctypes.POINTER(LayerParams), vp, vp, vp, vp, vp,
                                  ctypes.POINTER(LayerGrads), vp]),
+        "lstm_glr_workspace_bytes": (sz, [vp, ctypes.POINTER(GlrShape)]),
+        "lstm_glr_fwd": (c, [vp, ctypes.POINTER(GlrShape), ctypes.POINTER(GlrGates), vp, vp, vp, vp, vp]),
+        "lstm_glr_bwd": (c, [vp, ctypes.POINTER(GlrShape), ctypes.POINTER(GlrGates), vp, vp, vp,
+                             ctypes.POINTER(GlrGates), vp, vp]),
+        "lstm_glr_step": (c, [ctypes.POINTER(GlrShape), ctypes.POINTER(GlrGates), i32, vp, i32, vp, vp, vp, vp]),
+        "lstm_block_norm_fwd": (c, [ctypes.POINTER(BlockNormShape), ctypes.POINTER(BlockNormParams),
+                                    ctypes.POINTER(BlockNormInputs), i64, vp, vp, vp, vp]),
+        "lstm_block_norm_scratch_bytes": (sz, [ctypes.POINTER(BlockNormShape), i64]),
+        "lstm_block_norm_bwd": (c, [ctypes.POINTER(BlockNormShape), ctypes.POINTER(BlockNormParams),
+                                    ctypes.POINTER(BlockNormInputs), i64, vp, vp, vp, ctypes.POINTER(BlockNormInputs),
+                                    ctypes.POINTER(BlockNormParams), vp, vp]),
         "lstm_plan_dims": (c, [pi32, i32, i32, pi32, ctypes.POINTER(i64)]),
         "lstm_plan_compute_host": (c, [pi32, i32, i32, pi32, pi32, pi32, pi32, pi32, pi32, pi32]),
     }

@@ -11,6 +11,7 @@ namespace lstm {
 
 constexpr int kMaxCtasPerDir = 160;     // > 152 SMs; one flag per CTA
 constexpr int kRecThreads = 256;        // block size of the recurrent kernels
+constexpr int kScanChunk = 64;          // steps between the states that the linear recurrence keeps for its backward pass
 
 // Device status word layout (one int64 per plan):
 //   low 32 bits  lstm_status of the first failure (0 = none)
@@ -58,11 +59,13 @@ struct Plan {
     int32_t* h_perm = nullptr;      // [B]  caller index of slot j
     int32_t* h_len = nullptr;       // [B]  length of slot j
     int32_t* h_cstart = nullptr;    // [B+1] caller-order frame offsets
+    int64_t chunks = 0;             // pieces of at most kScanChunk steps of all sequences
     // device tables
     int32_t* d_bs = nullptr;
     int32_t* d_off = nullptr;
     int32_t* d_perm = nullptr;
     int32_t* d_len = nullptr;
+    int32_t* d_chunk = nullptr;     // [B+1] first piece of each slot (pieces of kScanChunk steps)
     int32_t* d_row_src = nullptr;   // [rows] caller-order frame of packed row (-1 = padding)
     int32_t* d_prev_fwd = nullptr;  // [rows] row holding h_{t-1} for the forward direction (-1 none)
     int32_t* d_prev_rev = nullptr;  // [rows] row holding the reverse direction's previous state

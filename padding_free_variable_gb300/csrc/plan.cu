@@ -118,7 +118,7 @@ static void free_plan(Plan& p)
     free(p.h_bs); free(p.h_off); free(p.h_perm); free(p.h_len); free(p.h_cstart);
     cudaFree(p.d_bs); cudaFree(p.d_off); cudaFree(p.d_perm); cudaFree(p.d_len);
     cudaFree(p.d_row_src); cudaFree(p.d_prev_fwd); cudaFree(p.d_prev_rev); cudaFree(p.d_row_slot);
-    cudaFree(p.d_row_dst);
+    cudaFree(p.d_row_dst); cudaFree(p.d_chunk);
     cudaFree(p.d_flags); cudaFree(p.d_status);
     p = Plan();
 }
@@ -245,6 +245,15 @@ static lstm_status create_plan(const int32_t* lengths, int32_t B, bool padded, l
     if (e == cudaSuccess && fm) e = upload(&p.d_row_dst, row_dst.data(), (size_t)rows);
     if (e == cudaSuccess) e = upload(&p.d_prev_fwd, prev_fwd.data(), (size_t)rows);
     if (e == cudaSuccess) e = upload(&p.d_prev_rev, prev_rev.data(), (size_t)rows);
+    {   // first kScanChunk-step piece of each slot
+        std::vector<int32_t> chunk(B + 1);
+        for (int32_t j = 0; j < B; ++j) {
+            chunk[j] = (int32_t)p.chunks;
+            p.chunks += (p.h_len[j] + kScanChunk - 1) / kScanChunk;
+        }
+        chunk[B] = (int32_t)p.chunks;
+        if (e == cudaSuccess) e = upload(&p.d_chunk, chunk.data(), (size_t)B + 1);
+    }
     {   // sorted slot of each packed row (row off[t] + j holds slot j)
         std::vector<int32_t> row_slot(rows);
         for (int t = 0; t < T; ++t)
