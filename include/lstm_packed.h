@@ -726,7 +726,8 @@ typedef struct {
 /* Pre-activations, device: unit u of direction d in row r at
  * f[r * row_stride + d * dir_stride + u] (elements), the same for z and i, so
  * they may be blocks of one projection's output.  i: gated cell only, else
- * NULL.  row_stride >= H; dir_stride >= H when there are two directions. */
+ * NULL.  H <= row_stride <= 2^29 (else LSTM_ERR_UNSUPPORTED); dir_stride >= H
+ * when there are two directions. */
 typedef struct {
     const void* f;
     const void* z;
@@ -750,6 +751,11 @@ typedef struct {
  * state per frame).  0 on a bad argument. */
 size_t lstm_glr_workspace_bytes(const lstm_plan* plan, const lstm_glr_shape* shape);
 
+/* Bytes of the transient scratch of lstm_glr_fwd and lstm_glr_bwd (the maps
+ * of the pieces that few long sequences are cut into, so that their pieces
+ * run side by side); 0 where none is needed, and on a bad argument. */
+size_t lstm_glr_scratch_bytes(const lstm_plan* plan, const lstm_glr_shape* shape);
+
 /*
  * Forward pass.
  *   h0         [ndir][B][H] fp32, caller order; NULL = zero
@@ -758,10 +764,13 @@ size_t lstm_glr_workspace_bytes(const lstm_plan* plan, const lstm_glr_shape* sha
  *              (h0 for a sequence of length 0); NULL to skip
  *   workspace  lstm_glr_workspace_bytes, kept for lstm_glr_bwd; NULL when no
  *              backward pass follows
+ *   scratch    lstm_glr_scratch_bytes; NULL: no sequence is cut (slower for
+ *              few long ones)
  * The plan's device must be the current one (else LSTM_ERR_INVALID_ARG).
  */
 lstm_status lstm_glr_fwd(const lstm_plan* plan, const lstm_glr_shape* shape, const lstm_glr_gates* gates,
-                         const float* h0, void* y, float* h_n, void* workspace, void* stream);
+                         const float* h0, void* y, float* h_n, void* workspace, void* scratch,
+                         void* stream);
 
 /*
  * Backward pass of the loss L = sum <y, dy> + <h_n, dh_n>.
@@ -772,10 +781,11 @@ lstm_status lstm_glr_fwd(const lstm_plan* plan, const lstm_glr_shape* shape, con
  *   grads      dL/df, dL/dz and (gated cell) dL/di
  *   dh0        [ndir][B][H] fp32: dL/dh0 (dh_n for a sequence of length 0);
  *              NULL to skip
+ *   scratch    as for lstm_glr_fwd
  */
 lstm_status lstm_glr_bwd(const lstm_plan* plan, const lstm_glr_shape* shape, const lstm_glr_gates* gates,
                          const void* workspace, const void* dy, const float* dh_n,
-                         const lstm_glr_gate_grads* grads, float* dh0, void* stream);
+                         const lstm_glr_gate_grads* grads, float* dh0, void* scratch, void* stream);
 
 /*
  * One new frame of each of `rows` streams (num_directions must be 1): the

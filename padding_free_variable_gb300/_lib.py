@@ -37,7 +37,7 @@ EXPORTED = (
     "lstm_md_plan_placement", "lstm_md_plan_step_cells", "lstm_md_plan_set_wait_limit", "lstm_md_status_poll",
     "lstm_md_plan_launch_count", "lstm_md_workspace_bytes", "lstm_md_scratch_bytes", "lstm_md_fwd", "lstm_md_bwd",
     "lstm_md_plan_enable_timing", "lstm_md_plan_read_timing", "lstm_md_debug_skip_arrival",
-    "lstm_glr_workspace_bytes", "lstm_glr_fwd", "lstm_glr_bwd", "lstm_glr_step",
+    "lstm_glr_workspace_bytes", "lstm_glr_scratch_bytes", "lstm_glr_fwd", "lstm_glr_bwd", "lstm_glr_step",
     "lstm_block_norm_fwd", "lstm_block_norm_scratch_bytes", "lstm_block_norm_bwd",
 )
 
@@ -196,9 +196,10 @@ def _declare(lib):
         "lstm_bwd_noalloc": (c, [vp, ctypes.POINTER(LayerShape), ctypes.POINTER(LayerParams), vp, vp, vp, vp, vp,
                                  ctypes.POINTER(LayerGrads), vp]),
         "lstm_glr_workspace_bytes": (sz, [vp, ctypes.POINTER(GlrShape)]),
-        "lstm_glr_fwd": (c, [vp, ctypes.POINTER(GlrShape), ctypes.POINTER(GlrGates), vp, vp, vp, vp, vp]),
+        "lstm_glr_scratch_bytes": (sz, [vp, ctypes.POINTER(GlrShape)]),
+        "lstm_glr_fwd": (c, [vp, ctypes.POINTER(GlrShape), ctypes.POINTER(GlrGates), vp, vp, vp, vp, vp, vp]),
         "lstm_glr_bwd": (c, [vp, ctypes.POINTER(GlrShape), ctypes.POINTER(GlrGates), vp, vp, vp,
-                             ctypes.POINTER(GlrGates), vp, vp]),
+                             ctypes.POINTER(GlrGates), vp, vp, vp]),
         "lstm_glr_step": (c, [ctypes.POINTER(GlrShape), ctypes.POINTER(GlrGates), i32, vp, i32, vp, vp, vp, vp]),
         "lstm_block_norm_fwd": (c, [ctypes.POINTER(BlockNormShape), ctypes.POINTER(BlockNormParams),
                                     ctypes.POINTER(BlockNormInputs), i64, vp, vp, vp, vp]),

@@ -11,37 +11,6 @@ namespace lstm {
 namespace {
 
 template <typename T, bool GATED>
-__global__ void glr_fwd_kernel(const GlrArgs p)
-{
-    const int u = blockIdx.x * blockDim.x + threadIdx.x;
-    const int j = blockIdx.y, d = blockIdx.z;
-    if (u >= p.H) return;
-    const int len = p.len[j], steps = p.padded ? p.T : len;
-    const int64_t cell = ((int64_t)d * p.B + p.perm[j]) * p.H + u;
-    float h = p.h0 ? p.h0[cell] : 0.f;
-    for (int s = 0; s < steps; ++s) {
-        const int t = s < len && d == 1 ? len - 1 - s : s;
-        const int64_t row = (int64_t)p.off[t] + j;
-        T* y = (T*)p.y + (row * p.ndir + d) * p.H + u;
-        if (s >= len) {
-            *y = from_f32<T>(0.f);
-            continue;
-        }
-        if (p.ws && s % kScanChunk == 0) p.ws[((int64_t)(p.chunk[j] + s / kScanChunk) * p.ndir + d) * p.H + u] = h;
-        const int64_t at = row * p.ld + d * p.dstride + u;
-        float a, b;
-        sigmoid_pair(to_f32(((const T*)p.f)[at]), a, b);
-        if (GATED) {
-            float c;
-            sigmoid_pair(to_f32(((const T*)p.i)[at]), b, c);
-        }
-        h = fmaf(a, h, b * to_f32(((const T*)p.z)[at]));
-        *y = from_f32<T>(h);
-    }
-    if (p.h_n) p.h_n[cell] = h;
-}
-
-template <typename T, bool GATED>
 __global__ void glr_bwd_kernel(const GlrArgs p)
 {
     const int u = blockIdx.x * blockDim.x + threadIdx.x;
@@ -150,6 +119,8 @@ bool right_device(const Plan& p)
     return cudaGetDevice(&dev) == cudaSuccess && dev == p.device;
 }
 
+bool fits(const void* p, int64_t bytes) { return ((uintptr_t)p & (bytes - 1)) == 0; }
+
 GlrArgs plan_args(const Plan& p, const lstm_glr_shape& s, const lstm_glr_gates& g)
 {
     GlrArgs a;
@@ -183,6 +154,46 @@ lstm_status pass_through(const float* in, float* out, size_t bytes, cudaStream_t
 
 }  // namespace
 
+GlrRows glr_rows(const GlrArgs& a, int elem)
+{
+    // every row of every operand starts on a multiple of `bytes`, and so does its length
+    auto whole = [&](int64_t bytes) {
+        bool ok = true;
+        for (int64_t n : {(int64_t)a.H, a.ld, a.ndir == 1 ? 0 : a.dstride, a.gld, a.ndir == 1 ? 0 : a.gdstride})
+            ok = ok && n * elem % bytes == 0;
+        for (const void* p : {a.f, a.z, a.i, (const void*)a.y, a.dy, (const void*)a.df, (const void*)a.dz, (const void*)a.di})
+            ok = ok && fits(p, bytes);
+        return ok;
+    };
+    // fp32 rows of at most 32 units fill a warp with one unit a lane
+    if (whole(16) && (elem == 2 || a.H > 32)) return GLR_WIDE;
+    return whole(4) ? GLR_NARROW : GLR_SINGLE;
+}
+
+void glr_cut(const Plan& p, int V, int ctas, void* scratch, GlrArgs* a)
+{
+    // An uncut sequence takes T/64 iterations one after another; all of them, spread evenly over
+    // the CTAs that the GPU holds, `share`.  Where the longest sequence would run far past that, it
+    // is cut (every piece's gates are then read twice), into pieces short enough to spread well and
+    // long enough that starting them (about two iterations) does not show.
+    const int64_t blocks = ceil_div(a->H, 32 * V), slots = (int64_t)p.num_sms * ctas;
+    const int64_t share = p.chunks * blocks * a->ndir / slots, longest = ceil_div(p.T, kScanChunk);
+    int l = p.levels - 1;
+    if (scratch && longest > share * 3 / 2 + 12)
+        for (l = 0; l < p.levels - 1 && ((int64_t)kScanPiece << l) < kScanChunk * share / 5; ++l) {}
+    a->pieces = p.d_pieces + p.level_first[l];
+    a->count = p.level_count[l];
+    a->cut = l < p.levels - 1;
+    a->piece = a->cut ? kScanPiece << l : INT32_MAX;
+    a->maps = (float4*)scratch;
+}
+
+size_t glr_scratch(const Plan& p, const lstm_glr_shape& s)
+{
+    // the finest level's maps, 8 bytes a unit, in blocks of at most 64 units
+    return p.levels < 2 ? 0 : (size_t)p.level_count[0] * s.num_directions * (size_t)ceil_div(s.hidden_size, 64) * 64 * 8;
+}
+
 }  // namespace lstm
 
 using namespace lstm;
@@ -196,8 +207,14 @@ size_t lstm_glr_workspace_bytes(const lstm_plan* plan, const lstm_glr_shape* sha
     return n > 16 ? n : 16;
 }
 
+size_t lstm_glr_scratch_bytes(const lstm_plan* plan, const lstm_glr_shape* shape)
+{
+    if (!plan || check_glr_shape(shape) != LSTM_OK) return 0;
+    return glr_scratch(plan->p, *shape);
+}
+
 lstm_status lstm_glr_fwd(const lstm_plan* plan, const lstm_glr_shape* shape, const lstm_glr_gates* gates,
-                         const float* h0, void* y, float* h_n, void* workspace, void* stream)
+                         const float* h0, void* y, float* h_n, void* workspace, void* scratch, void* stream)
 {
     if (!plan || !gates) return LSTM_ERR_INVALID_ARG;
     lstm_status st = check_glr_shape(shape);
@@ -205,25 +222,20 @@ lstm_status lstm_glr_fwd(const lstm_plan* plan, const lstm_glr_shape* shape, con
     const Plan& p = plan->p;
     const lstm_glr_shape& s = *shape;
     cudaStream_t cs = (cudaStream_t)stream;
-    if (!aligned(h0, 4) || !aligned(h_n, 4) || !aligned(workspace, 16) || !right_device(p)) return LSTM_ERR_INVALID_ARG;
+    if (!aligned(h0, 4) || !aligned(h_n, 4) || !aligned(workspace, 16) || !aligned(scratch, 16) || !right_device(p)) return LSTM_ERR_INVALID_ARG;
     if (p.rows == 0) return pass_through(h0, h_n, sizeof(float) * s.num_directions * p.B * s.hidden_size, cs);
     if (!y || !aligned(y, s.dtype == LSTM_BF16 ? 2 : 4) ||
         !good_gates(s, gates->f, gates->z, gates->i, gates->row_stride, gates->dir_stride))
         return LSTM_ERR_INVALID_ARG;
+    if (gates->row_stride > kGlrMaxStride) return LSTM_ERR_UNSUPPORTED;
     GlrArgs a = plan_args(p, s, *gates);
     a.h0 = h0; a.y = y; a.h_n = h_n; a.ws = (float*)workspace;
-    if (p.B > 65535) return LSTM_ERR_UNSUPPORTED;
-    dim3 grid(ceil_div(s.hidden_size, 64), p.B, s.num_directions);
-    dispatch(s, [&](auto* t, auto gated) {
-        glr_fwd_kernel<std::remove_pointer_t<decltype(t)>, decltype(gated)::value><<<grid, 64, 0, cs>>>(a);
-    });
-    trace_end(p, -1, cs, 1);
-    return launched();
+    return launch_glr_fwd(p, s, a, scratch, cs);
 }
 
 lstm_status lstm_glr_bwd(const lstm_plan* plan, const lstm_glr_shape* shape, const lstm_glr_gates* gates,
                          const void* workspace, const void* dy, const float* dh_n,
-                         const lstm_glr_gate_grads* grads, float* dh0, void* stream)
+                         const lstm_glr_gate_grads* grads, float* dh0, void* scratch, void* stream)
 {
     if (!plan || !gates || !grads) return LSTM_ERR_INVALID_ARG;
     lstm_status st = check_glr_shape(shape);
@@ -231,12 +243,13 @@ lstm_status lstm_glr_bwd(const lstm_plan* plan, const lstm_glr_shape* shape, con
     const Plan& p = plan->p;
     const lstm_glr_shape& s = *shape;
     cudaStream_t cs = (cudaStream_t)stream;
-    if (!aligned(dh_n, 4) || !aligned(dh0, 4) || !aligned(workspace, 16) || !right_device(p)) return LSTM_ERR_INVALID_ARG;
+    if (!aligned(dh_n, 4) || !aligned(dh0, 4) || !aligned(workspace, 16) || !aligned(scratch, 16) || !right_device(p)) return LSTM_ERR_INVALID_ARG;
     if (p.rows == 0) return pass_through(dh_n, dh0, sizeof(float) * s.num_directions * p.B * s.hidden_size, cs);
     if (!workspace || !dy || !aligned(dy, s.dtype == LSTM_BF16 ? 2 : 4) ||
         !good_gates(s, gates->f, gates->z, gates->i, gates->row_stride, gates->dir_stride) ||
         !good_gates(s, grads->f, grads->z, grads->i, grads->row_stride, grads->dir_stride))
         return LSTM_ERR_INVALID_ARG;
+    if (gates->row_stride > kGlrMaxStride || grads->row_stride > kGlrMaxStride) return LSTM_ERR_UNSUPPORTED;
     GlrArgs a = plan_args(p, s, *gates);
     a.ws = (float*)const_cast<void*>(workspace); a.dy = dy; a.dh_n = dh_n; a.dh0 = dh0;
     a.df = grads->f; a.dz = grads->z; a.di = grads->i; a.gld = grads->row_stride; a.gdstride = grads->dir_stride;

@@ -118,7 +118,7 @@ static void free_plan(Plan& p)
     free(p.h_bs); free(p.h_off); free(p.h_perm); free(p.h_len); free(p.h_cstart);
     cudaFree(p.d_bs); cudaFree(p.d_off); cudaFree(p.d_perm); cudaFree(p.d_len);
     cudaFree(p.d_row_src); cudaFree(p.d_prev_fwd); cudaFree(p.d_prev_rev); cudaFree(p.d_row_slot);
-    cudaFree(p.d_row_dst); cudaFree(p.d_chunk);
+    cudaFree(p.d_row_dst); cudaFree(p.d_chunk); cudaFree(p.d_pieces);
     cudaFree(p.d_flags); cudaFree(p.d_status);
     p = Plan();
 }
@@ -253,6 +253,33 @@ static lstm_status create_plan(const int32_t* lengths, int32_t B, bool padded, l
         }
         chunk[B] = (int32_t)p.chunks;
         if (e == cudaSuccess) e = upload(&p.d_chunk, chunk.data(), (size_t)B + 1);
+    }
+    {   // pieces of each level, the first pieces of all slots before their second ones
+        std::vector<int4> pieces;
+        std::vector<int32_t> first(B);
+        for (int32_t l = 0; ; ++l) {
+            const int64_t len = (int64_t)kScanPiece << l;
+            int32_t most = 1, sum = 0;
+            for (int32_t j = 0; j < B; ++j) {
+                const int32_t n = std::max<int32_t>(1, (int32_t)((p.h_len[j] + len - 1) / len));
+                first[j] = sum;
+                sum += n;
+                most = std::max(most, n);
+            }
+            p.level_first[l] = (int32_t)pieces.size();
+            p.level_count[l] = sum;
+            for (int32_t k = 0; k < most; ++k)
+                for (int32_t j = 0; j < B; ++j) {
+                    if (k > 0 && (int64_t)p.h_len[j] <= k * len) {
+                        if (!padded) break;         // sorted: no later slot is longer
+                        continue;
+                    }
+                    pieces.push_back(make_int4(j, k, p.h_len[j], first[j]));
+                }
+            p.levels = l + 1;
+            if (most == 1) break;
+        }
+        if (e == cudaSuccess) e = upload(&p.d_pieces, pieces.data(), pieces.size());
     }
     {   // sorted slot of each packed row (row off[t] + j holds slot j)
         std::vector<int32_t> row_slot(rows);

@@ -33,6 +33,7 @@ class Plan:
         lens = np.ascontiguousarray(np.asarray(lengths, dtype=np.int32))
         self.lengths = lens
         self.padded = padded
+        self.scratch = {}       # device buffers of the gated linear recurrence, by size
         h = ctypes.c_void_p()
         lp = lens.ctypes.data_as(ctypes.POINTER(ctypes.c_int32))
         if segments is not None:
@@ -651,6 +652,16 @@ def glr_workspace_bytes(plan: Plan, shape) -> int:
     return int(_lib.load().lstm_glr_workspace_bytes(plan.handle, ctypes.byref(shape)))
 
 
+def _glr_scratch(plan: Plan, shape, device):
+    """The plan's scratch of this size (kept with the plan: its calls share it, one stream at a time)."""
+    need = int(_lib.load().lstm_glr_scratch_bytes(plan.handle, ctypes.byref(shape)))
+    if need == 0:
+        return None
+    if need not in plan.scratch:
+        plan.scratch[need] = torch.empty(need, dtype=torch.uint8, device=device)
+    return plan.scratch[need].data_ptr()
+
+
 def glr_forward(plan: Plan, shape, f, z, i, h0, y, h_n, workspace, stream=None):
     """lstm_glr_fwd: f, z and (gated cell) i [rows, ndir, H] views, h0 / h_n [ndir, B, H] fp32 in caller order or None,
     y [rows, ndir, H]; workspace: a buffer of glr_workspace_bytes that glr_backward reads, or None."""
@@ -661,7 +672,7 @@ def glr_forward(plan: Plan, shape, f, z, i, h0, y, h_n, workspace, stream=None):
         plan.handle, ctypes.byref(shape), ctypes.byref(g), _dense(h0, torch.float32, st, "h0"),
         _dense(y, f.dtype, (plan.rows, nd, H), "y"), _dense(h_n, torch.float32, st, "h_n"),
         _bytes(workspace, glr_workspace_bytes(plan, shape), "workspace") if workspace is not None else None,
-        _stream(stream)), "lstm_glr_fwd")
+        _glr_scratch(plan, shape, f.device), _stream(stream)), "lstm_glr_fwd")
 
 
 def glr_backward(plan: Plan, shape, f, z, i, workspace, dy, dh_n, df, dz, di, dh0, stream=None):
@@ -674,7 +685,7 @@ def glr_backward(plan: Plan, shape, f, z, i, workspace, dy, dh_n, df, dz, di, dh
         plan.handle, ctypes.byref(shape), ctypes.byref(g),
         _bytes(workspace, glr_workspace_bytes(plan, shape), "workspace"), _dense(dy, f.dtype, (plan.rows, nd, H), "dy"),
         _dense(dh_n, torch.float32, st, "dh_n"), ctypes.byref(dg), _dense(dh0, torch.float32, st, "dh0"),
-        _stream(stream)), "lstm_glr_bwd")
+        _glr_scratch(plan, shape, f.device), _stream(stream)), "lstm_glr_bwd")
 
 
 def glr_step(shape, f, z, i, state_in, state_out, y, slots=None, stream=None):

@@ -95,8 +95,8 @@ def test_glr_refusals_without_a_device(lib):
     g = _lib.GlrGates(256, 512, None, 32, 32)
     assert lib.lstm_glr_workspace_bytes(None, ctypes.byref(ok)) == 0
     bad = _lib.LSTM_ERR_INVALID_ARG
-    assert lib.lstm_glr_fwd(None, ctypes.byref(ok), ctypes.byref(g), None, 256, None, None, None) == bad
-    assert lib.lstm_glr_bwd(None, ctypes.byref(ok), ctypes.byref(g), 256, 256, None, ctypes.byref(g), None, None) == bad
+    assert lib.lstm_glr_fwd(None, ctypes.byref(ok), ctypes.byref(g), None, 256, None, None, None, None) == bad
+    assert lib.lstm_glr_bwd(None, ctypes.byref(ok), ctypes.byref(g), 256, 256, None, ctypes.byref(g), None, None, None) == bad
 
     def step(shape=ok, gates=g, rows=4, slots=None, n=4, state=256, y=256):
         return lib.lstm_glr_step(ctypes.byref(shape) if shape else None, ctypes.byref(gates) if gates else None, rows,
