@@ -11,61 +11,6 @@ namespace lstm {
 namespace {
 
 template <typename T, bool GATED>
-__global__ void glr_bwd_kernel(const GlrArgs p)
-{
-    const int u = blockIdx.x * blockDim.x + threadIdx.x;
-    const int j = blockIdx.y, d = blockIdx.z;
-    if (u >= p.H) return;
-    const int len = p.len[j], steps = p.padded ? p.T : len;
-    const int64_t cell = ((int64_t)d * p.B + p.perm[j]) * p.H + u;
-    for (int t = len; t < steps; ++t) {
-        const int64_t g = ((int64_t)p.off[t] + j) * p.gld + d * p.gdstride + u;
-        ((T*)p.df)[g] = from_f32<T>(0.f);
-        ((T*)p.dz)[g] = from_f32<T>(0.f);
-        if (GATED) ((T*)p.di)[g] = from_f32<T>(0.f);
-    }
-    float e = p.dh_n ? p.dh_n[cell] : 0.f;
-    float hp[kScanChunk];
-    for (int s0 = (len - 1) / kScanChunk * kScanChunk; s0 >= 0 && len > 0; s0 -= kScanChunk) {
-        const int n = min(kScanChunk, len - s0);
-        float h = p.ws[((int64_t)(p.chunk[j] + s0 / kScanChunk) * p.ndir + d) * p.H + u];
-        for (int k = 0; k < n; ++k) {
-            const int t = d == 1 ? len - 1 - s0 - k : s0 + k;
-            const int64_t at = ((int64_t)p.off[t] + j) * p.ld + d * p.dstride + u;
-            hp[k] = h;
-            float a, b;
-            sigmoid_pair(to_f32(((const T*)p.f)[at]), a, b);
-            if (GATED) {
-                float c;
-                sigmoid_pair(to_f32(((const T*)p.i)[at]), b, c);
-            }
-            h = fmaf(a, h, b * to_f32(((const T*)p.z)[at]));
-        }
-        for (int k = n - 1; k >= 0; --k) {
-            const int t = d == 1 ? len - 1 - s0 - k : s0 + k;
-            const int64_t row = (int64_t)p.off[t] + j;
-            const int64_t at = row * p.ld + d * p.dstride + u, to = row * p.gld + d * p.gdstride + u;
-            float a, c;
-            sigmoid_pair(to_f32(((const T*)p.f)[at]), a, c);
-            const float z = to_f32(((const T*)p.z)[at]);
-            const float g = to_f32(((const T*)p.dy)[(row * p.ndir + d) * p.H + u]) + e;
-            if (GATED) {
-                float b, nb;
-                sigmoid_pair(to_f32(((const T*)p.i)[at]), b, nb);
-                ((T*)p.df)[to] = from_f32<T>(g * hp[k] * (a * c));
-                ((T*)p.dz)[to] = from_f32<T>(g * b);
-                ((T*)p.di)[to] = from_f32<T>(g * z * (b * nb));
-            } else {
-                ((T*)p.df)[to] = from_f32<T>(g * (hp[k] - z) * (a * c));
-                ((T*)p.dz)[to] = from_f32<T>(g * c);
-            }
-            e = a * g;
-        }
-    }
-    if (p.dh0) p.dh0[cell] = e;
-}
-
-template <typename T, bool GATED>
 __global__ void glr_step_kernel(const GlrArgs p, const int32_t* slots, int rows, int num_slots, const float* state_in,
                                 float* state_out)
 {
@@ -253,13 +198,7 @@ lstm_status lstm_glr_bwd(const lstm_plan* plan, const lstm_glr_shape* shape, con
     GlrArgs a = plan_args(p, s, *gates);
     a.ws = (float*)const_cast<void*>(workspace); a.dy = dy; a.dh_n = dh_n; a.dh0 = dh0;
     a.df = grads->f; a.dz = grads->z; a.di = grads->i; a.gld = grads->row_stride; a.gdstride = grads->dir_stride;
-    if (p.B > 65535) return LSTM_ERR_UNSUPPORTED;
-    dim3 grid(ceil_div(s.hidden_size, 64), p.B, s.num_directions);
-    dispatch(s, [&](auto* t, auto gated) {
-        glr_bwd_kernel<std::remove_pointer_t<decltype(t)>, decltype(gated)::value><<<grid, 64, 0, cs>>>(a);
-    });
-    trace_end(p, -1, cs, 1);
-    return launched();
+    return launch_glr_bwd(p, s, a, scratch, cs);
 }
 
 lstm_status lstm_glr_step(const lstm_glr_shape* shape, const lstm_glr_gates* gates, int32_t rows,

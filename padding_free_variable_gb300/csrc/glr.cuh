@@ -183,6 +183,97 @@ constexpr int64_t kGlrMaxStride = 1 << 29;
 constexpr int kGlrWarps = 8;            // pieces of a CTA's 64 steps, one a warp
 constexpr int kGlrSteps = 8;            // consecutive steps of one thread
 static_assert(kGlrWarps * kGlrSteps == kScanChunk, "a CTA's iteration is one kept state");
+// ---------------------------------------------------------------- affine maps of V units
+
+// V values of a lane, in pairs.
+template <int V> struct Vals {
+    F2 q[V / 2];
+    __device__ __forceinline__ float get(int v) const { return v & 1 ? q[v / 2].hi() : q[v / 2].lo(); }
+    __device__ __forceinline__ void fill(float x)
+    {
+#pragma unroll
+        for (int v = 0; v < V / 2; ++v) q[v] = F2(x, x);
+    }
+    __device__ __forceinline__ void mad(const Vals& a, const Vals& b)       // a * this + b
+    {
+#pragma unroll
+        for (int v = 0; v < V / 2; ++v) q[v] = fma2(a.q[v], q[v], b.q[v]);
+    }
+    __device__ __forceinline__ void mul(const Vals& a)
+    {
+#pragma unroll
+        for (int v = 0; v < V / 2; ++v) q[v] = a.q[v] * q[v];
+    }
+    __device__ __forceinline__ void add(const Vals& a)
+    {
+#pragma unroll
+        for (int v = 0; v < V / 2; ++v) q[v] = q[v] + a.q[v];
+    }
+    __device__ __forceinline__ void sub(const Vals& a)      // exact negation, one rounding
+    {
+#pragma unroll
+        for (int v = 0; v < V / 2; ++v) q[v] = fma2(a.q[v], F2(-1.f, -1.f), q[v]);
+    }
+    __device__ __forceinline__ void sigmoid()
+    {
+#pragma unroll
+        for (int v = 0; v < V / 2; ++v) q[v] = sigmoid2(q[v]);
+    }
+    __device__ __forceinline__ void sigmoids(Vals& s, Vals& c) const
+    {
+#pragma unroll
+        for (int v = 0; v < V / 2; ++v) sigmoid_pair2(q[v], s.q[v], c.q[v]);
+    }
+    template <typename G> __device__ __forceinline__ void each(G&& value)
+    {
+#pragma unroll
+        for (int v = 0; v < V; v += 2) q[v / 2] = F2(value(v), value(v + 1));
+    }
+};
+template <> struct Vals<1> {
+    float q;
+    __device__ __forceinline__ float get(int) const { return q; }
+    __device__ __forceinline__ void fill(float x) { q = x; }
+    __device__ __forceinline__ void mad(const Vals& a, const Vals& b) { q = fmaf(a.q, q, b.q); }
+    __device__ __forceinline__ void mul(const Vals& a) { q *= a.q; }
+    __device__ __forceinline__ void add(const Vals& a) { q += a.q; }
+    __device__ __forceinline__ void sub(const Vals& a) { q -= a.q; }
+    __device__ __forceinline__ void sigmoid() { q = rcp_approx(1.f + ex2_approx(q * kNegLog2e)); }
+    __device__ __forceinline__ void sigmoids(Vals& s, Vals& c) const { sigmoid_pair(q, s.q, c.q); }
+    template <typename G> __device__ __forceinline__ void each(G&& value) { q = value(0); }
+};
+
+// h -> A h + U of a warp's 32 V units, in shared memory.
+template <int V> struct WarpMap {
+    float4 m[V / 2][32];
+    __device__ __forceinline__ void put(int lane, const Vals<V>& A, const Vals<V>& U)
+    {
+#pragma unroll
+        for (int v = 0; v < V / 2; ++v) m[v][lane] = make_float4(A.q[v].lo(), A.q[v].hi(), U.q[v].lo(), U.q[v].hi());
+    }
+    __device__ __forceinline__ void get(int lane, Vals<V>& A, Vals<V>& U) const
+    {
+#pragma unroll
+        for (int v = 0; v < V / 2; ++v) {
+            const float4 x = m[v][lane];
+            A.q[v] = F2(x.x, x.y);
+            U.q[v] = F2(x.z, x.w);
+        }
+    }
+    __device__ __forceinline__ void apply(int lane, Vals<V>& h) const
+    {
+        Vals<V> A, U;
+        get(lane, A, U);
+        h.mad(A, U);
+    }
+};
+template <> struct WarpMap<1> {
+    float2 m[32];
+    __device__ __forceinline__ void put(int lane, const Vals<1>& A, const Vals<1>& U) { m[lane] = make_float2(A.q, U.q); }
+    __device__ __forceinline__ void get(int lane, Vals<1>& A, Vals<1>& U) const { A.q = m[lane].x; U.q = m[lane].y; }
+    __device__ __forceinline__ void apply(int lane, Vals<1>& h) const { h.q = fmaf(m[lane].x, h.q, m[lane].y); }
+};
+
 // How a kernel takes its rows.
 enum GlrRows {
     GLR_WIDE = 0,       // 2 units a lane; rows through shared memory in 16-byte pieces
@@ -242,79 +333,34 @@ template <typename T, int ROWS, int G> struct RowTile {
         r.load_shared(in + stage + (x * S + k) * RB + lane * OWN);
         return r;
     }
+    // The same through shared memory in either case; what `stash` puts there for rows loaded into registers.
+    __device__ __forceinline__ char* slot(int lane, int x, int k, int stage) const { return in + stage + (x * S + k) * RB + lane * OWN; }
+    __device__ __forceinline__ void stash(int lane) const
+    {
+        if constexpr (!STAGED) {
+#pragma unroll
+            for (int x = 0; x < G; ++x)
+#pragma unroll
+                for (int k = 0; k < S; ++k) {
+                    if constexpr (OWN == 2) *(unsigned short*)slot(lane, x, k, 0) = (unsigned short)raw[x][k].w[0];
+                    else *(unsigned*)slot(lane, x, k, 0) = raw[x][k].w[0];
+                }
+        }
+    }
+    __device__ __forceinline__ Vals<V> held(int lane, int x, int k, int stage) const
+    {
+        Raw<T, V> r;
+        r.load_shared(slot(lane, x, k, stage));
+        Vals<V> q;
+        q.each([&](int v) { return r.get(v); });
+        return q;
+    }
     // operand x of two units of step k, or of one unit of steps k and k + 1
     __device__ __forceinline__ F2 two(int lane, int x, int k, int stage) const
     {
         const Raw<T, V> r = value(lane, x, k, stage);
         return F2(r.get(0), V == 1 ? value(lane, x, k + 1, stage).get(0) : r.get(V - 1));
     }
-};
-
-// ---------------------------------------------------------------- affine maps of V units
-
-// V values of a lane, in pairs.
-template <int V> struct Vals {
-    F2 q[V / 2];
-    __device__ __forceinline__ float get(int v) const { return v & 1 ? q[v / 2].hi() : q[v / 2].lo(); }
-    __device__ __forceinline__ void fill(float x)
-    {
-#pragma unroll
-        for (int v = 0; v < V / 2; ++v) q[v] = F2(x, x);
-    }
-    __device__ __forceinline__ void mad(const Vals& a, const Vals& b)       // a * this + b
-    {
-#pragma unroll
-        for (int v = 0; v < V / 2; ++v) q[v] = fma2(a.q[v], q[v], b.q[v]);
-    }
-    __device__ __forceinline__ void mul(const Vals& a)
-    {
-#pragma unroll
-        for (int v = 0; v < V / 2; ++v) q[v] = a.q[v] * q[v];
-    }
-    template <typename G> __device__ __forceinline__ void each(G&& value)
-    {
-#pragma unroll
-        for (int v = 0; v < V; v += 2) q[v / 2] = F2(value(v), value(v + 1));
-    }
-};
-template <> struct Vals<1> {
-    float q;
-    __device__ __forceinline__ float get(int) const { return q; }
-    __device__ __forceinline__ void fill(float x) { q = x; }
-    __device__ __forceinline__ void mad(const Vals& a, const Vals& b) { q = fmaf(a.q, q, b.q); }
-    __device__ __forceinline__ void mul(const Vals& a) { q *= a.q; }
-    template <typename G> __device__ __forceinline__ void each(G&& value) { q = value(0); }
-};
-
-// h -> A h + U of a warp's 32 V units, in shared memory.
-template <int V> struct WarpMap {
-    float4 m[V / 2][32];
-    __device__ __forceinline__ void put(int lane, const Vals<V>& A, const Vals<V>& U)
-    {
-#pragma unroll
-        for (int v = 0; v < V / 2; ++v) m[v][lane] = make_float4(A.q[v].lo(), A.q[v].hi(), U.q[v].lo(), U.q[v].hi());
-    }
-    __device__ __forceinline__ void get(int lane, Vals<V>& A, Vals<V>& U) const
-    {
-#pragma unroll
-        for (int v = 0; v < V / 2; ++v) {
-            const float4 x = m[v][lane];
-            A.q[v] = F2(x.x, x.y);
-            U.q[v] = F2(x.z, x.w);
-        }
-    }
-    __device__ __forceinline__ void apply(int lane, Vals<V>& h) const
-    {
-        Vals<V> A, U;
-        get(lane, A, U);
-        h.mad(A, U);
-    }
-};
-template <> struct WarpMap<1> {
-    float2 m[32];
-    __device__ __forceinline__ void put(int lane, const Vals<1>& A, const Vals<1>& U) { m[lane] = make_float2(A.q, U.q); }
-    __device__ __forceinline__ void get(int lane, Vals<1>& A, Vals<1>& U) const { A.q = m[lane].x; U.q = m[lane].y; }
-    __device__ __forceinline__ void apply(int lane, Vals<1>& h) const { h.q = fmaf(m[lane].x, h.q, m[lane].y); }
 };
 
 GlrRows glr_rows(const GlrArgs& a, int elem);

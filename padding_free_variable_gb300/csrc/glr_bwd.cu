@@ -1,0 +1,349 @@
+// glr_bwd.cu -- backward scan of the gated linear recurrence.
+//
+// With G_t = dL/dh_t the total error of a state and e_t = a_t G_t what it passes to the one before,
+//     G_t = dy_t + e_{t+1},   e_t = a_t (dy_t + e_{t+1})
+// is the forward's recurrence run from the end, an affine map e -> A e + W of the same A, and
+//     df = G (h_{t-1} - z) a (1 - a),  dz = G (1 - a)                                  (tied)
+//     df = G h_{t-1} a (1 - a),  dz = G sig(i),  di = G z sig(i) (1 - sig(i))          (gated).
+// The states are not read back (y may be bf16): each 64 steps start from the fp32 state that the
+// forward pass kept and are run again.  A CTA walks 64 steps at a time from the end, its warps
+// holding 8 steps each as in the forward pass; both maps, (A, U) of h within the 64 steps and
+// (A, W) of e, meet in shared memory at one barrier.  Gates and errors stay where they arrived in
+// shared memory for the second pass over a warp's steps, and the gradients leave from there.
+#include "glr.cuh"
+
+namespace lstm {
+
+namespace {
+
+template <typename T, bool GATED, int ROWS> struct BwdTile : RowTile<T, ROWS, GATED ? 4 : 3> {
+    typedef RowTile<T, ROWS, GATED ? 4 : 3> R;
+    static constexpr int W = kGlrWarps;
+    static constexpr int STAGE = W * R::BYTES;
+    static constexpr int MAPS = 2 * 3 * W * (int)sizeof(WarpMap<R::V>);
+    static constexpr int CTAS = 2;
+    static constexpr int FIT = (227 * 1024 / CTAS - 1024 - MAPS) / STAGE;
+    static constexpr int NS = !R::STAGED || FIT < 2 ? 1 : 2;
+    static constexpr int SMEM = NS * STAGE + MAPS;
+};
+
+template <typename T, int ROWS, int G> __device__ __forceinline__ RowTile<T, ROWS, G> error_rows(const GlrArgs& p, const Place& c, int lane)
+{
+    constexpr int64_t e = (int64_t)sizeof(T);
+    RowTile<T, ROWS, G> t;
+    const int64_t from = (c.d * p.dstride + c.u0) * e;
+    t.src[0] = (const char*)p.f + from;
+    t.src[1] = (const char*)p.z + from;
+    if (G == 4) t.src[2] = (const char*)p.i + from;
+#pragma unroll
+    for (int x = 0; x < G - 1; ++x) t.ld[x] = (unsigned)p.ld * (unsigned)e;
+    t.src[G - 1] = (const char*)p.dy + ((int64_t)c.d * p.H + c.u0) * e;
+    t.ld[G - 1] = (unsigned)(p.ndir * p.H) * (unsigned)e;
+    t.place(lane, (p.H - c.u0) * (int)e);
+    return t;
+}
+
+template <typename T, bool GATED, int ROWS>
+__global__ void __launch_bounds__(32 * kGlrWarps, BwdTile<T, GATED, ROWS>::CTAS) glr_bwd_kernel(const GlrArgs p)
+{
+    typedef BwdTile<T, GATED, ROWS> C;
+    constexpr int S = C::S, W = C::W, V = C::V, NS = C::NS, G = GATED ? 4 : 3, DY = G - 1;
+    extern __shared__ __align__(128) char smem[];
+    WarpMap<V>* const s_map = (WarpMap<V>*)(smem + NS * C::STAGE);      // [3][W] of e, then [3][W] of h
+    const int lane = threadIdx.x % 32, w = threadIdx.x / 32;
+    const Place c(p, blockIdx.x, 32 * V);
+    const int u = c.u0 + lane * V, len = c.len;
+    const bool live = u < p.H;
+    const int64_t state = ((int64_t)c.d * p.B + p.perm[c.j]) * p.H + u;
+    auto tile = error_rows<T, ROWS, G>(p, c, lane);
+    tile.in = smem + w * C::BYTES;
+    const unsigned gld = (unsigned)p.gld * (unsigned)sizeof(T);
+    const int64_t to = (c.d * p.gdstride + c.u0) * (int64_t)sizeof(T) + tile.at;
+    char* grad[G - 1];
+    grad[0] = (char*)p.df + to;
+    grad[1] = (char*)p.dz + to;
+    if (GATED) grad[G - 2] = (char*)p.di + to;
+    Vals<V> e;
+    e.each([&](int v) { return live && p.dh_n ? p.dh_n[state + v] : 0.f; });
+    const int begin = p.cut ? c.piece * p.piece : 0, end = p.cut ? min(len, begin + p.piece) : len;
+
+    if (len > 0) {
+        int base = (end - 1) / kScanChunk * kScanChunk;
+        unsigned rows[NS + 2];          // of the iterations from this one on
+#pragma unroll
+        for (int q = 0; q < NS + 2; ++q) rows[q] = c.row_of(p, base + w * S - q * kScanChunk, lane);
+#pragma unroll
+        for (int q = 0; q < NS; ++q) tile.load(lane, rows[q], q * C::STAGE);
+        // the states kept before each 64 steps
+        const float* kept = p.ws + ((int64_t)(p.chunk[c.j] + base / kScanChunk) * p.ndir + c.d) * p.H + (live ? u : 0);
+        Vals<V> start;
+        start.each([&](int v) { return live ? __ldg(kept + v) : 0.f; });
+        WarpMap<V>*now = s_map, *before = s_map + 2 * W;        // maps of e; those of h lie 3 W further
+        Vals<V> A, U;
+        if (end < len) {
+            // the error from beyond this piece: the later pieces' maps, an eighth of them composed by each warp
+            const int last = (len - 1) / p.piece, n = last - c.piece, share = (n + W - 1) / W;
+            identity(A, U);
+#pragma unroll 4
+            for (int k = w * share; k < min(n, (w + 1) * share); ++k) {
+                Vals<V> a, b;
+                c.map<V>(p, last - k)->get(lane, a, b);
+                U.mad(a, b);
+                A.mul(a);
+            }
+            now[w].put(lane, A, U);
+            __syncthreads();
+#pragma unroll
+            for (int x = 0; x < W; ++x) now[x].apply(lane, e);
+        }
+        identity(A, U);
+        before[w].put(lane, A, U);
+        __syncthreads();
+        int stage = 0;
+        for (; base >= begin; base -= kScanChunk) {
+            const int s0 = base + w * S;
+            if (C::STAGED) {
+                cp_async_wait<NS - 1>();
+                __syncwarp();
+            } else {
+                tile.stash(lane);
+                tile.load(lane, rows[1], 0);
+            }
+            if (s0 + S > len) {         // past the end no error enters
+                for (int k = max(0, len - s0); k < S; ++k)
+                    for (int x = 0; x < C::OWN; x += (int)sizeof(T)) *(T*)(tile.slot(lane, DY, k, stage) + x) = from_f32<T>(0.f);
+                __syncwarp();
+            }
+            Vals<V> a[S], n[S], b[S];               // a, 1 - a, b
+#pragma unroll
+            for (int k = 0; k < S; ++k) {
+                const Vals<V> z = tile.held(lane, 1, k, stage);
+                tile.held(lane, 0, k, stage).sigmoids(a[k], n[k]);
+                if (GATED) {
+                    b[k] = tile.held(lane, 2, k, stage);
+                    b[k].sigmoid();
+                } else {
+                    b[k] = n[k];
+                }
+                b[k].mul(z);
+            }
+            if (s0 + S > len) {
+                Vals<V> zero;
+                zero.fill(0.f);
+#pragma unroll
+                for (int k = 0; k < S; ++k)
+                    if (s0 + k >= len) { a[k].fill(1.f); b[k] = zero; }
+            }
+            A = a[0];
+            U = b[0];
+#pragma unroll
+            for (int k = 1; k < S; ++k) {
+                U.mad(a[k], b[k]);
+                A.mul(a[k]);
+            }
+            now[3 * W + w].put(lane, A, U);
+            U = tile.held(lane, DY, S - 1, stage);
+            U.mul(a[S - 1]);
+#pragma unroll
+            for (int k = S - 2; k >= 0; --k) {
+                U.add(tile.held(lane, DY, k, stage));
+                U.mul(a[k]);
+            }
+            now[w].put(lane, A, U);
+            Vals<V> h = start;
+            if (base > begin) {
+                kept -= (int64_t)p.ndir * p.H;
+                start.each([&](int v) { return live ? __ldg(kept + v) : 0.f; });
+            }
+            __syncthreads();
+#pragma unroll
+            for (int x = 1; x < W; ++x) (w - x >= 0 ? before + w - x : now + w - x + W)->apply(lane, e);
+#pragma unroll
+            for (int x = 0; x < W - 1; ++x)
+                if (x < w) now[3 * W + x].apply(lane, h);
+            before = now;
+            now = now == s_map + 2 * W ? s_map : now + W;
+#pragma unroll
+            for (int k = 0; k < S; ++k) {           // b becomes the state before the step
+                const Vals<V> was = h;
+                h.mad(a[k], b[k]);
+                b[k] = was;
+            }
+            const unsigned rows_now = rows[0];
+            const int m = tile.writes ? len - s0 : 0;
+#pragma unroll
+            for (int k = S - 1; k >= 0; --k) {
+                e.add(tile.held(lane, DY, k, stage));       // G
+                const Vals<V> z = tile.held(lane, 1, k, stage);
+                Vals<V> df = e, dz = e, di = e;
+                n[k].mul(e);                                // G (1 - a)
+                if (GATED) {
+                    Vals<V> g, ng;
+                    tile.held(lane, 2, k, stage).sigmoids(g, ng);
+                    df = n[k];
+                    dz.mul(g);
+                    di = dz;
+                    di.mul(ng);
+                    di.mul(z);
+                } else {
+                    dz = n[k];
+                    df = dz;
+                    b[k].sub(z);
+                }
+                df.mul(a[k]);
+                df.mul(b[k]);
+                e.mul(a[k]);
+                if constexpr (C::STAGED) {
+                    store_values<T, V>(tile.slot(lane, 0, k, stage), df);
+                    store_values<T, V>(tile.slot(lane, 1, k, stage), dz);
+                    if (GATED) store_values<T, V>(tile.slot(lane, 2, k, stage), di);
+                } else {
+                    const uint64_t row = (uint64_t)__shfl_sync(0xffffffffu, rows_now, k) * gld;
+                    if (k < m) {
+                        store_values<T, V>(grad[0] + row, df);
+                        store_values<T, V>(grad[1] + row, dz);
+                        if (GATED) store_values<T, V>(grad[G - 2] + row, di);
+                    }
+                }
+            }
+            if constexpr (C::STAGED) {
+                __syncwarp();
+#pragma unroll
+                for (int k = 0; k < S; k += C::RI) {
+                    const int s = k + lane / C::LR;
+                    const uint64_t row = (uint64_t)__shfl_sync(0xffffffffu, rows_now, s) * gld;
+#pragma unroll
+                    for (int x = 0; x < G - 1; ++x) {
+                        const uint4 q = *(const uint4*)(tile.in + stage + (x * S + s) * C::RB + tile.at);
+                        if (s < m) *(uint4*)(grad[x] + row) = q;
+                    }
+                }
+                __syncwarp();
+                tile.load(lane, rows[NS], stage);
+                stage = stage == (NS - 1) * C::STAGE ? 0 : stage + C::STAGE;
+            }
+#pragma unroll
+            for (int q = 0; q < NS + 1; ++q) rows[q] = rows[q + 1];
+            rows[NS + 1] = c.row_of(p, s0 - (NS + 2) * kScanChunk, lane);
+        }
+        if (C::STAGED) cp_async_wait<0>();
+    }
+    if (p.dh0 && live && w == 0 && c.piece == 0)
+#pragma unroll
+        for (int v = 0; v < V; ++v) p.dh0[state + v] = e.get(v);
+    if (p.padded && tile.writes && c.piece == 0)        // the padded comparator's rows past the end
+        for (int t = len + w; t < p.T; t += W)
+#pragma unroll
+            for (int x = 0; x < G - 1; ++x)
+                for (int y = 0; y < C::WIDTH; y += (int)sizeof(T))
+                    *(T*)(grad[x] + (uint64_t)(p.off[t] + c.j) * gld + y) = from_f32<T>(0.f);
+}
+
+// A piece's map of e, from f and dy alone: every piece but a sequence's first.
+template <typename T, int ROWS> struct BwdMapTile : RowTile<T, ROWS, 2> {
+    typedef RowTile<T, ROWS, 2> R;
+    static constexpr int W = kGlrWarps;
+    static constexpr int STAGE = R::STAGED ? W * R::BYTES : 0;
+    static constexpr int NS = !R::STAGED || 2 * STAGE > 72 * 1024 ? 1 : 2;
+    static constexpr int SMEM = NS * STAGE;
+};
+
+template <typename T, int ROWS>
+__global__ void __launch_bounds__(32 * kGlrWarps, 3) glr_bwd_map_kernel(const GlrArgs p)
+{
+    typedef BwdMapTile<T, ROWS> C;
+    constexpr int S = C::S, W = C::W, V = C::V, NS = C::NS;
+    extern __shared__ __align__(128) char smem[];
+    __shared__ WarpMap<V> s_map[W];
+    const int lane = threadIdx.x % 32, w = threadIdx.x / 32;
+    const Place c(p, blockIdx.x, 32 * V);
+    if (c.piece == 0) return;
+    RowTile<T, ROWS, 2> tile;
+    constexpr int64_t el = (int64_t)sizeof(T);
+    tile.src[0] = (const char*)p.f + (c.d * p.dstride + c.u0) * el;
+    tile.ld[0] = (unsigned)p.ld * (unsigned)el;
+    tile.src[1] = (const char*)p.dy + ((int64_t)c.d * p.H + c.u0) * el;
+    tile.ld[1] = (unsigned)(p.ndir * p.H) * (unsigned)el;
+    tile.place(lane, (p.H - c.u0) * (int)el);
+    tile.in = smem + w * C::BYTES;
+    const int first = c.piece * p.piece + w * (p.piece / W);
+    int s0 = first + p.piece / W - S;
+    unsigned rows[NS + 1];
+#pragma unroll
+    for (int q = 0; q < NS + 1; ++q) rows[q] = c.row_of(p, s0 - q * S, lane);
+#pragma unroll
+    for (int q = 0; q < NS; ++q) tile.load(lane, rows[q], q * C::STAGE);
+    Vals<V> A, U;
+    identity(A, U);
+    int stage = 0;
+    for (; s0 >= first; s0 -= S) {
+        if (C::STAGED) {
+            cp_async_wait<NS - 1>();
+            __syncwarp();
+        }
+        Vals<V> a[S], d[S];
+#pragma unroll
+        for (int k = 0; k < S; ++k) {
+            const Raw<T, V> rf = tile.value(lane, 0, k, stage), rd = tile.value(lane, 1, k, stage);
+            a[k].each([&](int v) { return rf.get(v); });
+            a[k].sigmoid();
+            d[k].each([&](int v) { return rd.get(v); });
+        }
+        if (C::STAGED) __syncwarp();
+        tile.load(lane, rows[NS], stage);
+        rows[NS] = c.row_of(p, s0 - (NS + 1) * S, lane);
+        stage = stage == (NS - 1) * C::STAGE ? 0 : stage + C::STAGE;
+#pragma unroll
+        for (int k = S - 1; k >= 0; --k) {
+            if (s0 + k >= c.len) continue;
+            U.add(d[k]);
+            U.mul(a[k]);
+            A.mul(a[k]);
+        }
+    }
+    if (C::STAGED) cp_async_wait<0>();
+    s_map[w].put(lane, A, U);
+    __syncthreads();
+    if (w < W - 1) return;
+    for (int x = W - 2; x >= 0; --x) {
+        Vals<V> a, b;
+        s_map[x].get(lane, a, b);
+        U.mad(a, b);
+        A.mul(a);
+    }
+    c.map<V>(p, c.piece)->put(lane, A, U);
+}
+
+template <typename T, bool GATED, int ROWS>
+lstm_status go(const Plan& p, GlrArgs a, void* scratch, cudaStream_t cs)
+{
+    static std::atomic<uint64_t> ready{0}, ready_map{0};
+    typedef BwdTile<T, GATED, ROWS> C;
+    glr_cut(p, C::V, C::CTAS, scratch, &a);
+    if (a.cut) {
+        const lstm_status st = glr_launch(p, glr_bwd_map_kernel<T, ROWS>, a, C::V, BwdMapTile<T, ROWS>::SMEM, ready_map, cs);
+        if (st != LSTM_OK) return st;
+    }
+    return glr_launch(p, glr_bwd_kernel<T, GATED, ROWS>, a, C::V, C::SMEM, ready, cs);
+}
+
+template <typename T, bool GATED>
+lstm_status go(const Plan& p, const GlrArgs& a, void* scratch, cudaStream_t cs)
+{
+    const GlrRows rows = glr_rows(a, (int)sizeof(T));
+    if (rows == GLR_WIDE) return go<T, GATED, GLR_WIDE>(p, a, scratch, cs);
+    if constexpr (sizeof(T) == 2)
+        if (rows == GLR_SINGLE) return go<T, GATED, GLR_SINGLE>(p, a, scratch, cs);
+    return go<T, GATED, GLR_NARROW>(p, a, scratch, cs);
+}
+
+}  // namespace
+
+lstm_status launch_glr_bwd(const Plan& p, const lstm_glr_shape& s, GlrArgs a, void* scratch, cudaStream_t cs)
+{
+    const bool gated = s.cell == LSTM_GLR_GATED;
+    if (s.dtype == LSTM_BF16) return gated ? go<__nv_bfloat16, true>(p, a, scratch, cs) : go<__nv_bfloat16, false>(p, a, scratch, cs);
+    return gated ? go<float, true>(p, a, scratch, cs) : go<float, false>(p, a, scratch, cs);
+}
+
+}  // namespace lstm
