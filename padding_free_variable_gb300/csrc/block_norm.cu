@@ -1,197 +1,11 @@
-// block_norm.cu -- the norms before and after a block with its gate and residual scale: entry points and kernels.
+// block_norm.cu -- the norms before and after a block with its gate and residual scale: entry points.
 #include <algorithm>
 
-#include "glr.cuh"
+#include "block_norm.cuh"
 
 namespace lstm {
 
 namespace {
-
-constexpr int kSums = 5;            // w_post, b_post, scale, w_pre, b_pre
-constexpr int kMaxParts = 304;      // row ranges of the backward pass's column sums
-
-struct NormArgs {
-    int D = 0;
-    int post = 0, pre = 0, gate = 0;
-    bool branch16 = false, stream16 = false, norm16 = false;
-    float eps = 0.f;
-    int64_t rows = 0;
-    lstm_block_norm_params w = {};
-    const void* x = nullptr;
-    const void* y = nullptr;
-    const void* g = nullptr;
-    int64_t ldy = 0, ldg = 0;
-    void* x_out = nullptr;
-    void* n = nullptr;
-    float* stats = nullptr;         // [rows][4]: mean and 1/deviation, post then pre
-    // backward
-    const void* dx_out = nullptr;
-    const void* dn = nullptr;
-    void* dx = nullptr;
-    void* dy = nullptr;
-    void* dg = nullptr;
-    int64_t lddy = 0, lddg = 0;
-    float* part = nullptr;          // [parts][kSums][D]
-    float* sums[kSums] = {};
-    int parts = 0;
-};
-
-__device__ __forceinline__ float load1(const void* p, int64_t i, bool b16)
-{
-    return b16 ? __bfloat162float(((const __nv_bfloat16*)p)[i]) : ((const float*)p)[i];
-}
-
-__device__ __forceinline__ void store1(void* p, int64_t i, bool b16, float v)
-{
-    if (b16) ((__nv_bfloat16*)p)[i] = __float2bfloat16_rn(v);
-    else ((float*)p)[i] = v;
-}
-
-__device__ float block_sum(float v)
-{
-    __shared__ float part[32];
-    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    __syncthreads();
-    if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = v;
-    __syncthreads();
-    float s = 0.f;
-    for (int w = 0; w < (int)blockDim.x / 32; ++w) s += part[w];
-    return s;
-}
-
-// act(g) and act'(g)
-__device__ __forceinline__ void activation(int kind, float q, float& act, float& slope)
-{
-    if (kind == LSTM_GATE_NONE) { act = 1.f; slope = 0.f; return; }
-    float s, c;
-    sigmoid_pair(q, s, c);
-    if (kind == LSTM_GATE_SIGMOID) { act = s; slope = s * c; }
-    else { act = q * s; slope = s * (1.f + q * c); }
-}
-
-__device__ __forceinline__ float x_out_of(const NormArgs& p, int64_t r, int c, float mean, float rstd)
-{
-    float x = load1(p.x, r * p.D + c, p.stream16);
-    if (!p.y) return x;
-    const float hat = (load1(p.y, r * p.ldy + c, p.branch16) - mean) * rstd;
-    const float v = hat * (p.w.w_post ? p.w.w_post[c] : 1.f) + (p.w.b_post ? p.w.b_post[c] : 0.f);
-    float act = 1.f, slope;
-    if (p.gate) activation(p.gate, load1(p.g, r * p.ldg + c, p.branch16), act, slope);
-    return x + (p.w.scale ? p.w.scale[c] : 1.f) * v * act;
-}
-
-__global__ void block_norm_fwd_kernel(const NormArgs p)
-{
-    const int64_t r = blockIdx.x;
-    float my = 0.f, ry = 1.f, mx = 0.f, rx = 1.f;
-    if (p.post) {
-        float s = 0.f;
-        if (p.post == LSTM_NORM_LAYER) {
-            for (int c = threadIdx.x; c < p.D; c += blockDim.x) s += load1(p.y, r * p.ldy + c, p.branch16);
-            my = block_sum(s) / p.D;
-        }
-        s = 0.f;
-        for (int c = threadIdx.x; c < p.D; c += blockDim.x) {
-            const float v = load1(p.y, r * p.ldy + c, p.branch16) - my;
-            s += v * v;
-        }
-        ry = 1.f / sqrtf(block_sum(s) / p.D + p.eps);
-    }
-    if (p.pre) {
-        float s = 0.f;
-        if (p.pre == LSTM_NORM_LAYER) {
-            for (int c = threadIdx.x; c < p.D; c += blockDim.x) s += x_out_of(p, r, c, my, ry);
-            mx = block_sum(s) / p.D;
-        }
-        s = 0.f;
-        for (int c = threadIdx.x; c < p.D; c += blockDim.x) {
-            const float v = x_out_of(p, r, c, my, ry) - mx;
-            s += v * v;
-        }
-        rx = 1.f / sqrtf(block_sum(s) / p.D + p.eps);
-    }
-    for (int c = threadIdx.x; c < p.D; c += blockDim.x) {
-        const float x1 = x_out_of(p, r, c, my, ry);
-        if (p.n)
-            store1(p.n, r * p.D + c, p.norm16,
-                   (x1 - mx) * rx * (p.w.w_pre ? p.w.w_pre[c] : 1.f) + (p.w.b_pre ? p.w.b_pre[c] : 0.f));
-        if (p.x_out) store1(p.x_out, r * p.D + c, p.stream16, x1);
-    }
-    if (p.stats && threadIdx.x == 0) {
-        float* t = p.stats + r * 4;
-        t[0] = my; t[1] = ry; t[2] = mx; t[3] = rx;
-    }
-}
-
-__global__ void block_norm_bwd_kernel(const NormArgs p)
-{
-    float* part = p.part + (int64_t)blockIdx.x * kSums * p.D;
-    for (int c = threadIdx.x; c < kSums * p.D; c += blockDim.x) part[c] = 0.f;
-    __syncthreads();
-    for (int64_t r = blockIdx.x; r < p.rows; r += gridDim.x) {
-        const float my = p.stats[r * 4], ry = p.stats[r * 4 + 1], mx = p.stats[r * 4 + 2], rx = p.stats[r * 4 + 3];
-        // dx' = dx_out + rx (t - mean t - xh mean(t xh)), t = dn w_pre
-        float s0 = 0.f, s1 = 0.f;
-        if (p.dn)
-            for (int c = threadIdx.x; c < p.D; c += blockDim.x) {
-                const float t = load1(p.dn, r * p.D + c, p.norm16) * (p.w.w_pre ? p.w.w_pre[c] : 1.f);
-                s0 += t;
-                s1 += t * (x_out_of(p, r, c, my, ry) - mx) * rx;
-            }
-        const float m0 = p.pre == LSTM_NORM_LAYER ? block_sum(s0) / p.D : 0.f, m1 = block_sum(s1) / p.D;
-        auto dx_of = [&](int c) {
-            float dx = p.dx_out ? load1(p.dx_out, r * p.D + c, p.stream16) : 0.f;
-            if (p.dn) {
-                const float t = load1(p.dn, r * p.D + c, p.norm16) * (p.w.w_pre ? p.w.w_pre[c] : 1.f);
-                dx += rx * (t - m0 - (x_out_of(p, r, c, my, ry) - mx) * rx * m1);
-            }
-            return dx;
-        };
-        auto sc = [&](int c) { return p.w.scale ? p.w.scale[c] : 1.f; };
-        auto wp = [&](int c) { return p.w.w_post ? p.w.w_post[c] : 1.f; };
-        float q0 = 0.f, q1 = 0.f;
-        if (p.y && p.post)
-            for (int c = threadIdx.x; c < p.D; c += blockDim.x) {
-                float act = 1.f, slope;
-                if (p.gate) activation(p.gate, load1(p.g, r * p.ldg + c, p.branch16), act, slope);
-                const float t = dx_of(c) * sc(c) * act * wp(c);
-                q0 += t;
-                q1 += t * (load1(p.y, r * p.ldy + c, p.branch16) - my) * ry;
-            }
-        const float k0 = p.post == LSTM_NORM_LAYER ? block_sum(q0) / p.D : 0.f, k1 = block_sum(q1) / p.D;
-        for (int c = threadIdx.x; c < p.D; c += blockDim.x) {
-            const float dx = dx_of(c);
-            if (p.dn) {
-                const float dn = load1(p.dn, r * p.D + c, p.norm16);
-                part[3 * p.D + c] += dn * (x_out_of(p, r, c, my, ry) - mx) * rx;
-                part[4 * p.D + c] += dn;
-            }
-            if (p.y) {
-                const float hat = (load1(p.y, r * p.ldy + c, p.branch16) - my) * ry;
-                const float v = hat * wp(c) + (p.w.b_post ? p.w.b_post[c] : 0.f);
-                float act = 1.f, slope = 0.f;
-                if (p.gate) activation(p.gate, load1(p.g, r * p.ldg + c, p.branch16), act, slope);
-                const float du = dx * sc(c), dv = du * act, t = dv * wp(c);
-                part[c] += dv * hat;
-                part[p.D + c] += dv;
-                part[2 * p.D + c] += dx * v * act;
-                store1(p.dy, r * p.lddy + c, p.branch16, p.post ? ry * (t - k0 - hat * k1) : t);
-                if (p.gate) store1(p.dg, r * p.lddg + c, p.branch16, du * v * slope);
-            }
-            store1(p.dx, r * p.D + c, p.stream16, dx);
-        }
-        __syncthreads();
-    }
-}
-
-__global__ void block_norm_sums_kernel(const NormArgs p)
-{
-    const int c = blockIdx.x * blockDim.x + threadIdx.x, k = blockIdx.y;
-    if (c >= p.D || !p.sums[k]) return;
-    float s = 0.f;
-    for (int b = 0; b < p.parts; ++b) s += p.part[((int64_t)b * kSums + k) * p.D + c];
-    p.sums[k][c] = s;
-}
 
 bool aligned(const void* p, size_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 
@@ -242,11 +56,17 @@ lstm_status norm_args(const lstm_block_norm_shape* shape, const lstm_block_norm_
     return LSTM_OK;
 }
 
-int norm_parts(int64_t rows) { return (int)std::min<int64_t>(rows, kMaxParts); }
-
-lstm_status launched() { return cudaGetLastError() == cudaSuccess ? LSTM_OK : LSTM_ERR_CUDA; }
-
 }  // namespace
+
+bool norm_whole(const NormArgs& a)
+{
+    bool ok = a.D % 8 == 0 && a.ldy % 8 == 0 && a.ldg % 8 == 0 && a.lddy % 8 == 0 && a.lddg % 8 == 0;
+    for (const void* p : {a.x, a.y, a.g, (const void*)a.x_out, (const void*)a.n, a.dx_out, a.dn, (const void*)a.dx,
+                          (const void*)a.dy, (const void*)a.dg, (const void*)a.w.w_post, (const void*)a.w.b_post,
+                          (const void*)a.w.scale, (const void*)a.w.w_pre, (const void*)a.w.b_pre})
+        ok = ok && aligned(p, 16);
+    return ok;
+}
 
 }  // namespace lstm
 
@@ -267,14 +87,13 @@ lstm_status lstm_block_norm_fwd(const lstm_block_norm_shape* shape, const lstm_b
     if (!aligned(x_out, elem(shape->stream_dtype)) || !aligned(n, elem(shape->norm_dtype)) || !aligned(stats, 16))
         return LSTM_ERR_INVALID_ARG;
     a.x_out = x_out; a.n = n; a.stats = stats;
-    block_norm_fwd_kernel<<<(unsigned)rows, 256, 0, (cudaStream_t)stream>>>(a);
-    return launched();
+    return launch_norm_fwd(a, (cudaStream_t)stream);
 }
 
 size_t lstm_block_norm_scratch_bytes(const lstm_block_norm_shape* shape, int64_t rows)
 {
     if (check_norm_shape(shape) != LSTM_OK || rows < 0 || rows > INT32_MAX) return 0;
-    return std::max<size_t>(16, (size_t)norm_parts(rows) * kSums * shape->width * sizeof(float));
+    return std::max<size_t>(16, (size_t)norm_parts(rows, shape->width) * kSums * shape->width * sizeof(float));
 }
 
 lstm_status lstm_block_norm_bwd(const lstm_block_norm_shape* shape, const lstm_block_norm_params* params,
@@ -306,11 +125,9 @@ lstm_status lstm_block_norm_bwd(const lstm_block_norm_shape* shape, const lstm_b
     a.stats = const_cast<float*>(stats);
     a.dx_out = dx_out; a.dn = dn; a.dx = din->dx; a.dy = din->dy; a.dg = din->dgate;
     a.lddy = din->dy_stride; a.lddg = din->dgate_stride;
-    a.part = (float*)scratch; a.parts = norm_parts(rows);
+    a.part = (float*)scratch; a.parts = norm_parts(rows, shape->width);
     for (int k = 0; k < kSums; ++k) a.sums[k] = sums[k];
-    block_norm_bwd_kernel<<<a.parts, 256, 0, cs>>>(a);
-    block_norm_sums_kernel<<<dim3(ceil_div(a.D, 128), kSums), 128, 0, cs>>>(a);
-    return launched();
+    return launch_norm_bwd(a, cs);
 }
 
 }  // extern "C"

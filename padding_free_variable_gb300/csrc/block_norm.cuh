@@ -1,0 +1,221 @@
+// block_norm.cuh -- arguments of the block norms' kernels and the row access they share.
+#pragma once
+
+#include <type_traits>
+
+#include "glr.cuh"
+
+namespace lstm {
+
+constexpr int kSums = 5;            // w_post, b_post, scale, w_pre, b_pre
+
+struct NormArgs {
+    int D = 0;
+    int post = 0, pre = 0, gate = 0;
+    bool branch16 = false, stream16 = false, norm16 = false;
+    float eps = 0.f;
+    int64_t rows = 0;
+    lstm_block_norm_params w = {};
+    const void* x = nullptr;
+    const void* y = nullptr;
+    const void* g = nullptr;
+    int64_t ldy = 0, ldg = 0;
+    void* x_out = nullptr;
+    void* n = nullptr;
+    float* stats = nullptr;         // [rows][4]: mean and 1/deviation, post then pre
+    // backward
+    const void* dx_out = nullptr;
+    const void* dn = nullptr;
+    void* dx = nullptr;
+    void* dy = nullptr;
+    void* dg = nullptr;
+    int64_t lddy = 0, lddg = 0;
+    float* part = nullptr;          // [parts][kSums][D]
+    float* sums[kSums] = {};
+    int parts = 0;
+};
+
+
+// Values of a thread: PER groups of VEC neighbours, the threads of a row next to each other in each group.
+template <int VEC, int PER> struct Cols {
+    int t, n, D;            // thread of the row, threads of a row, width
+    __device__ __forceinline__ int at(int k) const { return (k * n + t) * VEC; }
+    __device__ __forceinline__ bool has(int k) const { return at(k) < D; }
+};
+
+// VEC values of one group as they lie in memory.
+template <typename T, int VEC> struct Group {
+    static constexpr int N = VEC * (int)sizeof(T) / 16 > 0 ? VEC * (int)sizeof(T) / 16 : 1;
+    uint4 w[VEC == 1 ? 1 : N];
+    __device__ __forceinline__ void load(const T* p)
+    {
+        if constexpr (VEC == 1) {
+            if constexpr (sizeof(T) == 2) w[0].x = __ldg((const unsigned short*)p);
+            else w[0].x = __ldg((const unsigned*)p);
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i) w[i] = __ldg((const uint4*)p + i);
+        }
+    }
+    // x and dx' may be overwritten in place by the thread that reads them: no read-only path
+    __device__ __forceinline__ void load_own(const T* p)
+    {
+        if constexpr (VEC == 1) {
+            if constexpr (sizeof(T) == 2) w[0].x = *(const unsigned short*)p;
+            else w[0].x = *(const unsigned*)p;
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i) w[i] = ((const uint4*)p)[i];
+        }
+    }
+    __device__ __forceinline__ void zero()
+    {
+#pragma unroll
+        for (int i = 0; i < (VEC == 1 ? 1 : N); ++i) w[i] = make_uint4(0, 0, 0, 0);
+    }
+    __device__ __forceinline__ unsigned word(int i) const
+    {
+        const uint4 q = w[i / 4];
+        return i % 4 == 0 ? q.x : i % 4 == 1 ? q.y : i % 4 == 2 ? q.z : q.w;
+    }
+    __device__ __forceinline__ float get(int v) const
+    {
+        if constexpr (sizeof(T) == 4) return __uint_as_float(word(v));
+        else return __uint_as_float(v % 2 ? word(v / 2) & 0xffff0000u : word(v / 2) << 16);
+    }
+};
+
+// The same with the type known at run time, for the kernels that are not worth a copy for each type.
+struct Any {};
+template <int VEC> struct Group<Any, VEC> {
+    static constexpr int N = VEC == 1 ? 1 : VEC / 4;
+    uint4 w[N];
+    __device__ __forceinline__ void load_any(const void* base, int64_t at, bool b16, bool own)
+    {
+        if constexpr (VEC == 1) {
+            if (b16) w[0].x = own ? ((const unsigned short*)base)[at] : __ldg((const unsigned short*)base + at);
+            else w[0].x = own ? ((const unsigned*)base)[at] : __ldg((const unsigned*)base + at);
+        } else {
+            const uint4* p = (const uint4*)((const char*)base + at * (b16 ? 2 : 4));
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                if (i < (b16 ? N / 2 : N)) w[i] = own ? p[i] : __ldg(p + i);
+        }
+    }
+    __device__ __forceinline__ void zero()
+    {
+#pragma unroll
+        for (int i = 0; i < N; ++i) w[i] = make_uint4(0, 0, 0, 0);
+    }
+    __device__ __forceinline__ unsigned word(int i) const
+    {
+        const uint4 q = w[i / 4];
+        return i % 4 == 0 ? q.x : i % 4 == 1 ? q.y : i % 4 == 2 ? q.z : q.w;
+    }
+    __device__ __forceinline__ float get(int v, bool b16) const
+    {
+        return __uint_as_float(!b16 ? word(v) : v % 2 ? word(v / 2) & 0xffff0000u : word(v / 2) << 16);
+    }
+};
+
+template <typename T, int VEC>
+__device__ __forceinline__ void load_group(Group<T, VEC>& g, const void* base, int64_t at, bool b16, bool own = false)
+{
+    if constexpr (std::is_same<T, Any>::value) g.load_any(base, at, b16, own);
+    else if (own) g.load_own((const T*)base + at);
+    else g.load((const T*)base + at);
+}
+template <typename T, int VEC> __device__ __forceinline__ float get_value(const Group<T, VEC>& g, int v, bool b16)
+{
+    if constexpr (std::is_same<T, Any>::value) return g.get(v, b16);
+    else return g.get(v);
+}
+
+// Store VEC values as bf16 or fp32.
+template <int VEC> __device__ __forceinline__ void put_group(void* base, int64_t at, bool b16, const float (&v)[VEC])
+{
+    if constexpr (VEC == 1) {
+        if (b16) ((__nv_bfloat16*)base)[at] = __float2bfloat16_rn(v[0]);
+        else ((float*)base)[at] = v[0];
+    } else if (b16) {
+        unsigned q[VEC / 2];
+#pragma unroll
+        for (int i = 0; i < VEC; i += 2) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(v[i], v[i + 1]);
+            q[i / 2] = *(const unsigned*)&h;
+        }
+        if constexpr (VEC == 8) *(uint4*)((__nv_bfloat16*)base + at) = make_uint4(q[0], q[1], q[2], q[3]);
+        else *(uint2*)((__nv_bfloat16*)base + at) = make_uint2(q[0], q[1]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < VEC; i += 4) *(float4*)((float*)base + at + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+    }
+}
+
+// VEC parameters, or `none` where there are no such parameters.
+template <int VEC> __device__ __forceinline__ void get_params(const float* p, int at, float none, float (&v)[VEC])
+{
+    if (!p) {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) v[i] = none;
+    } else if constexpr (VEC == 1) {
+        v[0] = __ldg(p + at);
+    } else {
+#pragma unroll
+        for (int i = 0; i < VEC; i += 4) {
+            const float4 q = __ldg((const float4*)(p + at + i));
+            v[i] = q.x; v[i + 1] = q.y; v[i + 2] = q.z; v[i + 3] = q.w;
+        }
+    }
+}
+
+// Sums over the threads of a row: within a warp by shuffles, across the warps of a CTA (then one
+// row a CTA) through shared memory, each use on the other half so that one barrier suffices.
+struct RowSum {
+    float2* part;           // [2][32]
+    int warps, half;
+    __device__ __forceinline__ float2 operator()(float a, float b)
+    {
+#pragma unroll
+        for (int o = 16; o; o >>= 1) {
+            a += __shfl_xor_sync(0xffffffffu, a, o);
+            b += __shfl_xor_sync(0xffffffffu, b, o);
+        }
+        if (warps == 1) return make_float2(a, b);
+        float2* s = part + half * 32;
+        half ^= 1;
+        if (threadIdx.x % 32 == 0) s[threadIdx.x / 32] = make_float2(a, b);
+        __syncthreads();
+        const float2 q = threadIdx.x % 32 < warps ? s[threadIdx.x % 32] : make_float2(0.f, 0.f);
+        a = q.x;
+        b = q.y;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) {
+            a += __shfl_xor_sync(0xffffffffu, a, o);
+            b += __shfl_xor_sync(0xffffffffu, b, o);
+        }
+        return make_float2(a, b);
+    }
+};
+
+// act(q) and act'(q)
+__device__ __forceinline__ void activation(int kind, float q, float& act, float& slope)
+{
+    float s, c;
+    sigmoid_pair(q, s, c);
+    act = kind == LSTM_GATE_SIGMOID ? s : q * s;
+    slope = kind == LSTM_GATE_SIGMOID ? s * c : s * fmaf(q, c, 1.f);
+}
+__device__ __forceinline__ float activation(int kind, float q)
+{
+    const float s = rcp_approx(1.f + ex2_approx(q * kNegLog2e));
+    return kind == LSTM_GATE_SIGMOID ? s : kind == LSTM_GATE_SILU ? q * s : 1.f;
+}
+
+// Rows, pointers and widths allow groups of eight.
+bool norm_whole(const NormArgs& a);
+int norm_parts(int64_t rows, int D);
+lstm_status launch_norm_fwd(const NormArgs& a, cudaStream_t cs);
+lstm_status launch_norm_bwd(const NormArgs& a, cudaStream_t cs);
+
+}  // namespace lstm

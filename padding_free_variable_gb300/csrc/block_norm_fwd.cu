@@ -1,0 +1,140 @@
+// block_norm_fwd.cu -- forward pass of the norms around a block.
+//
+// x' = x + scale * (norm(y) w + b) * act(gate), n = norm(x') w + b, row by row.  A row's values
+// stay in its threads' registers from the one read of x, y and gate to the one write of x' and n;
+// its variances are taken around its mean in a second sweep over registers, so a mean far above
+// the deviation costs no digits.  Bound by memory: 5 values of traffic against about 20 operations.
+// A warp takes a row of up to 1024 values (no barrier; many rows an SM hide the latency), wider
+// rows take a CTA; a call of few rows spreads each over as many threads as it has groups of
+// eight, since there only the time of one row counts.
+#include "block_norm.cuh"
+
+namespace lstm {
+
+namespace {
+
+template <typename TB, typename TS, int VEC, int PER>
+__global__ void __launch_bounds__(512) norm_fwd_kernel(const NormArgs p, const int tpr)
+{
+    __shared__ float2 s_part[2 * 32];
+    const int64_t r = tpr == 32 ? blockIdx.x * (int64_t)(blockDim.x / 32) + threadIdx.x / 32 : blockIdx.x;
+    if (r >= p.rows) return;
+    const Cols<VEC, PER> c{(int)threadIdx.x % tpr, tpr, p.D};
+    RowSum sum{s_part, tpr / 32, 0};
+    const float inv = 1.f / (float)p.D;
+
+    Group<TS, VEC> rx[PER];
+    Group<TB, VEC> ry[PER], rg[PER];
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+        rx[k].zero();
+        ry[k].zero();
+        rg[k].zero();
+        if (!c.has(k)) continue;
+        rx[k].load_own((const TS*)p.x + r * p.D + c.at(k));
+        if (p.y) ry[k].load((const TB*)p.y + r * p.ldy + c.at(k));
+        if (p.g) rg[k].load((const TB*)p.g + r * p.ldg + c.at(k));
+    }
+    float my = 0.f, sy = 1.f, mx = 0.f, sx = 1.f;
+    if (p.post) {
+        float a = 0.f;
+        if (p.post == LSTM_NORM_LAYER) {
+#pragma unroll
+            for (int k = 0; k < PER; ++k)
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) a += ry[k].get(v);
+            my = sum(a, 0.f).x * inv;
+            a = 0.f;
+        }
+#pragma unroll
+        for (int k = 0; k < PER; ++k)
+            if (c.has(k))
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) {
+                    const float d = ry[k].get(v) - my;
+                    a = fmaf(d, d, a);
+                }
+        sy = 1.f / sqrtf(fmaf(sum(a, 0.f).x, inv, p.eps));
+    }
+    float x1[PER][VEC];
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) x1[k][v] = rx[k].get(v);
+        if (!p.y || !c.has(k)) continue;
+        float w[VEC], b[VEC], s[VEC];
+        get_params<VEC>(p.w.w_post, c.at(k), 1.f, w);
+        get_params<VEC>(p.w.b_post, c.at(k), 0.f, b);
+        get_params<VEC>(p.w.scale, c.at(k), 1.f, s);
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) {
+            const float u = fmaf((ry[k].get(v) - my) * sy, w[v], b[v]);
+            x1[k][v] = fmaf(s[v] * u, activation(p.gate, rg[k].get(v)), x1[k][v]);
+        }
+        put_group<VEC>(p.x_out, r * p.D + c.at(k), sizeof(TS) == 2, x1[k]);
+    }
+    if (p.pre) {
+        float a = 0.f;
+        if (p.pre == LSTM_NORM_LAYER) {
+#pragma unroll
+            for (int k = 0; k < PER; ++k)
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) a += x1[k][v];
+            mx = sum(a, 0.f).x * inv;
+            a = 0.f;
+        }
+#pragma unroll
+        for (int k = 0; k < PER; ++k)
+            if (c.has(k))
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) {
+                    const float d = x1[k][v] - mx;
+                    a = fmaf(d, d, a);
+                }
+        sx = 1.f / sqrtf(fmaf(sum(a, 0.f).x, inv, p.eps));
+#pragma unroll
+        for (int k = 0; k < PER; ++k) {
+            if (!c.has(k)) continue;
+            float w[VEC], b[VEC];
+            get_params<VEC>(p.w.w_pre, c.at(k), 1.f, w);
+            get_params<VEC>(p.w.b_pre, c.at(k), 0.f, b);
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) w[v] = fmaf((x1[k][v] - mx) * sx, w[v], b[v]);
+            put_group<VEC>(p.n, r * p.D + c.at(k), p.norm16, w);
+        }
+    }
+    if (p.stats && c.t == 0) *(float4*)(p.stats + r * 4) = make_float4(my, sy, mx, sx);
+}
+
+template <typename TB, typename TS, int VEC, int PER> lstm_status run(const NormArgs& a, int tpr, cudaStream_t cs)
+{
+    const int threads = tpr == 32 ? 128 : tpr;
+    const int64_t blocks = tpr == 32 ? (a.rows + 3) / 4 : a.rows;
+    norm_fwd_kernel<TB, TS, VEC, PER><<<(unsigned)blocks, threads, 0, cs>>>(a, tpr);
+    return cudaGetLastError() == cudaSuccess ? LSTM_OK : LSTM_ERR_CUDA;
+}
+
+template <typename TB, typename TS> lstm_status go(const NormArgs& a, cudaStream_t cs)
+{
+    // values of a thread: 32 where rows are many, 8 where a call's few rows leave SMs idle
+    auto threads = [&](int each) { return (ceil_div(a.D, each) + 31) / 32 * 32; };
+    if (norm_whole(a)) {
+        const bool few = a.rows <= 304;
+        if (few && threads(8) <= 512) return run<TB, TS, 8, 1>(a, threads(8), cs);
+        if (a.D <= 256) return run<TB, TS, 8, 1>(a, 32, cs);
+        if (a.D <= 512 || (few && threads(16) <= 512)) return run<TB, TS, 8, 2>(a, threads(16), cs);
+        return run<TB, TS, 8, 4>(a, threads(32), cs);
+    }
+    if (threads(8) <= 32 || (a.rows <= 304 && threads(8) <= 512)) return run<TB, TS, 1, 8>(a, threads(8), cs);
+    return run<TB, TS, 1, 32>(a, threads(32), cs);
+}
+
+}  // namespace
+
+lstm_status launch_norm_fwd(const NormArgs& a, cudaStream_t cs)
+{
+    if (a.branch16) return a.stream16 ? go<__nv_bfloat16, __nv_bfloat16>(a, cs) : go<__nv_bfloat16, float>(a, cs);
+    return a.stream16 ? go<float, __nv_bfloat16>(a, cs) : go<float, float>(a, cs);
+}
+
+}  // namespace lstm
