@@ -58,6 +58,13 @@ lstm_status norm_args(const lstm_block_norm_shape* shape, const lstm_block_norm_
 
 }  // namespace
 
+bool norm_full(const NormArgs& a)
+{
+    const bool layer = a.post == LSTM_NORM_LAYER;
+    return a.y && a.post && a.post == a.pre && a.w.w_post && a.w.scale && a.w.w_pre && layer == (a.w.b_post != nullptr) &&
+           layer == (a.w.b_pre != nullptr) && a.norm16 == a.branch16 && (a.branch16 || !a.stream16);
+}
+
 bool norm_whole(const NormArgs& a)
 {
     bool ok = a.D % 8 == 0 && a.ldy % 8 == 0 && a.ldg % 8 == 0 && a.lddy % 8 == 0 && a.lddg % 8 == 0;

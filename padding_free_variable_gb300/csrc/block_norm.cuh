@@ -153,9 +153,11 @@ template <int VEC> __device__ __forceinline__ void put_group(void* base, int64_t
 }
 
 // VEC parameters, or `none` where there are no such parameters.
-template <int VEC> __device__ __forceinline__ void get_params(const float* p, int at, float none, float (&v)[VEC])
+// GIVEN: known to be there; EVER: such a kind has them at all.
+template <int VEC, bool GIVEN = false, bool EVER = true>
+__device__ __forceinline__ void get_params(const float* p, int at, float none, float (&v)[VEC])
 {
-    if (!p) {
+    if (!EVER || (!GIVEN && !p)) {
 #pragma unroll
         for (int i = 0; i < VEC; ++i) v[i] = none;
     } else if constexpr (VEC == 1) {
@@ -212,6 +214,8 @@ __device__ __forceinline__ float activation(int kind, float q)
     return kind == LSTM_GATE_SIGMOID ? s : kind == LSTM_GATE_SILU ? q * s : 1.f;
 }
 
+// A whole block: both norms of one kind with all that this kind has, types among those with kernels of their own.
+bool norm_full(const NormArgs& a);
 // Rows, pointers and widths allow groups of eight.
 bool norm_whole(const NormArgs& a);
 int norm_parts(int64_t rows, int D);

@@ -13,9 +13,16 @@ namespace lstm {
 
 namespace {
 
-template <typename TB, typename TS, int VEC, int PER>
+// KIND as in the backward pass: a whole block of one kind, or 0, whatever the arguments say.
+template <typename TB, typename TS, int VEC, int PER, int KIND, int GATE>
 __global__ void __launch_bounds__(512) norm_fwd_kernel(const NormArgs p, const int tpr)
 {
+    const int post = KIND ? KIND : p.post, pre = KIND ? KIND : p.pre, gate = KIND ? GATE : p.gate;
+    const bool has_y = KIND || p.y;
+    constexpr bool GIVEN = KIND != 0, BIAS = KIND != LSTM_NORM_RMS;
+    const bool S16 = std::is_same<TS, Any>::value ? p.stream16 : sizeof(TS) == 2;
+    const bool B16 = std::is_same<TB, Any>::value ? p.branch16 : sizeof(TB) == 2;
+    const bool N16 = KIND ? B16 : p.norm16;
     __shared__ float2 s_part[2 * 32];
     const int64_t r = tpr == 32 ? blockIdx.x * (int64_t)(blockDim.x / 32) + threadIdx.x / 32 : blockIdx.x;
     if (r >= p.rows) return;
@@ -31,18 +38,18 @@ __global__ void __launch_bounds__(512) norm_fwd_kernel(const NormArgs p, const i
         ry[k].zero();
         rg[k].zero();
         if (!c.has(k)) continue;
-        rx[k].load_own((const TS*)p.x + r * p.D + c.at(k));
-        if (p.y) ry[k].load((const TB*)p.y + r * p.ldy + c.at(k));
-        if (p.g) rg[k].load((const TB*)p.g + r * p.ldg + c.at(k));
+        load_group(rx[k], p.x, r * p.D + c.at(k), S16, true);
+        if (has_y) load_group(ry[k], p.y, r * p.ldy + c.at(k), B16);
+        if (gate) load_group(rg[k], p.g, r * p.ldg + c.at(k), B16);
     }
     float my = 0.f, sy = 1.f, mx = 0.f, sx = 1.f;
-    if (p.post) {
+    if (post) {
         float a = 0.f;
-        if (p.post == LSTM_NORM_LAYER) {
+        if (post == LSTM_NORM_LAYER) {
 #pragma unroll
             for (int k = 0; k < PER; ++k)
 #pragma unroll
-                for (int v = 0; v < VEC; ++v) a += ry[k].get(v);
+                for (int v = 0; v < VEC; ++v) a += get_value(ry[k], v, B16);
             my = sum(a, 0.f).x * inv;
             a = 0.f;
         }
@@ -51,7 +58,7 @@ __global__ void __launch_bounds__(512) norm_fwd_kernel(const NormArgs p, const i
             if (c.has(k))
 #pragma unroll
                 for (int v = 0; v < VEC; ++v) {
-                    const float d = ry[k].get(v) - my;
+                    const float d = get_value(ry[k], v, B16) - my;
                     a = fmaf(d, d, a);
                 }
         sy = 1.f / sqrtf(fmaf(sum(a, 0.f).x, inv, p.eps));
@@ -60,22 +67,22 @@ __global__ void __launch_bounds__(512) norm_fwd_kernel(const NormArgs p, const i
 #pragma unroll
     for (int k = 0; k < PER; ++k) {
 #pragma unroll
-        for (int v = 0; v < VEC; ++v) x1[k][v] = rx[k].get(v);
-        if (!p.y || !c.has(k)) continue;
+        for (int v = 0; v < VEC; ++v) x1[k][v] = get_value(rx[k], v, S16);
+        if (!has_y || !c.has(k)) continue;
         float w[VEC], b[VEC], s[VEC];
-        get_params<VEC>(p.w.w_post, c.at(k), 1.f, w);
-        get_params<VEC>(p.w.b_post, c.at(k), 0.f, b);
-        get_params<VEC>(p.w.scale, c.at(k), 1.f, s);
+        get_params<VEC, GIVEN>(p.w.w_post, c.at(k), 1.f, w);
+        get_params<VEC, GIVEN, BIAS>(p.w.b_post, c.at(k), 0.f, b);
+        get_params<VEC, GIVEN>(p.w.scale, c.at(k), 1.f, s);
 #pragma unroll
         for (int v = 0; v < VEC; ++v) {
-            const float u = fmaf((ry[k].get(v) - my) * sy, w[v], b[v]);
-            x1[k][v] = fmaf(s[v] * u, activation(p.gate, rg[k].get(v)), x1[k][v]);
+            const float u = fmaf((get_value(ry[k], v, B16) - my) * sy, w[v], b[v]);
+            x1[k][v] = fmaf(s[v] * u, gate ? activation(gate, get_value(rg[k], v, B16)) : 1.f, x1[k][v]);
         }
-        put_group<VEC>(p.x_out, r * p.D + c.at(k), sizeof(TS) == 2, x1[k]);
+        put_group<VEC>(p.x_out, r * p.D + c.at(k), S16, x1[k]);
     }
-    if (p.pre) {
+    if (pre) {
         float a = 0.f;
-        if (p.pre == LSTM_NORM_LAYER) {
+        if (pre == LSTM_NORM_LAYER) {
 #pragma unroll
             for (int k = 0; k < PER; ++k)
 #pragma unroll
@@ -96,45 +103,58 @@ __global__ void __launch_bounds__(512) norm_fwd_kernel(const NormArgs p, const i
         for (int k = 0; k < PER; ++k) {
             if (!c.has(k)) continue;
             float w[VEC], b[VEC];
-            get_params<VEC>(p.w.w_pre, c.at(k), 1.f, w);
-            get_params<VEC>(p.w.b_pre, c.at(k), 0.f, b);
+            get_params<VEC, GIVEN>(p.w.w_pre, c.at(k), 1.f, w);
+            get_params<VEC, GIVEN, BIAS>(p.w.b_pre, c.at(k), 0.f, b);
 #pragma unroll
             for (int v = 0; v < VEC; ++v) w[v] = fmaf((x1[k][v] - mx) * sx, w[v], b[v]);
-            put_group<VEC>(p.n, r * p.D + c.at(k), p.norm16, w);
+            put_group<VEC>(p.n, r * p.D + c.at(k), N16, w);
         }
     }
     if (p.stats && c.t == 0) *(float4*)(p.stats + r * 4) = make_float4(my, sy, mx, sx);
 }
 
-template <typename TB, typename TS, int VEC, int PER> lstm_status run(const NormArgs& a, int tpr, cudaStream_t cs)
+template <typename TB, typename TS, int VEC, int PER, int KIND, int GATE> lstm_status run(const NormArgs& a, int tpr, cudaStream_t cs)
 {
     const int threads = tpr == 32 ? 128 : tpr;
     const int64_t blocks = tpr == 32 ? (a.rows + 3) / 4 : a.rows;
-    norm_fwd_kernel<TB, TS, VEC, PER><<<(unsigned)blocks, threads, 0, cs>>>(a, tpr);
+    norm_fwd_kernel<TB, TS, VEC, PER, KIND, GATE><<<(unsigned)blocks, threads, 0, cs>>>(a, tpr);
     return cudaGetLastError() == cudaSuccess ? LSTM_OK : LSTM_ERR_CUDA;
+}
+
+template <typename TB, typename TS, int KIND, int GATE> lstm_status go(const NormArgs& a, cudaStream_t cs)
+{
+    // values of a thread: 32 where rows are many, 8 where a call's few rows leave SMs idle
+    auto threads = [&](int each) { return (ceil_div(a.D, each) + 31) / 32 * 32; };
+    const bool few = a.rows <= 304;
+    if (norm_whole(a)) {
+        if (a.D <= 256 || (few && threads(8) <= 512)) return run<TB, TS, 8, 1, KIND, GATE>(a, threads(8), cs);
+        if (a.D <= 512 || (few && threads(16) <= 512)) return run<TB, TS, 8, 2, KIND, GATE>(a, threads(16), cs);
+        return run<TB, TS, 8, 4, KIND, GATE>(a, threads(32), cs);
+    }
+    if (a.D <= 256 || (few && threads(8) <= 512)) return run<TB, TS, 1, 8, KIND, GATE>(a, threads(8), cs);
+    if (threads(16) <= 512) return run<TB, TS, 1, 16, KIND, GATE>(a, threads(16), cs);
+    return run<TB, TS, 1, 32, KIND, GATE>(a, threads(32), cs);
 }
 
 template <typename TB, typename TS> lstm_status go(const NormArgs& a, cudaStream_t cs)
 {
-    // values of a thread: 32 where rows are many, 8 where a call's few rows leave SMs idle
-    auto threads = [&](int each) { return (ceil_div(a.D, each) + 31) / 32 * 32; };
-    if (norm_whole(a)) {
-        const bool few = a.rows <= 304;
-        if (few && threads(8) <= 512) return run<TB, TS, 8, 1>(a, threads(8), cs);
-        if (a.D <= 256) return run<TB, TS, 8, 1>(a, 32, cs);
-        if (a.D <= 512 || (few && threads(16) <= 512)) return run<TB, TS, 8, 2>(a, threads(16), cs);
-        return run<TB, TS, 8, 4>(a, threads(32), cs);
+    constexpr int R = LSTM_NORM_RMS, L = LSTM_NORM_LAYER;
+    if (a.post == R) {
+        if (a.gate == LSTM_GATE_SILU) return go<TB, TS, R, LSTM_GATE_SILU>(a, cs);
+        return a.gate ? go<TB, TS, R, LSTM_GATE_SIGMOID>(a, cs) : go<TB, TS, R, LSTM_GATE_NONE>(a, cs);
     }
-    if (threads(8) <= 32 || (a.rows <= 304 && threads(8) <= 512)) return run<TB, TS, 1, 8>(a, threads(8), cs);
-    return run<TB, TS, 1, 32>(a, threads(32), cs);
+    if (a.gate == LSTM_GATE_SILU) return go<TB, TS, L, LSTM_GATE_SILU>(a, cs);
+    return a.gate ? go<TB, TS, L, LSTM_GATE_SIGMOID>(a, cs) : go<TB, TS, L, LSTM_GATE_NONE>(a, cs);
 }
 
 }  // namespace
 
 lstm_status launch_norm_fwd(const NormArgs& a, cudaStream_t cs)
 {
-    if (a.branch16) return a.stream16 ? go<__nv_bfloat16, __nv_bfloat16>(a, cs) : go<__nv_bfloat16, float>(a, cs);
-    return a.stream16 ? go<float, __nv_bfloat16>(a, cs) : go<float, float>(a, cs);
+    typedef __nv_bfloat16 H;
+    if (!norm_full(a)) return go<Any, Any, 0, 0>(a, cs);
+    if (!a.branch16) return go<float, float>(a, cs);
+    return a.stream16 ? go<H, H>(a, cs) : go<H, float>(a, cs);
 }
 
 }  // namespace lstm
