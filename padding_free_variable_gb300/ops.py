@@ -23,6 +23,12 @@ def _stream(stream=None) -> ctypes.c_void_p:
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _stream_of(stream, t) -> int:
+    """The stream's handle, by default the current one of t's device.  (torch.cuda.current_stream builds an object of
+    several microseconds, more than a small launch takes; torch's own compiled code asks for the bare handle.)"""
+    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(t.device.index)
+
+
 class Plan:
     """Packing plan of one batch of sequence lengths: packed (default), the padded layout,
     a segment plan (``segments=(chunk, step)``: lstm_plan_create_segments) or a window plan
@@ -33,7 +39,7 @@ class Plan:
         lens = np.ascontiguousarray(np.asarray(lengths, dtype=np.int32))
         self.lengths = lens
         self.padded = padded
-        self.scratch = {}       # device buffers of the gated linear recurrence, by size
+        self.scratch = {}       # sizes and device buffer of the gated linear recurrence's calls, by shape
         h = ctypes.c_void_p()
         lp = lens.ctypes.data_as(ctypes.POINTER(ctypes.c_int32))
         if segments is not None:
@@ -594,110 +600,113 @@ class MdLayer:
 
 # --------------------------------------------------------------------------- gated linear recurrence, block norms
 
-_DTYPES = {torch.float32: _lib.LSTM_F32, torch.bfloat16: _lib.LSTM_BF16}
-
-
 def _need(ok, what):
     if not ok:
         raise ValueError(what)
-
-
-def _addr(t):
-    return None if t is None else t.data_ptr()
 
 
 def _dense(t, dtype, shape, name):
     """Address of a contiguous tensor of this type and shape (None: none)."""
     if t is None:
         return None
-    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
-        raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {shape}, got {t.dtype} {tuple(t.shape)}")
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
     return t.data_ptr()
 
 
 def _bytes(t, need, name):
     if t is None:
         return None
-    _need(t.is_contiguous() and t.numel() * t.element_size() >= need, f"{name}: {need} contiguous bytes are needed")
+    if not t.is_contiguous() or t.numel() * t.element_size() < need:
+        raise ValueError(f"{name}: {need} contiguous bytes are needed")
     return t.data_ptr()
 
 
 def glr_shape(hidden_size, num_directions, bf16: bool, cell: str = "tied") -> _lib.GlrShape:
     """A gated linear recurrence's shape: cell "tied" (h = a h + (1 - a) z) or "gated" (h = a h + sig(i) z), a = sig(f)."""
     _need(cell in _lib.GLR_CELLS, f"unknown cell {cell!r}")
-    return _lib.GlrShape(int(hidden_size), int(num_directions), _lib.LSTM_BF16 if bf16 else _lib.LSTM_F32,
-                         _lib.GLR_CELLS.index(cell))
+    s = _lib.GlrShape(int(hidden_size), int(num_directions), _lib.LSTM_BF16 if bf16 else _lib.LSTM_F32,
+                      _lib.GLR_CELLS.index(cell))
+    s.key = (s.num_directions, s.hidden_size, torch.bfloat16 if bf16 else torch.float32, cell == "gated")
+    s.ref = ctypes.byref(s)
+    return s
 
 
-def _glr_gates(shape, f, z, i, rows, name):
+def _glr_gates(key, f, z, i, rows, name):
     """lstm_glr_gates of [rows, ndir, H] tensors that share their row and direction strides."""
-    nd, H = shape.num_directions, shape.hidden_size
-    dt = torch.bfloat16 if shape.dtype else torch.float32
-    if (i is not None) != (shape.cell == 1):
+    nd, H, dt, gated = key
+    want = (rows, nd, H)
+    if f.dtype is not dt or z.dtype is not dt or f.shape != want or z.shape != want:
+        raise ValueError(f"{name}: expected {dt} tensors of shape {want}, got {f.dtype} {tuple(f.shape)}, {z.dtype} {tuple(z.shape)}")
+    if gated:
+        if i is None or i.dtype is not dt or i.shape != want:
+            raise ValueError(f"{name}: the gated cell has a third one, i, like f and z")
+    elif i is not None:
         raise ValueError(f"{name}: i belongs to the gated cell")
-    want, strides = (rows, nd, H), None
-    for t in (f, z) if i is None else (f, z, i):
-        if t.dtype != dt or tuple(t.shape) != want:
-            raise ValueError(f"{name}: expected {dt} tensors of shape {want}, got {t.dtype} {tuple(t.shape)}")
-        ld, ds, us = t.stride()
-        # the stride of a single row, direction or unit is never stepped over
-        st = (ld if rows > 1 else H, ds if nd > 1 else H)
-        if (us != 1 and H > 1) or (strides is not None and st != strides):
+    ld, ds, us = f.stride()
+    # the stride of a single row, direction or unit is never stepped over
+    ld, ds = ld if rows > 1 else H, ds if nd > 1 else H
+    for t in (f, z, i) if gated else (f, z):
+        a, b, c = t.stride()
+        if (a != ld and rows > 1) or (b != ds and nd > 1) or (c != 1 and H > 1):
             raise ValueError(f"{name}: units have to lie next to each other, and all gates to have the same strides")
-        strides = st
-    return _lib.GlrGates(f.data_ptr(), z.data_ptr(), _addr(i), strides[0], strides[1])
+    return _lib.GlrGates(f.data_ptr(), z.data_ptr(), i.data_ptr() if gated else None, ld, ds)
+
+
+def _glr_sizes(plan: Plan, shape, device=None):
+    """Workspace bytes, and the plan's scratch for this shape (kept with the plan, whose calls share it, one stream at a
+    time)."""
+    got = plan.scratch.get(shape.key)
+    if got is None or (got[2] and got[1] is None and device is not None):
+        lib = _lib.load()
+        need = int(lib.lstm_glr_scratch_bytes(plan.handle, shape.ref))
+        buf = torch.empty(need, dtype=torch.uint8, device=device) if need and device is not None else None
+        got = plan.scratch[shape.key] = (int(lib.lstm_glr_workspace_bytes(plan.handle, shape.ref)), buf, need)
+    return got
 
 
 def glr_workspace_bytes(plan: Plan, shape) -> int:
-    return int(_lib.load().lstm_glr_workspace_bytes(plan.handle, ctypes.byref(shape)))
-
-
-def _glr_scratch(plan: Plan, shape, device):
-    """The plan's scratch of this size (kept with the plan: its calls share it, one stream at a time)."""
-    need = int(_lib.load().lstm_glr_scratch_bytes(plan.handle, ctypes.byref(shape)))
-    if need == 0:
-        return None
-    if need not in plan.scratch:
-        plan.scratch[need] = torch.empty(need, dtype=torch.uint8, device=device)
-    return plan.scratch[need].data_ptr()
+    return _glr_sizes(plan, shape)[0]
 
 
 def glr_forward(plan: Plan, shape, f, z, i, h0, y, h_n, workspace, stream=None):
     """lstm_glr_fwd: f, z and (gated cell) i [rows, ndir, H] views, h0 / h_n [ndir, B, H] fp32 in caller order or None,
     y [rows, ndir, H]; workspace: a buffer of glr_workspace_bytes that glr_backward reads, or None."""
-    nd, H = shape.num_directions, shape.hidden_size
-    g = _glr_gates(shape, f, z, i, plan.rows, "gates")
+    key, rows = shape.key, plan.rows
+    nd, H, dt, _ = key
+    g = _glr_gates(key, f, z, i, rows, "gates")
     st = (nd, plan.batch, H)
+    need, scratch, _ = _glr_sizes(plan, shape, f.device)
     check(_lib.load().lstm_glr_fwd(
-        plan.handle, ctypes.byref(shape), ctypes.byref(g), _dense(h0, torch.float32, st, "h0"),
-        _dense(y, f.dtype, (plan.rows, nd, H), "y"), _dense(h_n, torch.float32, st, "h_n"),
-        _bytes(workspace, glr_workspace_bytes(plan, shape), "workspace") if workspace is not None else None,
-        _glr_scratch(plan, shape, f.device), _stream(stream)), "lstm_glr_fwd")
+        plan.handle, shape.ref, ctypes.byref(g), _dense(h0, torch.float32, st, "h0"), _dense(y, dt, (rows, nd, H), "y"),
+        _dense(h_n, torch.float32, st, "h_n"), _bytes(workspace, need, "workspace"),
+        None if scratch is None else scratch.data_ptr(), _stream_of(stream, f)), "lstm_glr_fwd")
 
 
 def glr_backward(plan: Plan, shape, f, z, i, workspace, dy, dh_n, df, dz, di, dh0, stream=None):
     """lstm_glr_bwd: dy [rows, ndir, H], dh_n / dh0 [ndir, B, H] fp32 or None, df, dz, di [rows, ndir, H] views."""
-    nd, H = shape.num_directions, shape.hidden_size
-    g = _glr_gates(shape, f, z, i, plan.rows, "gates")
-    dg = _glr_gates(shape, df, dz, di, plan.rows, "gate gradients")
+    key, rows = shape.key, plan.rows
+    nd, H, dt, _ = key
+    g = _glr_gates(key, f, z, i, rows, "gates")
+    dg = _glr_gates(key, df, dz, di, rows, "gate gradients")
     st = (nd, plan.batch, H)
+    need, scratch, _ = _glr_sizes(plan, shape, f.device)
     check(_lib.load().lstm_glr_bwd(
-        plan.handle, ctypes.byref(shape), ctypes.byref(g),
-        _bytes(workspace, glr_workspace_bytes(plan, shape), "workspace"), _dense(dy, f.dtype, (plan.rows, nd, H), "dy"),
+        plan.handle, shape.ref, ctypes.byref(g), _bytes(workspace, need, "workspace"), _dense(dy, dt, (rows, nd, H), "dy"),
         _dense(dh_n, torch.float32, st, "dh_n"), ctypes.byref(dg), _dense(dh0, torch.float32, st, "dh0"),
-        _glr_scratch(plan, shape, f.device), _stream(stream)), "lstm_glr_bwd")
+        None if scratch is None else scratch.data_ptr(), _stream_of(stream, f)), "lstm_glr_bwd")
 
 
 def glr_step(shape, f, z, i, state_in, state_out, y, slots=None, stream=None):
     """lstm_glr_step: one frame of each of f.shape[0] streams; state_in / state_out [slots, H] fp32 (may be the same),
     y [rows, 1, H]; slots: int32 [rows] state row of each stream (outside the cache: idle), None for stream r in row r."""
-    rows, H = f.shape[0], shape.hidden_size
-    g = _glr_gates(shape, f, z, i, rows, "gates")
-    n = state_in.shape[0]
+    key, rows, n = shape.key, f.shape[0], state_in.shape[0]
+    H = key[1]
+    g = _glr_gates(key, f, z, i, rows, "gates")
     check(_lib.load().lstm_glr_step(
-        ctypes.byref(shape), ctypes.byref(g), rows, _dense(slots, torch.int32, (rows,), "slots"), n,
+        shape.ref, ctypes.byref(g), rows, _dense(slots, torch.int32, (rows,), "slots"), n,
         _dense(state_in, torch.float32, (n, H), "state_in"), _dense(state_out, torch.float32, (n, H), "state_out"),
-        _dense(y, f.dtype, (rows, 1, H), "y"), _stream(stream)), "lstm_glr_step")
+        _dense(y, key[2], (rows, 1, H), "y"), _stream_of(stream, f)), "lstm_glr_step")
 
 
 def block_norm_shape(width, kind: str = "rms", gate: str = "silu", branch_bf16: bool = False, stream_bf16: bool = False,
@@ -706,64 +715,68 @@ def block_norm_shape(width, kind: str = "rms", gate: str = "silu", branch_bf16: 
     post = kind if post_kind is None else post_kind
     _need(kind in _lib.NORM_KINDS and post in _lib.NORM_KINDS, f"unknown norm {kind!r} / {post!r}")
     _need(gate in _lib.GATE_KINDS, f"unknown gate {gate!r}")
-    return _lib.BlockNormShape(int(width), _lib.NORM_KINDS.index(post), _lib.NORM_KINDS.index(kind),
-                               _lib.GATE_KINDS.index(gate), int(bool(branch_bf16)), int(bool(stream_bf16)),
-                               int(bool(norm_bf16)), float(eps))
+    s = _lib.BlockNormShape(int(width), _lib.NORM_KINDS.index(post), _lib.NORM_KINDS.index(kind),
+                            _lib.GATE_KINDS.index(gate), int(bool(branch_bf16)), int(bool(stream_bf16)),
+                            int(bool(norm_bf16)), float(eps))
+    s.types = tuple(torch.bfloat16 if b else torch.float32 for b in (branch_bf16, stream_bf16, norm_bf16))
+    s.row, s.ref = (s.width,), ctypes.byref(s)
+    return s
 
 
 def _norm_params(shape, p):
     """w_post, b_post, scale, w_pre, b_pre of a dict that may lack any of them."""
-    d = (shape.width,)
-    return _lib.BlockNormParams(*[_dense(p.get(k), torch.float32, d, k) for k in
-                                  ("w_post", "b_post", "scale", "w_pre", "b_pre")])
+    d, f32, get = shape.row, torch.float32, p.get
+    return _lib.BlockNormParams(_dense(get("w_post"), f32, d, "w_post"), _dense(get("b_post"), f32, d, "b_post"),
+                                _dense(get("scale"), f32, d, "scale"), _dense(get("w_pre"), f32, d, "w_pre"),
+                                _dense(get("b_pre"), f32, d, "b_pre"))
 
 
-def _rows(t, dtype, rows, width, name):
+def _rows(t, dtype, shape, name):
     """(address, row stride) of a [rows, width] tensor whose columns lie next to each other (None: none)."""
     if t is None:
         return None, 0
-    if t.dtype != dtype or tuple(t.shape) != (rows, width) or (t.stride(1) != 1 and width > 1):
-        raise ValueError(f"{name}: expected a {dtype} tensor of shape {(rows, width)} with adjacent columns")
-    return t.data_ptr(), t.stride(0) if rows > 1 else max(t.stride(0), width)
+    ld, one = t.stride() if t.dim() == 2 else (0, 0)
+    if t.dtype is not dtype or t.shape != shape or (one != 1 and shape[1] > 1):
+        raise ValueError(f"{name}: expected a {dtype} tensor of shape {tuple(shape)} with adjacent columns")
+    return t.data_ptr(), ld if shape[0] > 1 else shape[1]
 
 
-def _norm_rows(shape, x, y, gate, names):
-    br = torch.bfloat16 if shape.branch_dtype else torch.float32
-    rows, D = x.shape
-    yp, yst = _rows(y, br, rows, D, names[1])
-    gp, gst = _rows(gate, br, rows, D, names[2])
-    return _lib.BlockNormInputs(_dense(x, torch.bfloat16 if shape.stream_dtype else torch.float32, (rows, shape.width),
-                                       names[0]), yp, gp, yst, gst)
+def _norm_rows(types, shape, x, y, gate, names):
+    yp, yst = _rows(y, types[0], shape, names[1])
+    gp, gst = _rows(gate, types[0], shape, names[2])
+    return _lib.BlockNormInputs(_dense(x, types[1], shape, names[0]), yp, gp, yst, gst)
+
+
+_FORWARD_ROWS, _BACKWARD_ROWS = ("x", "y", "gate"), ("dx", "dy", "dgate")
 
 
 def block_norm_forward(shape, x, y, gate, params: dict, x_out, n, stats=None, stream=None):
     """lstm_block_norm_fwd: x [rows, D], y and gate [rows, D] (rows may be strided) or None, params a dict of w_post,
     b_post, scale, w_pre, b_pre (fp32 [D], any may be absent); writes x_out and n, and stats [rows, 4] fp32 for the
     backward pass."""
-    rows, D = x.shape
-    rin = _norm_rows(shape, x, y, gate, ("x", "y", "gate"))
+    rows, types = x.shape[0], shape.types
+    rd = (rows, shape.width)
+    rin = _norm_rows(types, rd, x, y, gate, _FORWARD_ROWS)
     p = _norm_params(shape, params)
     check(_lib.load().lstm_block_norm_fwd(
-        ctypes.byref(shape), ctypes.byref(p), ctypes.byref(rin), rows, _dense(x_out, x.dtype, (rows, D), "x_out"),
-        _dense(n, torch.bfloat16 if shape.norm_dtype else torch.float32, (rows, D), "n"),
-        _dense(stats, torch.float32, (rows, 4), "stats"), _stream(stream)), "lstm_block_norm_fwd")
+        shape.ref, ctypes.byref(p), ctypes.byref(rin), rows, _dense(x_out, types[1], rd, "x_out"), _dense(n, types[2], rd, "n"),
+        _dense(stats, torch.float32, (rows, 4), "stats"), _stream_of(stream, x)), "lstm_block_norm_fwd")
 
 
 def block_norm_scratch_bytes(shape, rows: int) -> int:
-    return int(_lib.load().lstm_block_norm_scratch_bytes(ctypes.byref(shape), int(rows)))
+    return int(_lib.load().lstm_block_norm_scratch_bytes(shape.ref, int(rows)))
 
 
 def block_norm_backward(shape, x, y, gate, params: dict, stats, dx_out, dn, dx, dy, dgate, grads: dict, scratch,
                         stream=None):
     """lstm_block_norm_bwd: x, y, gate, params, stats of the forward call; dx_out and dn [rows, D] or None; writes dx, dy,
     dgate and the gradients of the parameters that `grads` names."""
-    rows, D = x.shape
-    rin = _norm_rows(shape, x, y, gate, ("x", "y", "gate"))
-    din = _norm_rows(shape, dx, dy, dgate, ("dx", "dy", "dgate"))
+    rows, types = x.shape[0], shape.types
+    rd = (rows, shape.width)
+    rin = _norm_rows(types, rd, x, y, gate, _FORWARD_ROWS)
+    din = _norm_rows(types, rd, dx, dy, dgate, _BACKWARD_ROWS)
     p, g = _norm_params(shape, params), _norm_params(shape, grads)
     check(_lib.load().lstm_block_norm_bwd(
-        ctypes.byref(shape), ctypes.byref(p), ctypes.byref(rin), rows, _dense(stats, torch.float32, (rows, 4), "stats"),
-        _dense(dx_out, x.dtype, (rows, D), "dx_out"),
-        _dense(dn, torch.bfloat16 if shape.norm_dtype else torch.float32, (rows, D), "dn"), ctypes.byref(din),
-        ctypes.byref(g), _bytes(scratch, block_norm_scratch_bytes(shape, rows), "scratch"), _stream(stream)),
-        "lstm_block_norm_bwd")
+        shape.ref, ctypes.byref(p), ctypes.byref(rin), rows, _dense(stats, torch.float32, (rows, 4), "stats"),
+        _dense(dx_out, types[1], rd, "dx_out"), _dense(dn, types[2], rd, "dn"), ctypes.byref(din), ctypes.byref(g),
+        _bytes(scratch, block_norm_scratch_bytes(shape, rows), "scratch"), _stream_of(stream, x)), "lstm_block_norm_bwd")
