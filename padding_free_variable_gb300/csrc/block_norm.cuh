@@ -174,29 +174,36 @@ __device__ __forceinline__ void get_params(const float* p, int at, float none, f
 // Sums over the threads of a row: within a warp by shuffles, across the warps of a CTA (then one
 // row a CTA) through shared memory, each use on the other half so that one barrier suffices.
 struct RowSum {
-    float2* part;           // [2][32]
+    float* part;            // [2][16][4]
     int warps, half;
-    __device__ __forceinline__ float2 operator()(float a, float b)
+    template <int N> __device__ __forceinline__ void operator()(float (&v)[N])
     {
+        static_assert(N <= 4, "four sums at a time");
 #pragma unroll
-        for (int o = 16; o; o >>= 1) {
-            a += __shfl_xor_sync(0xffffffffu, a, o);
-            b += __shfl_xor_sync(0xffffffffu, b, o);
-        }
-        if (warps == 1) return make_float2(a, b);
-        float2* s = part + half * 32;
+        for (int o = 16; o; o >>= 1)
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+        if (warps == 1) return;
+        float* s = part + half * 64;
         half ^= 1;
-        if (threadIdx.x % 32 == 0) s[threadIdx.x / 32] = make_float2(a, b);
-        __syncthreads();
-        const float2 q = threadIdx.x % 32 < warps ? s[threadIdx.x % 32] : make_float2(0.f, 0.f);
-        a = q.x;
-        b = q.y;
+        if (threadIdx.x % 32 == 0)
 #pragma unroll
-        for (int o = 16; o; o >>= 1) {
-            a += __shfl_xor_sync(0xffffffffu, a, o);
-            b += __shfl_xor_sync(0xffffffffu, b, o);
-        }
-        return make_float2(a, b);
+            for (int i = 0; i < N; ++i) s[threadIdx.x / 32 * 4 + i] = v[i];
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = threadIdx.x % 32 < warps ? s[threadIdx.x % 32 * 4 + i] : 0.f;
+#pragma unroll
+        for (int o = 8; o; o >>= 1)
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = __shfl_sync(0xffffffffu, v[i], 0);
+    }
+    __device__ __forceinline__ float operator()(float x)
+    {
+        float v[1] = {x};
+        (*this)(v);
+        return v[0];
     }
 };
 
@@ -220,6 +227,6 @@ bool norm_full(const NormArgs& a);
 bool norm_whole(const NormArgs& a);
 int norm_parts(int64_t rows, int D);
 lstm_status launch_norm_fwd(const NormArgs& a, cudaStream_t cs);
-lstm_status launch_norm_bwd(const NormArgs& a, cudaStream_t cs);
+lstm_status launch_norm_bwd(NormArgs a, cudaStream_t cs);
 
 }  // namespace lstm

@@ -24,6 +24,8 @@ struct BwdShape {
 };
 
 // Eight values a thread while a row then fits a CTA of 512.
+constexpr int kSMs = 152;
+
 inline BwdShape bwd_shape(int D)
 {
     BwdShape s;
@@ -37,31 +39,80 @@ inline BwdShape bwd_shape(int D)
 
 namespace {
 
+// Arithmetic on one value or on two at once.
+__device__ __forceinline__ float fma2(float a, float b, float c) { return fmaf(a, b, c); }
+template <typename X> __device__ __forceinline__ X both(float v);
+template <> __device__ __forceinline__ float both<float>(float v) { return v; }
+template <> __device__ __forceinline__ F2 both<F2>(float v) { return F2(v, v); }
+template <typename X> __device__ __forceinline__ X minus(X a, X b) { return fma2(b, both<X>(-1.f), a); }
+__device__ __forceinline__ float total(float v) { return v; }
+__device__ __forceinline__ float total(F2 v) { return v.lo() + v.hi(); }
+__device__ __forceinline__ void spread(float v, float* to) { to[0] = v; }
+__device__ __forceinline__ void spread(F2 v, float* to) { to[0] = v.lo(); to[1] = v.hi(); }
+__device__ __forceinline__ void gate_pair(float x, float& s, float& c) { sigmoid_pair(x, s, c); }
+__device__ __forceinline__ void gate_pair(F2 x, F2& s, F2& c) { sigmoid_pair2(x, s, c); }
+__device__ __forceinline__ float gate_value(float x) { return rcp_approx(1.f + ex2_approx(x * kNegLog2e)); }
+__device__ __forceinline__ F2 gate_value(F2 x) { return sigmoid2(x); }
+
+template <typename X, typename G> __device__ __forceinline__ X values(const G& g, int v, bool b16)
+{
+    if constexpr (std::is_same<X, float>::value) return get_value(g, v, b16);
+    else return F2(get_value(g, v, b16), get_value(g, v + 1, b16));
+}
+template <typename X> __device__ __forceinline__ X pick(const float* v, int i)
+{
+    if constexpr (std::is_same<X, float>::value) return v[i];
+    else return F2(v[i], v[i + 1]);
+}
+
+// Means over a row of t xh (m1) and, for centred norms, of t (m0); sums: R of the one, R of the other.
+template <int R> __device__ __forceinline__ void row_means(RowSum& sum, float (&sums)[2 * R], bool centred, float inv, float (&m0)[R], float (&m1)[R])
+{
+    if (centred) {
+        sum(sums);
+    } else {
+        float v[R];
+#pragma unroll
+        for (int q = 0; q < R; ++q) v[q] = sums[q];
+        sum(v);
+#pragma unroll
+        for (int q = 0; q < R; ++q) sums[q] = v[q];
+    }
+#pragma unroll
+    for (int q = 0; q < R; ++q) {
+        m1[q] = sums[q] * inv;
+        m0[q] = centred ? sums[R + q] * inv : 0.f;
+    }
+}
+
 // One warp a row (four rows a CTA) up to 256 columns, one CTA a row beyond.
-template <typename TB, typename TS, typename TN, int VEC, int PER, int THREADS, int CTAS, int KIND, int GATE>
+template <typename TB, typename TS, typename TN, int VEC, int PER, int R, int THREADS, int CTAS, int KIND, int GATE>
 __global__ void __launch_bounds__(THREADS, CTAS) norm_bwd_kernel(const NormArgs p, const int tpr)
 {
     // KIND: LSTM_NORM_RMS (no biases) or LSTM_NORM_LAYER (biases), a whole block with everything
     // given and wanted, or 0: whatever the arguments say
     const int post = KIND ? KIND : p.post, pre = KIND ? KIND : p.pre, gate = KIND ? GATE : p.gate;
     const bool has_y = KIND || p.y, has_dn = KIND || p.dn, has_dxo = KIND || p.dx_out;
-    constexpr bool GIVEN = KIND != 0, BIAS = KIND != LSTM_NORM_RMS;
+    constexpr bool GIVEN = KIND != 0, BIAS = KIND != LSTM_NORM_RMS, CENTRED = BIAS;
     auto wants = [&](int which) { return KIND ? which % 3 != 1 || KIND == LSTM_NORM_LAYER : p.sums[which] != nullptr; };
     constexpr int Q = VEC == 1 ? 1 : 4, N = VEC / Q;        // values handled together, such pieces of a group
+    typedef typename std::conditional<VEC == 1, float, F2>::type X;     // values taken at once: P of them
+    constexpr int P = VEC == 1 ? 1 : 2;
     constexpr bool FAR = PER * VEC > 16;                    // the widest rows' sums do not fit shared memory: in the CTA's part
     // known types at compile time
     const bool S16 = std::is_same<TS, Any>::value ? p.stream16 : sizeof(TS) == 2;
     const bool B16 = std::is_same<TB, Any>::value ? p.branch16 : sizeof(TB) == 2;
     const bool N16 = std::is_same<TN, Any>::value ? p.norm16 : sizeof(TN) == 2;
-    __shared__ float2 s_part[2 * 32];
+    __shared__ float s_part[2 * 64];
     extern __shared__ __align__(16) float s_sums[];         // [kSums][PER * N][THREADS][Q]
     const int groups = blockDim.x / tpr, group = threadIdx.x / tpr;
+    // R rows at a time: the parameters are read and their sums updated once for them
     const Cols<VEC, PER> c{(int)threadIdx.x % tpr, tpr, p.D};
     RowSum sum{s_part, tpr / 32, 0};
     const float inv = 1.f / (float)p.D;
-    float* const part = p.part + (int64_t)blockIdx.x * kSums * p.D;
+    float* const out = p.part + (int64_t)blockIdx.x * kSums * p.D;
     auto place = [&](int which, int k, int n) {
-        return FAR ? part + which * p.D + c.at(k) + n * Q : s_sums + ((which * PER * N + k * N + n) * THREADS + (int)threadIdx.x) * Q;
+        return FAR ? out + which * p.D + c.at(k) + n * Q : s_sums + ((which * PER * N + k * N + n) * THREADS + (int)threadIdx.x) * Q;
     };
     auto add = [&](int which, int k, int n, const float (&x)[Q]) {
         float* at = place(which, k, n);
@@ -82,35 +133,50 @@ __global__ void __launch_bounds__(THREADS, CTAS) norm_bwd_kernel(const NormArgs 
 #pragma unroll
                     for (int i = 0; i < Q; ++i) place(which, k, n)[i] = 0.f;
 
-    for (int64_t r = blockIdx.x * (int64_t)groups + group; r < p.rows; r += (int64_t)gridDim.x * groups) {
-        Group<TS, VEC> rx[PER], rd[PER];
-        Group<TB, VEC> ry[PER], rg[PER];
-        Group<TN, VEC> rn[PER];
+    for (int64_t r0 = (blockIdx.x * (int64_t)groups + group) * R; r0 < p.rows; r0 += (int64_t)gridDim.x * groups * R) {
+        Group<TS, VEC> rx[R][PER], rd[R][PER];
+        Group<TB, VEC> ry[R][PER], rg[R][PER];
+        Group<TN, VEC> rn[R][PER];
+        float my[R], sy[R], mx[R], sx[R];
 #pragma unroll
-        for (int k = 0; k < PER; ++k) {
-            rx[k].zero();
-            rd[k].zero();
-            ry[k].zero();
-            rg[k].zero();
-            rn[k].zero();
-            if (!c.has(k)) continue;
-            load_group(rx[k], p.x, r * p.D + c.at(k), S16);
-            if (has_y) load_group(ry[k], p.y, r * p.ldy + c.at(k), B16);
-            if (gate) load_group(rg[k], p.g, r * p.ldg + c.at(k), B16);
-            if (has_dn) load_group(rn[k], p.dn, r * p.D + c.at(k), N16);
-            if (has_dxo) load_group(rd[k], p.dx_out, r * p.D + c.at(k), S16, true);
+        for (int q = 0; q < R; ++q) {
+            // a last row without a partner: zeros, which add nothing and are not written
+            const bool row = q == 0 || r0 + q < p.rows;
+            const int64_t r = row ? r0 + q : r0;
+#pragma unroll
+            for (int k = 0; k < PER; ++k) {
+                rx[q][k].zero();
+                rd[q][k].zero();
+                ry[q][k].zero();
+                rg[q][k].zero();
+                rn[q][k].zero();
+                if (!c.has(k) || !row) continue;
+                load_group(rx[q][k], p.x, r * p.D + c.at(k), S16);
+                if (has_y) load_group(ry[q][k], p.y, r * p.ldy + c.at(k), B16);
+                if (gate) load_group(rg[q][k], p.g, r * p.ldg + c.at(k), B16);
+                if (has_dn) load_group(rn[q][k], p.dn, r * p.D + c.at(k), N16);
+                if (has_dxo) load_group(rd[q][k], p.dx_out, r * p.D + c.at(k), S16, true);
+            }
+            const float4 st = __ldg((const float4*)(p.stats + r * 4));
+            my[q] = KIND == LSTM_NORM_RMS ? 0.f : st.x;
+            sy[q] = st.y;
+            mx[q] = KIND == LSTM_NORM_RMS ? 0.f : st.z;
+            sx[q] = st.w;
         }
-        const float4 st = __ldg((const float4*)(p.stats + r * 4));
-        const float my = KIND == LSTM_NORM_RMS ? 0.f : st.x, sy = st.y, mx = KIND == LSTM_NORM_RMS ? 0.f : st.z, sx = st.w;
-        float xh[PER][VEC], t[PER][VEC];
-        float a = 0.f, b = 0.f;
+        X xh[R][PER][VEC / P], t[R][PER][VEC / P];
+        float sums[2 * R];              // of t xh, then (centred norms) of t
+        X part[2 * R];
+#pragma unroll
+        for (int q = 0; q < 2 * R; ++q) part[q] = both<X>(0.f);
 #pragma unroll
         for (int k = 0; k < PER; ++k)
 #pragma unroll
             for (int n = 0; n < N; ++n) {
                 float wq[Q], bq[Q], s[Q], wp[Q];
 #pragma unroll
-                for (int i = 0; i < Q; ++i) xh[k][n * Q + i] = t[k][n * Q + i] = 0.f;
+                for (int q = 0; q < R; ++q)
+#pragma unroll
+                    for (int i = n * Q / P; i < (n + 1) * Q / P; ++i) xh[q][k][i] = t[q][k][i] = both<X>(0.f);
                 if (!c.has(k)) continue;
                 const int at = c.at(k) + n * Q;
                 get_params<Q, GIVEN>(p.w.w_post, at, 1.f, wq);
@@ -118,83 +184,133 @@ __global__ void __launch_bounds__(THREADS, CTAS) norm_bwd_kernel(const NormArgs 
                 get_params<Q, GIVEN>(p.w.scale, at, 1.f, s);
                 get_params<Q, GIVEN>(p.w.w_pre, at, 1.f, wp);
 #pragma unroll
-                for (int i = 0; i < Q; ++i) {
-                    const int v = n * Q + i;
-                    float x1 = get_value(rx[k], v, S16);
-                    if (has_y) {
-                        const float u = fmaf((get_value(ry[k], v, B16) - my) * sy, wq[i], bq[i]);
-                        x1 = fmaf(s[i] * u, gate ? activation(gate, get_value(rg[k], v, B16)) : 1.f, x1);
+                for (int q = 0; q < R; ++q)
+#pragma unroll
+                    for (int i = 0; i < Q; i += P) {
+                        const int v = n * Q + i;
+                        X x1 = values<X>(rx[q][k], v, S16);
+                        if (has_y) {
+                            X u = values<X>(ry[q][k], v, B16);
+                            if (CENTRED) u = u + both<X>(-my[q]);
+                            u = u * both<X>(sy[q]) * pick<X>(wq, i);
+                            if (BIAS) u = u + pick<X>(bq, i);
+                            u = u * pick<X>(s, i);
+                            if (gate) {
+                                const X g = values<X>(rg[q][k], v, B16), a = gate_value(g);
+                                u = u * (gate == LSTM_GATE_SILU ? g * a : a);
+                            }
+                            x1 = x1 + u;
+                        }
+                        if (CENTRED) x1 = x1 + both<X>(-mx[q]);
+                        const X h = x1 * both<X>(sx[q]), e = values<X>(rn[q][k], v, N16) * pick<X>(wp, i);
+                        xh[q][k][v / P] = h;
+                        t[q][k][v / P] = e;
+                        part[q] = fma2(e, h, part[q]);
+                        if (CENTRED) part[R + q] = part[R + q] + e;
                     }
-                    xh[k][v] = (x1 - mx) * sx;
-                    t[k][v] = get_value(rn[k], v, N16) * wp[i];
-                    a += t[k][v];
-                    b = fmaf(t[k][v], xh[k][v], b);
-                }
             }
-        float m0 = 0.f, m1 = 0.f;
-        if (has_dn) {
-            const float2 q = sum(a, b);
-            if (pre == LSTM_NORM_LAYER) m0 = q.x * inv;
-            m1 = q.y * inv;
+#pragma unroll
+        for (int q = 0; q < 2 * R; ++q) {
+            sums[q] = total(part[q]);
+            part[q] = both<X>(0.f);
         }
-        a = b = 0.f;
+        float m0[R], m1[R];
+        if (has_dn) row_means(sum, sums, pre == LSTM_NORM_LAYER, inv, m0, m1);
 #pragma unroll
         for (int k = 0; k < PER; ++k)
 #pragma unroll
             for (int n = 0; n < N; ++n) {
                 if (!c.has(k)) continue;
-                float wq[Q], bq[Q], s[Q], dx[Q], dg[Q], e[Q], f[Q];
+                float wq[Q], bq[Q], s[Q];
+                X a[kSums][Q / P];      // the parameters' gradients' terms of these rows
                 const int at = c.at(k) + n * Q;
-#pragma unroll
-                for (int i = 0; i < Q; ++i) {
-                    const int v = n * Q + i;
-                    dx[i] = get_value(rd[k], v, S16);
-                    if (has_dn) dx[i] = fmaf(sx, t[k][v] - m0 - xh[k][v] * m1, dx[i]);
-                    e[i] = get_value(rn[k], v, N16);
-                    f[i] = e[i] * xh[k][v];
-                }
-                if (wants(3)) add(3, k, n, f);
-                if (wants(4)) add(4, k, n, e);
-                put_group<Q>(p.dx, r * p.D + at, S16, dx);
-                if (!has_y) continue;
                 get_params<Q, GIVEN>(p.w.w_post, at, 1.f, wq);
                 get_params<Q, GIVEN, BIAS>(p.w.b_post, at, 0.f, bq);
                 get_params<Q, GIVEN>(p.w.scale, at, 1.f, s);
 #pragma unroll
-                for (int i = 0; i < Q; ++i) {
-                    const int v = n * Q + i;
-                    const float yh = (get_value(ry[k], v, B16) - my) * sy, u = fmaf(yh, wq[i], bq[i]), du = dx[i] * s[i];
-                    float act = 1.f, slope = 0.f;
-                    if (gate) activation(gate, get_value(rg[k], v, B16), act, slope);
-                    const float dv = du * act;
-                    dg[i] = du * u * slope;
-                    t[k][v] = dv * wq[i];
-                    xh[k][v] = yh;
-                    a += t[k][v];
-                    b = fmaf(t[k][v], yh, b);
-                    wq[i] = dv * yh;
-                    bq[i] = dv;
-                    s[i] = dx[i] * u * act;
+                for (int which = 0; which < kSums; ++which)
+#pragma unroll
+                    for (int i = 0; i < Q / P; ++i) a[which][i] = both<X>(0.f);
+#pragma unroll
+                for (int q = 0; q < R; ++q) {
+                    const bool row = q == 0 || r0 + q < p.rows;
+                    const int64_t r = r0 + q;
+                    float dx[Q], dg[Q];
+#pragma unroll
+                    for (int i = 0; i < Q; i += P) {
+                        const int v = n * Q + i;
+                        const X h = xh[q][k][v / P], e = values<X>(rn[q][k], v, N16);
+                        X d = values<X>(rd[q][k], v, S16);
+                        if (has_dn) {
+                            X x = fma2(h, both<X>(-m1[q]), t[q][k][v / P]);
+                            if (CENTRED) x = x + both<X>(-m0[q]);
+                            d = fma2(x, both<X>(sx[q]), d);
+                        }
+                        a[3][i / P] = fma2(e, h, a[3][i / P]);
+                        a[4][i / P] = a[4][i / P] + e;
+                        spread(d, dx + i);
+                        if (!has_y) continue;
+                        X yh = values<X>(ry[q][k], v, B16);
+                        if (CENTRED) yh = yh + both<X>(-my[q]);
+                        yh = yh * both<X>(sy[q]);
+                        X u = yh * pick<X>(wq, i);
+                        if (BIAS) u = u + pick<X>(bq, i);
+                        X du = d * pick<X>(s, i), dv = du, ua = u;
+                        if (gate) {
+                            const X g = values<X>(rg[q][k], v, B16);
+                            X act, neg;
+                            gate_pair(g, act, neg);
+                            // act' = s (1 - s), or of the silu gate s (1 + g (1 - s))
+                            const X slope = gate == LSTM_GATE_SILU ? act * fma2(g, neg, both<X>(1.f)) : act * neg;
+                            if (gate == LSTM_GATE_SILU) act = g * act;
+                            spread(du * u * slope, dg + i);
+                            dv = du * act;
+                            ua = u * act;
+                        }
+                        const X e2 = dv * pick<X>(wq, i);
+                        t[q][k][v / P] = e2;
+                        xh[q][k][v / P] = yh;
+                        part[q] = fma2(e2, yh, part[q]);
+                        if (CENTRED) part[R + q] = part[R + q] + e2;
+                        a[0][i / P] = fma2(dv, yh, a[0][i / P]);
+                        a[1][i / P] = a[1][i / P] + dv;
+                        a[2][i / P] = fma2(d, ua, a[2][i / P]);
+                    }
+                    if (row) put_group<Q>(p.dx, r * p.D + at, S16, dx);
+                    if (gate && row) put_group<Q>(p.dg, r * p.lddg + at, B16, dg);
                 }
-                if (wants(0)) add(0, k, n, wq);
-                if (wants(1)) add(1, k, n, bq);
-                if (wants(2)) add(2, k, n, s);
-                if (gate) put_group<Q>(p.dg, r * p.lddg + at, B16, dg);
+#pragma unroll
+                for (int which = 0; which < kSums; ++which)
+                    if (wants(which)) {
+                        float f[Q];
+#pragma unroll
+                        for (int i = 0; i < Q; i += P) spread(a[which][i / P], f + i);
+                        add(which, k, n, f);
+                    }
             }
         if (!has_y) continue;
-        float k0 = 0.f, k1 = 0.f;
-        if (post) {
-            const float2 q = sum(a, b);
-            if (post == LSTM_NORM_LAYER) k0 = q.x * inv;
-            k1 = q.y * inv;
-        }
 #pragma unroll
-        for (int k = 0; k < PER; ++k) {
-            if (!c.has(k)) continue;
-            float dy[VEC];
+        for (int q = 0; q < 2 * R; ++q) sums[q] = total(part[q]);
+        if (post) row_means(sum, sums, post == LSTM_NORM_LAYER, inv, m0, m1);
 #pragma unroll
-            for (int v = 0; v < VEC; ++v) dy[v] = post ? sy * (t[k][v] - k0 - xh[k][v] * k1) : t[k][v];
-            put_group<VEC>(p.dy, r * p.lddy + c.at(k), B16, dy);
+        for (int q = 0; q < R; ++q) {
+            if (q > 0 && r0 + q >= p.rows) continue;
+#pragma unroll
+            for (int k = 0; k < PER; ++k) {
+                if (!c.has(k)) continue;
+                float dy[VEC];
+#pragma unroll
+                for (int v = 0; v < VEC; v += P) {
+                    X d = t[q][k][v / P];
+                    if (post) {
+                        d = fma2(xh[q][k][v / P], both<X>(-m1[q]), d);
+                        if (CENTRED) d = d + both<X>(-m0[q]);
+                        d = d * both<X>(sy[q]);
+                    }
+                    spread(d, dy + v);
+                }
+                put_group<VEC>(p.dy, (r0 + q) * p.lddy + c.at(k), B16, dy);
+            }
         }
     }
     if (FAR) return;
@@ -212,16 +328,16 @@ __global__ void __launch_bounds__(THREADS, CTAS) norm_bwd_kernel(const NormArgs 
                     for (int i = 0; i < Q; ++i) {
                         float s = 0.f;
                         for (int g = 0; g < groups; ++g) s += place(which, k, n)[g * tpr * Q + i];
-                        part[which * p.D + c.at(k) + n * Q + i] = s;
+                        out[which * p.D + c.at(k) + n * Q + i] = s;
                     }
     }
 }
 
-template <typename TB, typename TS, typename TN, int VEC, int PER, int THREADS, int CTAS, int KIND, int GATE>
-lstm_status run(const NormArgs& a, const BwdShape& s, cudaStream_t cs)
+template <typename TB, typename TS, typename TN, int VEC, int PER, int R, int THREADS, int CTAS, int KIND, int GATE>
+lstm_status run(NormArgs& a, const BwdShape& s, cudaStream_t cs)
 {
     static std::atomic<uint64_t> ready{0};
-    auto* fn = norm_bwd_kernel<TB, TS, TN, VEC, PER, THREADS, CTAS, KIND, GATE>;
+    auto* fn = norm_bwd_kernel<TB, TS, TN, VEC, PER, R, THREADS, CTAS, KIND, GATE>;
     const size_t smem = PER * VEC > 16 ? 0 : sizeof(float) * kSums * PER * VEC * THREADS;
     int dev = 0;
     LSTM_CUDA_TRY(cudaGetDevice(&dev));
@@ -230,24 +346,29 @@ lstm_status run(const NormArgs& a, const BwdShape& s, cudaStream_t cs)
         LSTM_CUDA_TRY(cudaFuncSetAttribute((const void*)fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
         if (dev < 64) ready.fetch_or(bit, std::memory_order_release);
     }
+    // as many CTAs as stay resident
+    const int64_t rows = (a.rows + R - 1) / R, groups = s.threads / s.tpr;
+    a.parts = (int)std::min<int64_t>(a.parts, std::min<int64_t>((rows + groups - 1) / groups, (int64_t)kSMs * CTAS));
     fn<<<a.parts, s.threads, smem, cs>>>(a, s.tpr);
     return cudaGetLastError() == cudaSuccess ? LSTM_OK : LSTM_ERR_CUDA;
 }
 
 // A whole block of one kind and gate, by types: y's, x's (dn has y's).
-template <int KIND, int GATE, typename TB, typename TS> lstm_status run_block(const NormArgs& a, const BwdShape& s, cudaStream_t cs)
+template <int KIND, int GATE, typename TB, typename TS> lstm_status run_block(NormArgs& a, const BwdShape& s, cudaStream_t cs)
 {
+    // rows of 2-byte values two at a time
+    constexpr int R = sizeof(TB) + sizeof(TS) == 4 ? 2 : 1;
     if (norm_whole(a)) {
-        if (s.threads <= 128) return run<TB, TS, TB, 8, 1, 128, 6, KIND, GATE>(a, s, cs);
-        if (s.threads <= 256) return run<TB, TS, TB, 8, 1, 256, 3, KIND, GATE>(a, s, cs);
-        return run<TB, TS, TB, 8, 1, 512, 1, KIND, GATE>(a, s, cs);
+        if (s.threads <= 128) return run<TB, TS, TB, 8, 1, R, 128, R == 2 ? 4 : 6, KIND, GATE>(a, s, cs);
+        if (s.threads <= 256) return run<TB, TS, TB, 8, 1, R, 256, R == 2 ? 2 : 3, KIND, GATE>(a, s, cs);
+        return run<TB, TS, TB, 8, 1, R, 512, 1, KIND, GATE>(a, s, cs);
     }
-    if (s.threads <= 128) return run<TB, TS, TB, 1, 8, 128, 6, KIND, GATE>(a, s, cs);
-    if (s.threads <= 256) return run<TB, TS, TB, 1, 8, 256, 3, KIND, GATE>(a, s, cs);
-    return run<TB, TS, TB, 1, 8, 512, 1, KIND, GATE>(a, s, cs);
+    if (s.threads <= 128) return run<TB, TS, TB, 1, 8, 1, 128, 6, KIND, GATE>(a, s, cs);
+    if (s.threads <= 256) return run<TB, TS, TB, 1, 8, 1, 256, 3, KIND, GATE>(a, s, cs);
+    return run<TB, TS, TB, 1, 8, 1, 512, 1, KIND, GATE>(a, s, cs);
 }
 
-template <int GATE> lstm_status run_gate(const NormArgs& a, const BwdShape& s, cudaStream_t cs)
+template <int GATE> lstm_status run_gate(NormArgs& a, const BwdShape& s, cudaStream_t cs)
 {
     typedef __nv_bfloat16 H;
     const bool rms = a.post == LSTM_NORM_RMS;
@@ -259,8 +380,8 @@ template <int GATE> lstm_status run_gate(const NormArgs& a, const BwdShape& s, c
 }  // namespace
 
 // One translation unit a gate.
-lstm_status norm_bwd_none(const NormArgs& a, const BwdShape& s, cudaStream_t cs);
-lstm_status norm_bwd_sigmoid(const NormArgs& a, const BwdShape& s, cudaStream_t cs);
-lstm_status norm_bwd_silu(const NormArgs& a, const BwdShape& s, cudaStream_t cs);
+lstm_status norm_bwd_none(NormArgs& a, const BwdShape& s, cudaStream_t cs);
+lstm_status norm_bwd_sigmoid(NormArgs& a, const BwdShape& s, cudaStream_t cs);
+lstm_status norm_bwd_silu(NormArgs& a, const BwdShape& s, cudaStream_t cs);
 
 }  // namespace lstm

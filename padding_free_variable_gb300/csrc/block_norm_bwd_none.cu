@@ -3,6 +3,6 @@
 
 namespace lstm {
 
-lstm_status norm_bwd_none(const NormArgs& a, const BwdShape& s, cudaStream_t cs) { return run_gate<LSTM_GATE_NONE>(a, s, cs); }
+lstm_status norm_bwd_none(NormArgs& a, const BwdShape& s, cudaStream_t cs) { return run_gate<LSTM_GATE_NONE>(a, s, cs); }
 
 }  // namespace lstm

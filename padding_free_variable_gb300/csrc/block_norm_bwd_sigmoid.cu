@@ -3,6 +3,6 @@
 
 namespace lstm {
 
-lstm_status norm_bwd_sigmoid(const NormArgs& a, const BwdShape& s, cudaStream_t cs) { return run_gate<LSTM_GATE_SIGMOID>(a, s, cs); }
+lstm_status norm_bwd_sigmoid(NormArgs& a, const BwdShape& s, cudaStream_t cs) { return run_gate<LSTM_GATE_SIGMOID>(a, s, cs); }
 
 }  // namespace lstm

@@ -3,6 +3,6 @@
 
 namespace lstm {
 
-lstm_status norm_bwd_silu(const NormArgs& a, const BwdShape& s, cudaStream_t cs) { return run_gate<LSTM_GATE_SILU>(a, s, cs); }
+lstm_status norm_bwd_silu(NormArgs& a, const BwdShape& s, cudaStream_t cs) { return run_gate<LSTM_GATE_SILU>(a, s, cs); }
 
 }  // namespace lstm

@@ -23,7 +23,7 @@ __global__ void __launch_bounds__(512) norm_fwd_kernel(const NormArgs p, const i
     const bool S16 = std::is_same<TS, Any>::value ? p.stream16 : sizeof(TS) == 2;
     const bool B16 = std::is_same<TB, Any>::value ? p.branch16 : sizeof(TB) == 2;
     const bool N16 = KIND ? B16 : p.norm16;
-    __shared__ float2 s_part[2 * 32];
+    __shared__ float s_part[2 * 64];
     const int64_t r = tpr == 32 ? blockIdx.x * (int64_t)(blockDim.x / 32) + threadIdx.x / 32 : blockIdx.x;
     if (r >= p.rows) return;
     const Cols<VEC, PER> c{(int)threadIdx.x % tpr, tpr, p.D};
@@ -50,7 +50,7 @@ __global__ void __launch_bounds__(512) norm_fwd_kernel(const NormArgs p, const i
             for (int k = 0; k < PER; ++k)
 #pragma unroll
                 for (int v = 0; v < VEC; ++v) a += get_value(ry[k], v, B16);
-            my = sum(a, 0.f).x * inv;
+            my = sum(a) * inv;
             a = 0.f;
         }
 #pragma unroll
@@ -61,7 +61,7 @@ __global__ void __launch_bounds__(512) norm_fwd_kernel(const NormArgs p, const i
                     const float d = get_value(ry[k], v, B16) - my;
                     a = fmaf(d, d, a);
                 }
-        sy = 1.f / sqrtf(fmaf(sum(a, 0.f).x, inv, p.eps));
+        sy = 1.f / sqrtf(fmaf(sum(a), inv, p.eps));
     }
     float x1[PER][VEC];
 #pragma unroll
@@ -87,7 +87,7 @@ __global__ void __launch_bounds__(512) norm_fwd_kernel(const NormArgs p, const i
             for (int k = 0; k < PER; ++k)
 #pragma unroll
                 for (int v = 0; v < VEC; ++v) a += x1[k][v];
-            mx = sum(a, 0.f).x * inv;
+            mx = sum(a) * inv;
             a = 0.f;
         }
 #pragma unroll
@@ -98,7 +98,7 @@ __global__ void __launch_bounds__(512) norm_fwd_kernel(const NormArgs p, const i
                     const float d = x1[k][v] - mx;
                     a = fmaf(d, d, a);
                 }
-        sx = 1.f / sqrtf(fmaf(sum(a, 0.f).x, inv, p.eps));
+        sx = 1.f / sqrtf(fmaf(sum(a), inv, p.eps));
 #pragma unroll
         for (int k = 0; k < PER; ++k) {
             if (!c.has(k)) continue;
