@@ -65,14 +65,26 @@ bool norm_full(const NormArgs& a)
            layer == (a.w.b_pre != nullptr) && a.norm16 == a.branch16 && (a.branch16 || !a.stream16);
 }
 
-bool norm_whole(const NormArgs& a)
+static bool norm_aligned(const NormArgs& a)
 {
-    bool ok = a.D % 8 == 0 && a.ldy % 8 == 0 && a.ldg % 8 == 0 && a.lddy % 8 == 0 && a.lddg % 8 == 0;
+    bool ok = true;
     for (const void* p : {a.x, a.y, a.g, (const void*)a.x_out, (const void*)a.n, a.dx_out, a.dn, (const void*)a.dx,
                           (const void*)a.dy, (const void*)a.dg, (const void*)a.w.w_post, (const void*)a.w.b_post,
                           (const void*)a.w.scale, (const void*)a.w.w_pre, (const void*)a.w.b_pre})
         ok = ok && aligned(p, 16);
     return ok;
+}
+
+bool norm_whole(const NormArgs& a)
+{
+    return a.D % 8 == 0 && a.ldy % 8 == 0 && a.ldg % 8 == 0 && a.lddy % 8 == 0 && a.lddg % 8 == 0 && norm_aligned(a);
+}
+
+bool norm_shifted(const NormArgs& a)
+{
+    const int64_t D = a.D;
+    return norm_full(a) && a.D % 8 != 0 && (a.ldy - D) % 8 == 0 && (!a.g || (a.ldg - D) % 8 == 0) && (!a.dy || (a.lddy - D) % 8 == 0) &&
+           (!a.dg || (a.lddg - D) % 8 == 0) && norm_aligned(a);
 }
 
 }  // namespace lstm

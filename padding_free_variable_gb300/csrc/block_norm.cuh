@@ -36,11 +36,18 @@ struct NormArgs {
 };
 
 
-// Values of a thread: PER groups of VEC neighbours, the threads of a row next to each other in each group.
+// Values of a thread: PER groups of VEC neighbours, the threads of a row next to each other in each
+// group.  Rows of a width that no multiple of 8 divides start anywhere in memory: then a group is
+// 8 values from a multiple of 8 in memory, `shift` before the columns that a row on such a boundary
+// would give it, and its first and last group of a row reach into the neighbours.
 template <int VEC, int PER> struct Cols {
     int t, n, D;            // thread of the row, threads of a row, width
-    __device__ __forceinline__ int at(int k) const { return (k * n + t) * VEC; }
-    __device__ __forceinline__ bool has(int k) const { return at(k) < D; }
+    int shift = 0;
+    bool row = true;        // is there a row at all?
+    __device__ __forceinline__ int at(int k) const { return (k * n + t) * VEC - shift; }
+    __device__ __forceinline__ bool has(int k) const { return row && at(k) < D; }
+    __device__ __forceinline__ bool whole(int k) const { return at(k) >= 0 && at(k) + VEC <= D; }
+    __device__ __forceinline__ bool valid(int k, int v) const { return (unsigned)(at(k) + v) < (unsigned)D; }
 };
 
 // VEC values of one group as they lie in memory.
@@ -125,6 +132,28 @@ __device__ __forceinline__ void load_group(Group<T, VEC>& g, const void* base, i
     else if (own) g.load_own((const T*)base + at);
     else g.load((const T*)base + at);
 }
+// A group of shifted columns, the neighbours' values in it as 0 (whatever they are, NaN too, stays
+// theirs).  `inside`: all of it lies in the tensor; else value by value.
+template <typename T, int VEC, int PER>
+__device__ __forceinline__ void load_shifted(Group<T, VEC>& g, const void* base, int64_t row, const Cols<VEC, PER>& c, int k, bool inside, bool own = false)
+{
+    if (inside) {
+        load_group(g, base, row + c.at(k), sizeof(T) == 2, own);
+        if (c.whole(k)) return;
+#pragma unroll
+        for (int v = 0; v < VEC; ++v)
+            if (!c.valid(k, v)) ((unsigned*)g.w)[v * (int)sizeof(T) / 4] &= sizeof(T) == 4 ? 0u : v % 2 ? 0xffffu : 0xffff0000u;
+        return;
+    }
+    const T* p = (const T*)base + row + c.at(k);
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) {
+        unsigned x = 0;
+        if (c.valid(k, v)) x = sizeof(T) == 2 ? (unsigned)*(const unsigned short*)(p + v) : *(const unsigned*)(p + v);
+        unsigned& w = ((unsigned*)g.w)[v * (int)sizeof(T) / 4];
+        w = sizeof(T) == 4 ? x : v % 2 ? w | x << 16 : x;
+    }
+}
 template <typename T, int VEC> __device__ __forceinline__ float get_value(const Group<T, VEC>& g, int v, bool b16)
 {
     if constexpr (std::is_same<T, Any>::value) return g.get(v, b16);
@@ -152,6 +181,49 @@ template <int VEC> __device__ __forceinline__ void put_group(void* base, int64_t
     }
 }
 
+// The valid values of a shifted group, one by one at a row's ends.
+template <typename T, int VEC, int PER>
+__device__ __forceinline__ void put_shifted(T* base, int64_t row, const Cols<VEC, PER>& c, int k, const float (&x)[VEC])
+{
+    if (c.whole(k)) {
+        put_group<VEC>(base, row + c.at(k), sizeof(T) == 2, x);
+        return;
+    }
+#pragma unroll
+    for (int v = 0; v < VEC; ++v)
+        if (c.valid(k, v)) base[row + c.at(k) + v] = from_f32<T>(x[v]);
+}
+
+// A thread's own parameters in shared memory, four neighbours at a time, the threads' next to each
+// other: for shifted columns, which no vector load of the parameters fits; 0 beyond a row's ends.
+template <int VEC, int PER> struct OwnParams {
+    float4* s;
+    static constexpr int bytes(int count, int threads) { return count * PER * VEC * 4 * threads; }
+    __device__ __forceinline__ float4* place(int which, int k, int n) const { return s + ((which * PER + k) * (VEC / 4) + n) * blockDim.x + threadIdx.x; }
+    template <typename V> __device__ __forceinline__ void fill(int which, const Cols<VEC, PER>& c, V&& value) const
+    {
+#pragma unroll
+        for (int k = 0; k < PER; ++k)
+#pragma unroll
+            for (int n = 0; n < VEC / 4; ++n) {
+                float x[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) x[i] = c.valid(k, n * 4 + i) ? value(c.at(k) + n * 4 + i) : 0.f;
+                *place(which, k, n) = make_float4(x[0], x[1], x[2], x[3]);
+            }
+    }
+    template <int Q> __device__ __forceinline__ void get(int which, int k, int n, float (&v)[Q]) const
+    {
+#pragma unroll
+        for (int i = 0; i < Q; i += 4) {
+            const float4 q = *place(which, k, n + i / 4);
+            v[i] = q.x; v[i + 1] = q.y; v[i + 2] = q.z; v[i + 3] = q.w;
+        }
+    }
+};
+// Rows that one thread takes one after another are a multiple of 8 apart, so that their columns are shifted alike.
+inline int64_t shifted_blocks(int64_t blocks) { return (blocks + 7) / 8 * 8; }
+
 // VEC parameters, or `none` where there are no such parameters.
 // GIVEN: known to be there; EVER: such a kind has them at all.
 template <int VEC, bool GIVEN = false, bool EVER = true>
@@ -175,15 +247,17 @@ __device__ __forceinline__ void get_params(const float* p, int at, float none, f
 // row a CTA) through shared memory, each use on the other half so that one barrier suffices.
 struct RowSum {
     float* part;            // [2][16][4]
-    int warps, half;
+    int lanes, half;        // threads of a row: a power of two up to 32, or whole warps
     template <int N> __device__ __forceinline__ void operator()(float (&v)[N])
     {
         static_assert(N <= 4, "four sums at a time");
 #pragma unroll
         for (int o = 16; o; o >>= 1)
+            if (o < lanes)
 #pragma unroll
-            for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
-        if (warps == 1) return;
+                for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+        if (lanes <= 32) return;
+        const int warps = lanes / 32;
         float* s = part + half * 64;
         half ^= 1;
         if (threadIdx.x % 32 == 0)
@@ -223,8 +297,12 @@ __device__ __forceinline__ float activation(int kind, float q)
 
 // A whole block: both norms of one kind with all that this kind has, types among those with kernels of their own.
 bool norm_full(const NormArgs& a);
-// Rows, pointers and widths allow groups of eight.
+// Rows, pointers and widths allow groups of eight; the same for shifted ones (rows that all start
+// equally far from a multiple of 8 values).
 bool norm_whole(const NormArgs& a);
+bool norm_shifted(const NormArgs& a);
+// Threads of a row of `groups` groups: 4, 8, 16 or whole warps.
+inline int row_threads(int groups) { return groups <= 4 ? 4 : groups <= 8 ? 8 : groups <= 16 ? 16 : (groups + 31) / 32 * 32; }
 int norm_parts(int64_t rows, int D);
 lstm_status launch_norm_fwd(const NormArgs& a, cudaStream_t cs);
 lstm_status launch_norm_bwd(NormArgs a, cudaStream_t cs);

@@ -45,7 +45,7 @@ int norm_parts(int64_t rows, int D)
 {
     const BwdShape s = bwd_shape(D);
     const int64_t groups = s.threads / s.tpr;
-    return (int)std::min<int64_t>((rows + groups - 1) / groups, (int64_t)kSMs * s.ctas);
+    return (int)shifted_blocks(std::min<int64_t>((rows + groups - 1) / groups, (int64_t)kSMs * s.ctas));
 }
 
 lstm_status launch_norm_bwd(NormArgs a, cudaStream_t cs)

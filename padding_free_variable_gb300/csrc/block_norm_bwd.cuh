@@ -23,19 +23,20 @@ struct BwdShape {
     int per, tpr, threads, ctas;        // values of a thread / 8, threads of a row and of a CTA, CTAs an SM
 };
 
-// Eight values a thread while a row then fits a CTA of 512.
+// Eight values a thread while a row then fits a CTA of 512.  (7 columns more than a row has: shifted
+// rows may need a group more.)
 constexpr int kSMs = 152;
 
 inline BwdShape bwd_shape(int D)
 {
     BwdShape s;
-    s.per = D <= 4096 ? 1 : D <= 8192 ? 2 : 4;
-    s.tpr = (ceil_div(D, 8 * s.per) + 31) / 32 * 32;
-    s.threads = s.tpr == 32 ? 128 : s.tpr;
+    const int wide = D % 8 && D + 7 <= 4096 ? D + 7 : D;
+    s.per = wide <= 4096 ? 1 : wide <= 8192 ? 2 : 4;
+    s.tpr = row_threads(ceil_div(wide, 8 * s.per));
+    s.threads = s.tpr <= 32 ? 128 : s.tpr;
     s.ctas = s.threads <= 128 ? 6 : s.threads <= 256 ? 3 : 1;
     return s;
 }
-
 
 namespace {
 
@@ -65,6 +66,19 @@ template <typename X> __device__ __forceinline__ X pick(const float* v, int i)
     else return F2(v[i], v[i + 1]);
 }
 
+// Q neighbouring values of a shifted group.
+template <typename T, int VEC, int PER, int Q>
+__device__ __forceinline__ void put_piece(T* base, int64_t row, const Cols<VEC, PER>& c, int k, int n, const float (&x)[Q])
+{
+    if (c.whole(k)) {
+        put_group<Q>(base, row + c.at(k) + n * Q, sizeof(T) == 2, x);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < Q; ++i)
+        if (c.valid(k, n * Q + i)) base[row + c.at(k) + n * Q + i] = from_f32<T>(x[i]);
+}
+
 // Means over a row of t xh (m1) and, for centred norms, of t (m0); sums: R of the one, R of the other.
 template <int R> __device__ __forceinline__ void row_means(RowSum& sum, float (&sums)[2 * R], bool centred, float inv, float (&m0)[R], float (&m1)[R])
 {
@@ -86,7 +100,7 @@ template <int R> __device__ __forceinline__ void row_means(RowSum& sum, float (&
 }
 
 // One warp a row (four rows a CTA) up to 256 columns, one CTA a row beyond.
-template <typename TB, typename TS, typename TN, int VEC, int PER, int R, int THREADS, int CTAS, int KIND, int GATE>
+template <typename TB, typename TS, typename TN, int VEC, int PER, int R, int THREADS, int CTAS, int KIND, int GATE, bool SHIFT>
 __global__ void __launch_bounds__(THREADS, CTAS) norm_bwd_kernel(const NormArgs p, const int tpr)
 {
     // KIND: LSTM_NORM_RMS (no biases) or LSTM_NORM_LAYER (biases), a whole block with everything
@@ -107,8 +121,8 @@ __global__ void __launch_bounds__(THREADS, CTAS) norm_bwd_kernel(const NormArgs 
     extern __shared__ __align__(16) float s_sums[];         // [kSums][PER * N][THREADS][Q]
     const int groups = blockDim.x / tpr, group = threadIdx.x / tpr;
     // R rows at a time: the parameters are read and their sums updated once for them
-    const Cols<VEC, PER> c{(int)threadIdx.x % tpr, tpr, p.D};
-    RowSum sum{s_part, tpr / 32, 0};
+    Cols<VEC, PER> c{(int)threadIdx.x % tpr, tpr, p.D};
+    RowSum sum{s_part, tpr, 0};
     const float inv = 1.f / (float)p.D;
     float* const out = p.part + (int64_t)blockIdx.x * kSums * p.D;
     auto place = [&](int which, int k, int n) {
@@ -124,6 +138,18 @@ __global__ void __launch_bounds__(THREADS, CTAS) norm_bwd_kernel(const NormArgs 
             *(float4*)at = q;
         }
     };
+    // shifted columns' parameters, after the sums: w_post, scale, w_pre (1, b_post)
+    const OwnParams<SHIFT ? VEC : 4, PER> own{(float4*)(s_sums + kSums * PER * VEC * THREADS)};
+    if constexpr (SHIFT) {
+        c.shift = (int)((blockIdx.x * (uint64_t)groups + group) * (unsigned)p.D & 7u);
+        own.fill(0, c, [&](int i) { return p.w.w_post[i]; });
+        own.fill(1, c, [&](int i) { return p.w.scale[i]; });
+        own.fill(2, c, [&](int i) { return p.w.w_pre[i]; });
+        if (BIAS) {
+            own.fill(3, c, [](int) { return 1.f; });
+            own.fill(4, c, [&](int i) { return p.w.b_post[i]; });
+        }
+    }
     for (int which = 0; which < kSums; ++which)
 #pragma unroll
         for (int k = 0; k < PER; ++k)
@@ -132,17 +158,28 @@ __global__ void __launch_bounds__(THREADS, CTAS) norm_bwd_kernel(const NormArgs 
                 for (int n = 0; n < N; ++n)
 #pragma unroll
                     for (int i = 0; i < Q; ++i) place(which, k, n)[i] = 0.f;
+    auto params = [&](int k, int n, int which, const float* from, bool ever, float none, float (&v)[Q]) {
+        if (SHIFT && ever) {
+            if constexpr (SHIFT) own.get(which, k, n, v);
+        } else if (ever) {
+            get_params<Q, GIVEN>(from, c.at(k) + n * Q, none, v);
+        } else {
+            get_params<Q, false, false>(from, 0, none, v);
+        }
+    };
 
-    for (int64_t r0 = (blockIdx.x * (int64_t)groups + group) * R; r0 < p.rows; r0 += (int64_t)gridDim.x * groups * R) {
+    const int64_t step = (int64_t)gridDim.x * groups;           // the R rows lie this far apart
+    for (int64_t base = blockIdx.x * (int64_t)groups; base < p.rows; base += step * R) {
+        const int64_t r0 = base + group;
         Group<TS, VEC> rx[R][PER], rd[R][PER];
         Group<TB, VEC> ry[R][PER], rg[R][PER];
         Group<TN, VEC> rn[R][PER];
         float my[R], sy[R], mx[R], sx[R];
 #pragma unroll
         for (int q = 0; q < R; ++q) {
-            // a last row without a partner: zeros, which add nothing and are not written
-            const bool row = q == 0 || r0 + q < p.rows;
-            const int64_t r = row ? r0 + q : r0;
+            // past the last row: zeros, which add nothing and are not written
+            const bool row = r0 + q * step < p.rows;
+            const int64_t r = row ? r0 + q * step : p.rows - 1;
 #pragma unroll
             for (int k = 0; k < PER; ++k) {
                 rx[q][k].zero();
@@ -151,6 +188,15 @@ __global__ void __launch_bounds__(THREADS, CTAS) norm_bwd_kernel(const NormArgs 
                 rg[q][k].zero();
                 rn[q][k].zero();
                 if (!c.has(k) || !row) continue;
+                if constexpr (SHIFT) {
+                    const bool inside = c.whole(k) || r < p.rows - 1;
+                    load_shifted(rx[q][k], p.x, r * p.D, c, k, inside);
+                    load_shifted(ry[q][k], p.y, r * p.ldy, c, k, inside);
+                    if (gate) load_shifted(rg[q][k], p.g, r * p.ldg, c, k, inside);
+                    load_shifted(rn[q][k], p.dn, r * p.D, c, k, inside);
+                    load_shifted(rd[q][k], p.dx_out, r * p.D, c, k, inside, true);
+                    continue;
+                }
                 load_group(rx[q][k], p.x, r * p.D + c.at(k), S16);
                 if (has_y) load_group(ry[q][k], p.y, r * p.ldy + c.at(k), B16);
                 if (gate) load_group(rg[q][k], p.g, r * p.ldg + c.at(k), B16);
@@ -172,17 +218,17 @@ __global__ void __launch_bounds__(THREADS, CTAS) norm_bwd_kernel(const NormArgs 
         for (int k = 0; k < PER; ++k)
 #pragma unroll
             for (int n = 0; n < N; ++n) {
-                float wq[Q], bq[Q], s[Q], wp[Q];
+                float wq[Q], bq[Q], s[Q], wp[Q], in[Q];
 #pragma unroll
                 for (int q = 0; q < R; ++q)
 #pragma unroll
                     for (int i = n * Q / P; i < (n + 1) * Q / P; ++i) xh[q][k][i] = t[q][k][i] = both<X>(0.f);
                 if (!c.has(k)) continue;
-                const int at = c.at(k) + n * Q;
-                get_params<Q, GIVEN>(p.w.w_post, at, 1.f, wq);
-                get_params<Q, GIVEN, BIAS>(p.w.b_post, at, 0.f, bq);
-                get_params<Q, GIVEN>(p.w.scale, at, 1.f, s);
-                get_params<Q, GIVEN>(p.w.w_pre, at, 1.f, wp);
+                params(k, n, 0, p.w.w_post, true, 1.f, wq);
+                params(k, n, 4, p.w.b_post, BIAS, 0.f, bq);
+                params(k, n, 3, nullptr, SHIFT && CENTRED, 1.f, in);
+                params(k, n, 1, p.w.scale, true, 1.f, s);
+                params(k, n, 2, p.w.w_pre, true, 1.f, wp);
 #pragma unroll
                 for (int q = 0; q < R; ++q)
 #pragma unroll
@@ -202,7 +248,10 @@ __global__ void __launch_bounds__(THREADS, CTAS) norm_bwd_kernel(const NormArgs 
                             x1 = x1 + u;
                         }
                         if (CENTRED) x1 = x1 + both<X>(-mx[q]);
-                        const X h = x1 * both<X>(sx[q]), e = values<X>(rn[q][k], v, N16) * pick<X>(wp, i);
+                        X h = x1 * both<X>(sx[q]);
+                        const X e = values<X>(rn[q][k], v, N16) * pick<X>(wp, i);
+                        // (zeros beyond a row's ends stay zeros unless a mean is taken off)
+                        if (SHIFT && CENTRED) h = h * pick<X>(in, i);
                         xh[q][k][v / P] = h;
                         t[q][k][v / P] = e;
                         part[q] = fma2(e, h, part[q]);
@@ -221,20 +270,20 @@ __global__ void __launch_bounds__(THREADS, CTAS) norm_bwd_kernel(const NormArgs 
 #pragma unroll
             for (int n = 0; n < N; ++n) {
                 if (!c.has(k)) continue;
-                float wq[Q], bq[Q], s[Q];
+                float wq[Q], bq[Q], s[Q], in[Q];
                 X a[kSums][Q / P];      // the parameters' gradients' terms of these rows
-                const int at = c.at(k) + n * Q;
-                get_params<Q, GIVEN>(p.w.w_post, at, 1.f, wq);
-                get_params<Q, GIVEN, BIAS>(p.w.b_post, at, 0.f, bq);
-                get_params<Q, GIVEN>(p.w.scale, at, 1.f, s);
+                params(k, n, 0, p.w.w_post, true, 1.f, wq);
+                params(k, n, 4, p.w.b_post, BIAS, 0.f, bq);
+                params(k, n, 3, nullptr, SHIFT && CENTRED, 1.f, in);
+                params(k, n, 1, p.w.scale, true, 1.f, s);
 #pragma unroll
                 for (int which = 0; which < kSums; ++which)
 #pragma unroll
                     for (int i = 0; i < Q / P; ++i) a[which][i] = both<X>(0.f);
 #pragma unroll
                 for (int q = 0; q < R; ++q) {
-                    const bool row = q == 0 || r0 + q < p.rows;
-                    const int64_t r = r0 + q;
+                    const int64_t r = r0 + q * step;
+                    const bool row = r < p.rows;
                     float dx[Q], dg[Q];
 #pragma unroll
                     for (int i = 0; i < Q; i += P) {
@@ -246,6 +295,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) norm_bwd_kernel(const NormArgs 
                             if (CENTRED) x = x + both<X>(-m0[q]);
                             d = fma2(x, both<X>(sx[q]), d);
                         }
+                        if (SHIFT && CENTRED) d = d * pick<X>(in, i);
                         a[3][i / P] = fma2(e, h, a[3][i / P]);
                         a[4][i / P] = a[4][i / P] + e;
                         spread(d, dx + i);
@@ -276,8 +326,14 @@ __global__ void __launch_bounds__(THREADS, CTAS) norm_bwd_kernel(const NormArgs 
                         a[1][i / P] = a[1][i / P] + dv;
                         a[2][i / P] = fma2(d, ua, a[2][i / P]);
                     }
-                    if (row) put_group<Q>(p.dx, r * p.D + at, S16, dx);
-                    if (gate && row) put_group<Q>(p.dg, r * p.lddg + at, B16, dg);
+                    if (!row) continue;
+                    if constexpr (SHIFT) {
+                        put_piece((TS*)p.dx, r * p.D, c, k, n, dx);
+                        if (gate) put_piece((TB*)p.dg, r * p.lddg, c, k, n, dg);
+                    } else {
+                        put_group<Q>(p.dx, r * p.D + c.at(k) + n * Q, S16, dx);
+                        if (gate) put_group<Q>(p.dg, r * p.lddg + c.at(k) + n * Q, B16, dg);
+                    }
                 }
 #pragma unroll
                 for (int which = 0; which < kSums; ++which)
@@ -294,7 +350,8 @@ __global__ void __launch_bounds__(THREADS, CTAS) norm_bwd_kernel(const NormArgs 
         if (post) row_means(sum, sums, post == LSTM_NORM_LAYER, inv, m0, m1);
 #pragma unroll
         for (int q = 0; q < R; ++q) {
-            if (q > 0 && r0 + q >= p.rows) continue;
+            const int64_t r = r0 + q * step;
+            if (r >= p.rows) continue;
 #pragma unroll
             for (int k = 0; k < PER; ++k) {
                 if (!c.has(k)) continue;
@@ -309,13 +366,27 @@ __global__ void __launch_bounds__(THREADS, CTAS) norm_bwd_kernel(const NormArgs 
                     }
                     spread(d, dy + v);
                 }
-                put_group<VEC>(p.dy, (r0 + q) * p.lddy + c.at(k), B16, dy);
+                if constexpr (SHIFT) put_shifted((TB*)p.dy, r * p.lddy, c, k, dy);
+                else put_group<VEC>(p.dy, r * p.lddy + c.at(k), B16, dy);
             }
         }
     }
     if (FAR) return;
     // this CTA's sums, its rows' groups added in order
     __syncthreads();
+    if constexpr (SHIFT) {      // the groups' columns are shifted differently: by column
+        for (int which = 0; which < kSums; ++which)
+            for (int i = threadIdx.x; wants(which) && i < p.D; i += blockDim.x) {
+                float s = 0.f;
+                for (int g = 0; g < groups; ++g) {
+                    const int shift = (int)((blockIdx.x * (uint64_t)groups + g) * (unsigned)p.D & 7u), at = i + shift;
+                    const int n = at % VEC / Q, t = at / VEC;
+                    s += s_sums[((which * N + n) * THREADS + g * tpr + t) * Q + at % Q];
+                }
+                out[which * p.D + i] = s;
+            }
+        return;
+    }
     if (group > 0) return;
     for (int which = 0; which < kSums; ++which) {
         if (!wants(which)) continue;
@@ -333,12 +404,14 @@ __global__ void __launch_bounds__(THREADS, CTAS) norm_bwd_kernel(const NormArgs 
     }
 }
 
-template <typename TB, typename TS, typename TN, int VEC, int PER, int R, int THREADS, int CTAS, int KIND, int GATE>
+template <typename TB, typename TS, typename TN, int VEC, int PER, int R, int THREADS, int CTAS, int KIND, int GATE, bool SHIFT = false>
 lstm_status run(NormArgs& a, const BwdShape& s, cudaStream_t cs)
 {
     static std::atomic<uint64_t> ready{0};
-    auto* fn = norm_bwd_kernel<TB, TS, TN, VEC, PER, R, THREADS, CTAS, KIND, GATE>;
-    const size_t smem = PER * VEC > 16 ? 0 : sizeof(float) * kSums * PER * VEC * THREADS;
+    auto* fn = norm_bwd_kernel<TB, TS, TN, VEC, PER, R, THREADS, CTAS, KIND, GATE, SHIFT>;
+    const int64_t groups = s.threads / s.tpr;
+    constexpr size_t SUMS = PER * VEC > 16 ? 0 : sizeof(float) * kSums * PER * VEC * THREADS;
+    constexpr size_t smem = SUMS + (SHIFT ? sizeof(float) * 5 * PER * VEC * THREADS : 0);
     int dev = 0;
     LSTM_CUDA_TRY(cudaGetDevice(&dev));
     const uint64_t bit = 1ull << (dev & 63);
@@ -347,8 +420,9 @@ lstm_status run(NormArgs& a, const BwdShape& s, cudaStream_t cs)
         if (dev < 64) ready.fetch_or(bit, std::memory_order_release);
     }
     // as many CTAs as stay resident
-    const int64_t rows = (a.rows + R - 1) / R, groups = s.threads / s.tpr;
+    const int64_t rows = (a.rows + R - 1) / R;
     a.parts = (int)std::min<int64_t>(a.parts, std::min<int64_t>((rows + groups - 1) / groups, (int64_t)kSMs * CTAS));
+    if (SHIFT) a.parts = (int)shifted_blocks(a.parts);
     fn<<<a.parts, s.threads, smem, cs>>>(a, s.tpr);
     return cudaGetLastError() == cudaSuccess ? LSTM_OK : LSTM_ERR_CUDA;
 }
@@ -362,6 +436,11 @@ template <int KIND, int GATE, typename TB, typename TS> lstm_status run_block(No
         if (s.threads <= 128) return run<TB, TS, TB, 8, 1, R, 128, R == 2 ? 4 : 6, KIND, GATE>(a, s, cs);
         if (s.threads <= 256) return run<TB, TS, TB, 8, 1, R, 256, R == 2 ? 2 : 3, KIND, GATE>(a, s, cs);
         return run<TB, TS, TB, 8, 1, R, 512, 1, KIND, GATE>(a, s, cs);
+    }
+    if (norm_shifted(a) && a.D + 7 <= 4096) {
+        if (s.threads <= 128) return run<TB, TS, TB, 8, 1, 1, 128, 5, KIND, GATE, true>(a, s, cs);
+        if (s.threads <= 256) return run<TB, TS, TB, 8, 1, 1, 256, 3, KIND, GATE, true>(a, s, cs);
+        return run<TB, TS, TB, 8, 1, 1, 512, 1, KIND, GATE, true>(a, s, cs);
     }
     if (s.threads <= 128) return run<TB, TS, TB, 1, 8, 1, 128, 6, KIND, GATE>(a, s, cs);
     if (s.threads <= 256) return run<TB, TS, TB, 1, 8, 1, 256, 3, KIND, GATE>(a, s, cs);
