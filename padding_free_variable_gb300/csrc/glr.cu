@@ -10,32 +10,67 @@ namespace lstm {
 
 namespace {
 
-template <typename T, bool GATED>
-__global__ void glr_step_kernel(const GlrArgs p, const int32_t* slots, int rows, int num_slots, const float* state_in,
-                                float* state_out)
+// V units of a stream a thread; threads of a block: x along the units, y along the streams.  Bound
+// by memory: gates and states read once, states and outputs written once.
+template <typename T, bool GATED, int V>
+__global__ void __launch_bounds__(128) glr_step_kernel(const GlrArgs p, const int32_t* slots, int rows, int num_slots, const float* state_in,
+                                                       float* state_out)
 {
-    const int64_t n = (int64_t)rows * p.H;
-    for (int64_t k = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; k < n; k += (int64_t)gridDim.x * blockDim.x) {
-        const int64_t r = k / p.H;
-        const int u = (int)(k - r * p.H);
-        const int slot = slots ? slots[r] : (int)r;
-        float h = 0.f;
+    typedef typename std::conditional<V * sizeof(T) == 16, uint4, T>::type Bits;
+    union G { Bits b; T e[V]; __device__ G() {} };
+    const int u = (blockIdx.x * blockDim.x + threadIdx.x) * V;
+    if (u >= p.H) return;
+    for (int64_t r = blockIdx.y * (int64_t)blockDim.y + threadIdx.y; r < rows; r += (int64_t)gridDim.y * blockDim.y) {
+        const int slot = slots ? __ldg(slots + r) : (int)r;
+        G f, z, g, out;
+        float h[V];
+        const int64_t at = r * p.ld + u, state = (int64_t)slot * p.H + u;
         if (slot >= 0 && slot < num_slots) {
-            const int64_t at = r * p.ld + u;
-            float a, b;
-            sigmoid_pair(to_f32(((const T*)p.f)[at]), a, b);
-            if (GATED) {
-                float c;
-                sigmoid_pair(to_f32(((const T*)p.i)[at]), b, c);
+            f.b = *(const Bits*)((const T*)p.f + at);
+            z.b = *(const Bits*)((const T*)p.z + at);
+            if (GATED) g.b = *(const Bits*)((const T*)p.i + at);
+            if constexpr (V % 4 == 0) {
+#pragma unroll
+                for (int v = 0; v < V; v += 4) {
+                    const float4 q = *(const float4*)(state_in + state + v);
+                    h[v] = q.x; h[v + 1] = q.y; h[v + 2] = q.z; h[v + 3] = q.w;
+                }
+            } else {
+                h[0] = state_in[state];
             }
-            h = fmaf(a, state_in[(int64_t)slot * p.H + u], b * to_f32(((const T*)p.z)[at]));
-            state_out[(int64_t)slot * p.H + u] = h;
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                float a, b;
+                sigmoid_pair(to_f32(f.e[v]), a, b);
+                if (GATED) b = rcp_approx(1.f + ex2_approx(to_f32(g.e[v]) * kNegLog2e));
+                h[v] = fmaf(a, h[v], b * to_f32(z.e[v]));
+            }
+            if constexpr (V % 4 == 0) {
+#pragma unroll
+                for (int v = 0; v < V; v += 4) *(float4*)(state_out + state + v) = make_float4(h[v], h[v + 1], h[v + 2], h[v + 3]);
+            } else {
+                state_out[state] = h[0];
+            }
+        } else {
+#pragma unroll
+            for (int v = 0; v < V; ++v) h[v] = 0.f;
         }
-        ((T*)p.y)[k] = from_f32<T>(h);
+#pragma unroll
+        for (int v = 0; v < V; ++v) out.e[v] = from_f32<T>(h[v]);
+        *(Bits*)((T*)p.y + r * p.H + u) = out.b;
     }
 }
 
-lstm_status launched() { return cudaGetLastError() == cudaSuccess ? LSTM_OK : LSTM_ERR_CUDA; }
+template <typename T, bool GATED, int V>
+lstm_status step(const GlrArgs& a, const int32_t* slots, int rows, int num_slots, const float* in, float* out, cudaStream_t cs)
+{
+    const int along = ceil_div(a.H, V);
+    int x = 1;
+    while (x < 128 && x < along) x *= 2;
+    const dim3 block(x, 128 / x), grid(ceil_div(along, x), (unsigned)std::min<int64_t>(((int64_t)rows + block.y - 1) / block.y, 65535));
+    glr_step_kernel<T, GATED, V><<<grid, block, 0, cs>>>(a, slots, rows, num_slots, in, out);
+    return cudaGetLastError() == cudaSuccess ? LSTM_OK : LSTM_ERR_CUDA;
+}
 
 lstm_status check_glr_shape(const lstm_glr_shape* s)
 {
@@ -99,20 +134,22 @@ lstm_status pass_through(const float* in, float* out, size_t bytes, cudaStream_t
 
 }  // namespace
 
+// Every row of every operand starts on a multiple of `bytes`, and so does its length.
+static bool glr_whole(const GlrArgs& a, int elem, int64_t bytes)
+{
+    bool ok = true;
+    for (int64_t n : {(int64_t)a.H, a.ld, a.ndir == 1 ? 0 : a.dstride, a.gld, a.ndir == 1 ? 0 : a.gdstride})
+        ok = ok && n * elem % bytes == 0;
+    for (const void* p : {a.f, a.z, a.i, (const void*)a.y, a.dy, (const void*)a.df, (const void*)a.dz, (const void*)a.di})
+        ok = ok && fits(p, bytes);
+    return ok;
+}
+
 GlrRows glr_rows(const GlrArgs& a, int elem)
 {
-    // every row of every operand starts on a multiple of `bytes`, and so does its length
-    auto whole = [&](int64_t bytes) {
-        bool ok = true;
-        for (int64_t n : {(int64_t)a.H, a.ld, a.ndir == 1 ? 0 : a.dstride, a.gld, a.ndir == 1 ? 0 : a.gdstride})
-            ok = ok && n * elem % bytes == 0;
-        for (const void* p : {a.f, a.z, a.i, (const void*)a.y, a.dy, (const void*)a.df, (const void*)a.dz, (const void*)a.di})
-            ok = ok && fits(p, bytes);
-        return ok;
-    };
     // fp32 rows of at most 32 units fill a warp with one unit a lane
-    if (whole(16) && (elem == 2 || a.H > 32)) return GLR_WIDE;
-    return whole(4) ? GLR_NARROW : GLR_SINGLE;
+    if (glr_whole(a, elem, 16) && (elem == 2 || a.H > 32)) return GLR_WIDE;
+    return glr_whole(a, elem, 4) ? GLR_NARROW : GLR_SINGLE;
 }
 
 void glr_cut(const Plan& p, int V, int ctas, void* scratch, GlrArgs* a)
@@ -218,13 +255,16 @@ lstm_status lstm_glr_step(const lstm_glr_shape* shape, const lstm_glr_gates* gat
     GlrArgs a;
     a.H = s.hidden_size;
     a.f = gates->f; a.z = gates->z; a.i = gates->i; a.ld = gates->row_stride; a.y = y;
-    const int64_t n = (int64_t)rows * s.hidden_size;
-    const unsigned grid = (unsigned)std::min<int64_t>((n + 255) / 256, 65535);
+    const bool whole = fits(state_in, 16) && fits(state_out, 16) && glr_whole(a, s.dtype == LSTM_BF16 ? 2 : 4, 16);
+    lstm_status st2 = LSTM_OK;
     dispatch(s, [&](auto* t, auto gated) {
-        glr_step_kernel<std::remove_pointer_t<decltype(t)>, decltype(gated)::value>
-            <<<grid, 256, 0, (cudaStream_t)stream>>>(a, slots, rows, num_slots, state_in, state_out);
+        typedef std::remove_pointer_t<decltype(t)> T;
+        constexpr bool G = decltype(gated)::value;
+        cudaStream_t cs = (cudaStream_t)stream;
+        st2 = whole ? step<T, G, 16 / (int)sizeof(T)>(a, slots, rows, num_slots, state_in, state_out, cs)
+                    : step<T, G, 1>(a, slots, rows, num_slots, state_in, state_out, cs);
     });
-    return launched();
+    return st2;
 }
 
 }  // extern "C"
