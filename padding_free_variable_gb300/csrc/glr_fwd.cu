@@ -123,7 +123,8 @@ __global__ void __launch_bounds__(32 * kGlrWarps, FwdTile<T, GATED, ROWS>::CTAS)
     extern __shared__ __align__(128) char smem[];
     WarpMap<V>* const s_map = (WarpMap<V>*)(smem + NS * C::STAGE + C::OUT);
     const int lane = threadIdx.x % 32, w = threadIdx.x / 32;
-    const Place c(p, blockIdx.x, 32 * V);
+    // cut sequences: the pieces whose maps were formed last are the ones still in L2
+    const Place c(p, p.cut ? gridDim.x - 1 - blockIdx.x : blockIdx.x, 32 * V);
     const int u = c.u0 + lane * V, len = c.len;
     const bool live = u < p.H;
     const int64_t state = ((int64_t)c.d * p.B + p.perm[c.j]) * p.H + u;
