@@ -170,6 +170,21 @@ void glr_cut(const Plan& p, int V, int ctas, void* scratch, GlrArgs* a)
     a->maps = (float4*)scratch;
 }
 
+bool glr_short(const Plan& p, int V, int ctas, GlrArgs* a)
+{
+    // A warp takes 8 steps at a time, all warps that the GPU holds at once: the longest sequence's
+    // tiles against an even share.  A CTA's 64 steps cost it as much for a sequence of 8.
+    const int64_t items = (int64_t)ceil_div(a->H, 32 * V) * a->ndir * p.B, warps = (int64_t)p.num_sms * ctas * kGlrWarps;
+    const int64_t longest = ceil_div(p.T, kGlrSteps), share = p.rows / kGlrSteps * (items / p.B) / warps;
+    if (longest > 2 && (items * 2 < warps || longest > 2 * share + 8)) return false;
+    const int l = p.levels - 1;
+    a->pieces = p.d_pieces + p.level_first[l];
+    a->count = p.level_count[l];
+    a->cut = false;
+    a->piece = INT32_MAX;
+    return true;
+}
+
 size_t glr_scratch(const Plan& p, const lstm_glr_shape& s)
 {
     // the finest level's maps, 8 bytes a unit, in blocks of at most 64 units

@@ -310,9 +310,13 @@ template <typename T, int ROWS, int G> struct RowTile {
 #pragma unroll
         for (int x = 0; x < G; ++x) src[x] += from;
     }
-    // `rows`: lane k < 8 holds the packed row of the warp's step k
-    __device__ __forceinline__ void load(int lane, unsigned rows, int stage)
+    // `rows`: lane k < 8 holds the packed row of the warp's step k; `any`: is there one to load?
+    __device__ __forceinline__ void load(int lane, unsigned rows, int stage, bool any = true)
     {
+        if (STAGED && !any) {       // (a branch around loads into registers would wait for them)
+            cp_async_commit();
+            return;
+        }
         char* to = in + stage + lane / LR * RB + at;
 #pragma unroll
         for (int k = 0; k < S; k += RI) {
@@ -368,6 +372,8 @@ GlrRows glr_rows(const GlrArgs& a, int elem);
 // `ctas` is what an SM holds of the scan kernel, `scratch` the caller's (null: uncut).
 void glr_cut(const Plan& p, int V, int ctas, void* scratch, GlrArgs* a);
 size_t glr_scratch(const Plan& p, const lstm_glr_shape& s);
+// Whether each warp takes a sequence of its own (uncut: fills the pieces' fields).
+bool glr_short(const Plan& p, int V, int ctas, GlrArgs* a);
 
 lstm_status launch_glr_fwd(const Plan& p, const lstm_glr_shape& s, GlrArgs a, void* scratch, cudaStream_t cs);
 lstm_status launch_glr_bwd(const Plan& p, const lstm_glr_shape& s, GlrArgs a, void* scratch, cudaStream_t cs);
@@ -386,6 +392,22 @@ lstm_status glr_launch(const Plan& p, F* fn, const GlrArgs& a, int V, size_t sme
         if (p.device < 64) ready.fetch_or(bit, std::memory_order_release);
     }
     fn<<<(unsigned)items, 32 * kGlrWarps, smem, cs>>>(a);
+    trace_end(p, -1, cs, 1);
+    return cudaGetLastError() == cudaSuccess ? LSTM_OK : LSTM_ERR_CUDA;
+}
+
+// The same for a kernel whose warps take an item each.
+template <typename F>
+lstm_status glr_launch_warps(const Plan& p, F* fn, const GlrArgs& a, int V, size_t smem, std::atomic<uint64_t>& ready, cudaStream_t cs)
+{
+    const int64_t items = (int64_t)ceil_div(a.H, 32 * V) * a.ndir * a.count;
+    if (items > INT32_MAX) return LSTM_ERR_UNSUPPORTED;
+    const uint64_t bit = 1ull << (p.device & 63);
+    if (!(ready.load(std::memory_order_acquire) & bit)) {
+        LSTM_CUDA_TRY(cudaFuncSetAttribute((const void*)fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
+        if (p.device < 64) ready.fetch_or(bit, std::memory_order_release);
+    }
+    fn<<<(unsigned)((items + kGlrWarps - 1) / kGlrWarps), 32 * kGlrWarps, smem, cs>>>(a, (int)items);
     trace_end(p, -1, cs, 1);
     return cudaGetLastError() == cudaSuccess ? LSTM_OK : LSTM_ERR_CUDA;
 }

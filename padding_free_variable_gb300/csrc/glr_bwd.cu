@@ -43,6 +43,61 @@ template <typename T, int ROWS, int G> __device__ __forceinline__ RowTile<T, ROW
     return t;
 }
 
+// a, 1 - a and b of 8 steps, the identity for those past the end.
+template <bool GATED, typename Tile>
+__device__ __forceinline__ void step_parts(const Tile& tile, int lane, int stage, int left, Vals<Tile::V> (&a)[kGlrSteps],
+                                           Vals<Tile::V> (&n)[kGlrSteps], Vals<Tile::V> (&b)[kGlrSteps])
+{
+#pragma unroll
+    for (int k = 0; k < kGlrSteps; ++k) {
+        const Vals<Tile::V> z = tile.held(lane, 1, k, stage);
+        tile.held(lane, 0, k, stage).sigmoids(a[k], n[k]);
+        if (GATED) {
+            b[k] = tile.held(lane, 2, k, stage);
+            b[k].sigmoid();
+        } else {
+            b[k] = n[k];
+        }
+        b[k].mul(z);
+    }
+    if (left < kGlrSteps) {
+#pragma unroll
+        for (int k = 0; k < kGlrSteps; ++k)
+            if (k >= left) {
+                a[k].fill(1.f);
+                b[k].fill(0.f);
+            }
+    }
+}
+
+// One step backwards: e comes in as the error from the step after and leaves as what this one passes on; `h` is the
+// state before the step.
+template <bool GATED, typename Tile, int V>
+__device__ __forceinline__ void step_gradients(const Tile& tile, int lane, int k, int stage, const Vals<V>& a, Vals<V> n, Vals<V> h, Vals<V>& e,
+                                               Vals<V>& df, Vals<V>& dz, Vals<V>& di)
+{
+    e.add(tile.held(lane, GATED ? 3 : 2, k, stage));        // G
+    const Vals<V> z = tile.held(lane, 1, k, stage);
+    n.mul(e);                                               // G (1 - a)
+    dz = di = e;
+    if (GATED) {
+        Vals<V> g, ng;
+        tile.held(lane, 2, k, stage).sigmoids(g, ng);
+        df = n;
+        dz.mul(g);
+        di = dz;
+        di.mul(ng);
+        di.mul(z);
+    } else {
+        dz = n;
+        df = n;
+        h.sub(z);
+    }
+    df.mul(a);
+    df.mul(h);
+    e.mul(a);
+}
+
 template <typename T, bool GATED, int ROWS>
 __global__ void __launch_bounds__(32 * kGlrWarps, BwdTile<T, GATED, ROWS>::CTAS) glr_bwd_kernel(const GlrArgs p)
 {
@@ -116,25 +171,7 @@ __global__ void __launch_bounds__(32 * kGlrWarps, BwdTile<T, GATED, ROWS>::CTAS)
                 __syncwarp();
             }
             Vals<V> a[S], n[S], b[S];               // a, 1 - a, b
-#pragma unroll
-            for (int k = 0; k < S; ++k) {
-                const Vals<V> z = tile.held(lane, 1, k, stage);
-                tile.held(lane, 0, k, stage).sigmoids(a[k], n[k]);
-                if (GATED) {
-                    b[k] = tile.held(lane, 2, k, stage);
-                    b[k].sigmoid();
-                } else {
-                    b[k] = n[k];
-                }
-                b[k].mul(z);
-            }
-            if (s0 + S > len) {
-                Vals<V> zero;
-                zero.fill(0.f);
-#pragma unroll
-                for (int k = 0; k < S; ++k)
-                    if (s0 + k >= len) { a[k].fill(1.f); b[k] = zero; }
-            }
+            step_parts<GATED>(tile, lane, stage, len - s0, a, n, b);
             A = a[0];
             U = b[0];
 #pragma unroll
@@ -174,26 +211,8 @@ __global__ void __launch_bounds__(32 * kGlrWarps, BwdTile<T, GATED, ROWS>::CTAS)
             const int m = tile.writes ? len - s0 : 0;
 #pragma unroll
             for (int k = S - 1; k >= 0; --k) {
-                e.add(tile.held(lane, DY, k, stage));       // G
-                const Vals<V> z = tile.held(lane, 1, k, stage);
-                Vals<V> df = e, dz = e, di = e;
-                n[k].mul(e);                                // G (1 - a)
-                if (GATED) {
-                    Vals<V> g, ng;
-                    tile.held(lane, 2, k, stage).sigmoids(g, ng);
-                    df = n[k];
-                    dz.mul(g);
-                    di = dz;
-                    di.mul(ng);
-                    di.mul(z);
-                } else {
-                    dz = n[k];
-                    df = dz;
-                    b[k].sub(z);
-                }
-                df.mul(a[k]);
-                df.mul(b[k]);
-                e.mul(a[k]);
+                Vals<V> df, dz, di;
+                step_gradients<GATED>(tile, lane, k, stage, a[k], n[k], b[k], e, df, dz, di);
                 if constexpr (C::STAGED) {
                     store_values<T, V>(tile.slot(lane, 0, k, stage), df);
                     store_values<T, V>(tile.slot(lane, 1, k, stage), dz);
@@ -234,6 +253,141 @@ __global__ void __launch_bounds__(32 * kGlrWarps, BwdTile<T, GATED, ROWS>::CTAS)
         for (int v = 0; v < V; ++v) p.dh0[state + v] = e.get(v);
     if (p.padded && tile.writes && c.piece == 0)        // the padded comparator's rows past the end
         for (int t = len + w; t < p.T; t += W)
+#pragma unroll
+            for (int x = 0; x < G - 1; ++x)
+                for (int y = 0; y < C::WIDTH; y += (int)sizeof(T))
+                    *(T*)(grad[x] + (uint64_t)(p.off[t] + c.j) * gld + y) = from_f32<T>(0.f);
+}
+
+// A warp a sequence, as in the forward pass: each 64 steps from the end, their states run again 8
+// steps at a time (a second reading, out of the caches, where there are more than 8), then their
+// gradients 8 steps at a time.
+template <typename T, bool GATED, int ROWS> struct BwdShortTile : RowTile<T, ROWS, GATED ? 4 : 3> {
+    typedef RowTile<T, ROWS, GATED ? 4 : 3> R;
+    static constexpr int W = kGlrWarps, CTAS = 2;
+    static constexpr int TILES = kScanChunk / kGlrSteps;
+    static constexpr int STATES = TILES * 32 * R::V * 4;        // a warp's
+    static constexpr int FIT = (112 * 1024 / W - STATES) / R::BYTES;
+    static constexpr int NS = !R::STAGED || FIT < 2 ? 1 : FIT > 3 ? 3 : FIT;
+    static constexpr int WARP = NS * R::BYTES + STATES, SMEM = W * WARP;
+};
+
+template <typename T, bool GATED, int ROWS>
+__global__ void __launch_bounds__(32 * kGlrWarps, 2) glr_bwd_short_kernel(const GlrArgs p, const int items)
+{
+    typedef BwdShortTile<T, GATED, ROWS> C;
+    constexpr int S = C::S, V = C::V, NS = C::NS, G = GATED ? 4 : 3;
+    extern __shared__ __align__(128) char smem[];
+    const int lane = threadIdx.x % 32, w = threadIdx.x / 32, item = blockIdx.x * kGlrWarps + w;
+    if (item >= items) return;
+    const Place c(p, item, 32 * V);
+    const int u = c.u0 + lane * V, len = c.len;
+    const bool live = u < p.H;
+    const int64_t state = ((int64_t)c.d * p.B + p.perm[c.j]) * p.H + u;
+    auto tile = error_rows<T, ROWS, G>(p, c, lane);
+    tile.in = smem + w * C::WARP;
+    Vals<V>* const before = (Vals<V>*)(tile.in + NS * C::BYTES) + lane;     // [tile][lane]: states before the tiles
+    const unsigned gld = (unsigned)p.gld * (unsigned)sizeof(T);
+    const int64_t to = (c.d * p.gdstride + c.u0) * (int64_t)sizeof(T) + tile.at;
+    char* grad[G - 1];
+    grad[0] = (char*)p.df + to;
+    grad[1] = (char*)p.dz + to;
+    if (GATED) grad[G - 2] = (char*)p.di + to;
+    Vals<V> e;
+    e.each([&](int v) { return live && p.dh_n ? p.dh_n[state + v] : 0.f; });
+    for (int base = len > 0 ? (len - 1) / kScanChunk * kScanChunk : -1; base >= 0; base -= kScanChunk) {
+        const float* kept = p.ws + ((int64_t)(p.chunk[c.j] + base / kScanChunk) * p.ndir + c.d) * p.H + (live ? u : 0);
+        Vals<V> h;
+        h.each([&](int v) { return live ? __ldg(kept + v) : 0.f; });
+        const int tiles = min(C::TILES, (len - base + S - 1) / S);
+        before[0] = h;
+        // sweep 0: the tiles but the last, forwards, for the states before them; sweep 1: all of them, backwards
+        for (int sweep = tiles > 1 ? 0 : 1; sweep < 2; ++sweep) {
+            const int count = sweep == 0 ? tiles - 1 : tiles;
+            auto first = [&](int x) { return base + (sweep == 0 ? x : tiles - 1 - x) * S; };     // step of the x-th tile
+            unsigned rows[NS + 2];
+#pragma unroll
+            for (int q = 0; q < NS + 2; ++q) rows[q] = c.row_of(p, first(q), lane);
+#pragma unroll
+            for (int q = 0; q < NS; ++q) tile.load(lane, rows[q], q * C::BYTES, q < count);
+            int stage = 0;
+            for (int x = 0; x < count; ++x) {
+                const int s0 = first(x);
+                if (C::STAGED) {
+                    cp_async_wait<NS - 1>();
+                    __syncwarp();
+                } else {
+                    tile.stash(lane);
+                    tile.load(lane, rows[1], 0);
+                }
+                if (s0 + S > len) {     // past the end no error enters
+                    for (int k = max(0, len - s0); k < S; ++k)
+                        for (int y = 0; y < C::OWN; y += (int)sizeof(T)) *(T*)(tile.slot(lane, G - 1, k, stage) + y) = from_f32<T>(0.f);
+                    __syncwarp();
+                }
+                Vals<V> a[S], n[S], b[S];
+                step_parts<GATED>(tile, lane, stage, len - s0, a, n, b);
+                if (sweep == 0) {
+#pragma unroll
+                    for (int k = 0; k < S; ++k) h.mad(a[k], b[k]);
+                    before[(x + 1) * 32] = h;
+                } else {
+                    h = before[(tiles - 1 - x) * 32];
+#pragma unroll
+                    for (int k = 0; k < S; ++k) {       // b becomes the state before the step
+                        const Vals<V> was = h;
+                        h.mad(a[k], b[k]);
+                        b[k] = was;
+                    }
+                    const int m = tile.writes ? len - s0 : 0;
+#pragma unroll
+                    for (int k = S - 1; k >= 0; --k) {
+                        Vals<V> df, dz, di;
+                        step_gradients<GATED>(tile, lane, k, stage, a[k], n[k], b[k], e, df, dz, di);
+                        if constexpr (C::STAGED) {
+                            store_values<T, V>(tile.slot(lane, 0, k, stage), df);
+                            store_values<T, V>(tile.slot(lane, 1, k, stage), dz);
+                            if (GATED) store_values<T, V>(tile.slot(lane, 2, k, stage), di);
+                        } else {
+                            const uint64_t row = (uint64_t)__shfl_sync(0xffffffffu, rows[0], k) * gld;
+                            if (k < m) {
+                                store_values<T, V>(grad[0] + row, df);
+                                store_values<T, V>(grad[1] + row, dz);
+                                if (GATED) store_values<T, V>(grad[G - 2] + row, di);
+                            }
+                        }
+                    }
+                    if constexpr (C::STAGED) {
+                        __syncwarp();
+#pragma unroll
+                        for (int k = 0; k < S; k += C::RI) {
+                            const int s = k + lane / C::LR;
+                            const uint64_t row = (uint64_t)__shfl_sync(0xffffffffu, rows[0], s) * gld;
+#pragma unroll
+                            for (int q = 0; q < G - 1; ++q) {
+                                const uint4 bits = *(const uint4*)(tile.in + stage + (q * S + s) * C::RB + tile.at);
+                                if (s < m) *(uint4*)(grad[q] + row) = bits;
+                            }
+                        }
+                    }
+                }
+                if (C::STAGED) {
+                    __syncwarp();
+                    tile.load(lane, rows[NS], stage, x + NS < count);
+                    stage = stage == (NS - 1) * C::BYTES ? 0 : stage + C::BYTES;
+                }
+#pragma unroll
+                for (int q = 0; q < NS + 1; ++q) rows[q] = rows[q + 1];
+                rows[NS + 1] = c.row_of(p, first(x + NS + 2), lane);
+            }
+            if (C::STAGED) cp_async_wait<0>();
+        }
+    }
+    if (p.dh0 && live)
+#pragma unroll
+        for (int v = 0; v < V; ++v) p.dh0[state + v] = e.get(v);
+    if (p.padded && tile.writes)        // the padded comparator's rows past the end
+        for (int t = len; t < p.T; ++t)
 #pragma unroll
             for (int x = 0; x < G - 1; ++x)
                 for (int y = 0; y < C::WIDTH; y += (int)sizeof(T))
@@ -320,6 +474,9 @@ lstm_status go(const Plan& p, GlrArgs a, void* scratch, cudaStream_t cs)
 {
     static std::atomic<uint64_t> ready{0}, ready_map{0};
     typedef BwdTile<T, GATED, ROWS> C;
+    typedef BwdShortTile<T, GATED, ROWS> Q;
+    static std::atomic<uint64_t> ready_short{0};
+    if (glr_short(p, C::V, Q::CTAS, &a)) return glr_launch_warps(p, glr_bwd_short_kernel<T, GATED, ROWS>, a, C::V, Q::SMEM, ready_short, cs);
     glr_cut(p, C::V, C::CTAS, scratch, &a);
     if (a.cut) {
         const lstm_status st = glr_launch(p, glr_bwd_map_kernel<T, ROWS>, a, C::V, BwdMapTile<T, ROWS>::SMEM, ready_map, cs);

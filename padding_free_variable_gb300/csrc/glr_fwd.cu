@@ -215,6 +215,87 @@ __global__ void __launch_bounds__(32 * kGlrWarps, FwdTile<T, GATED, ROWS>::CTAS)
     if (p.padded && tile.writes && c.piece == 0) zero_past_end<T, C::WIDTH>(p, c, y, yld, w, W);
 }
 
+// ---------------------------------------------------------------- a warp a sequence
+
+// Many sequences, or very short ones: a warp walks a sequence 8 steps at a time by itself, running
+// the steps as they come.  No maps, no barriers, and no warp idles past a short sequence's end.
+template <typename T, bool GATED, int ROWS> struct ShortTile : RowTile<T, ROWS, GATED ? 3 : 2> {
+    typedef RowTile<T, ROWS, GATED ? 3 : 2> R;
+    static constexpr int W = kGlrWarps, CTAS = 3;
+    static constexpr int OUT = R::STAGED ? R::S * R::RB : 0;                    // a warp's
+    static constexpr int FIT = (72 * 1024 / W - OUT) / R::BYTES;
+    static constexpr int NS = !R::STAGED || FIT < 2 ? 1 : FIT > 4 ? 4 : FIT;
+    static constexpr int WARP = (R::STAGED ? NS * R::BYTES : 0) + OUT, SMEM = W * WARP;
+};
+
+template <typename T, bool GATED, int ROWS>
+__global__ void __launch_bounds__(32 * kGlrWarps, 3) glr_fwd_short_kernel(const GlrArgs p, const int items)
+{
+    typedef ShortTile<T, GATED, ROWS> C;
+    constexpr int S = C::S, V = C::V, NS = C::NS;
+    extern __shared__ __align__(128) char smem[];
+    const int lane = threadIdx.x % 32, w = threadIdx.x / 32, item = blockIdx.x * kGlrWarps + w;
+    if (item >= items) return;
+    const Place c(p, item, 32 * V);
+    const int u = c.u0 + lane * V, len = c.len;
+    const bool live = u < p.H;
+    const int64_t state = ((int64_t)c.d * p.B + p.perm[c.j]) * p.H + u;
+    auto tile = gate_rows<T, ROWS, GATED ? 3 : 2>(p, c, lane);
+    tile.in = smem + w * C::WARP;
+    char* const out = tile.in + (C::STAGED ? NS * C::BYTES : 0);
+    const unsigned yld = (unsigned)(p.ndir * p.H) * (unsigned)sizeof(T);
+    char* y = (char*)p.y + ((int64_t)c.d * p.H + c.u0) * (int64_t)sizeof(T) + tile.at;
+    Vals<V> h;
+    if (len > 0) {
+        unsigned rows[NS + 2];          // of the tiles from this one on
+#pragma unroll
+        for (int q = 0; q < NS + 2; ++q) rows[q] = c.row_of(p, q * S, lane);
+#pragma unroll
+        for (int q = 0; q < NS; ++q) tile.load(lane, rows[q], q * C::BYTES, q * S < len);
+        h.each([&](int v) { return live && p.h0 ? p.h0[state + v] : 0.f; });
+        int stage = 0;
+        for (int s0 = 0; s0 < len; s0 += S) {
+            Vals<V> a[S], b[S];
+            if (C::STAGED) {
+                cp_async_wait<NS - 1>();
+                __syncwarp();
+            }
+            step_maps<RowTile<T, ROWS, GATED ? 3 : 2>, GATED>(tile, lane, stage, len - s0, a, b);
+            if (C::STAGED) __syncwarp();
+            tile.load(lane, rows[NS], stage, s0 + NS * S < len);
+            stage = stage == (NS - 1) * C::BYTES ? 0 : stage + C::BYTES;
+            const unsigned rows_now = rows[0];
+#pragma unroll
+            for (int q = 0; q < NS + 1; ++q) rows[q] = rows[q + 1];
+            rows[NS + 1] = c.row_of(p, s0 + (NS + 2) * S, lane);
+            if (p.ws && live && s0 % kScanChunk == 0) {
+                float* ws = p.ws + ((int64_t)(p.chunk[c.j] + s0 / kScanChunk) * p.ndir + c.d) * p.H + u;
+#pragma unroll
+                for (int v = 0; v < V; ++v) ws[v] = h.get(v);
+            }
+            const int n = tile.writes ? len - s0 : 0;
+#pragma unroll
+            for (int k = 0; k < S; ++k) {
+                h.mad(a[k], b[k]);
+                if constexpr (C::STAGED) {
+                    store_values<T, V>(out + k * C::RB + lane * C::OWN, h);
+                } else {
+                    const unsigned row = __shfl_sync(0xffffffffu, rows_now, k);
+                    if (k < n) store_values<T, V>(y + (uint64_t)row * yld, h);
+                }
+            }
+            if constexpr (C::STAGED) flush_rows<C>(out, lane, tile.at, y, yld, rows_now, n);
+        }
+        if (C::STAGED) cp_async_wait<0>();
+    } else {
+        h.each([&](int v) { return live && p.h0 ? p.h0[state + v] : 0.f; });
+    }
+    if (p.h_n && live)
+#pragma unroll
+        for (int v = 0; v < V; ++v) p.h_n[state + v] = h.get(v);
+    if (p.padded && tile.writes) zero_past_end<T, C::WIDTH>(p, c, y, yld, 0, 1);
+}
+
 // ---------------------------------------------------------------- a piece's map
 
 // Where sequences are cut, every piece but a sequence's last is first reduced to its map: warp w
@@ -278,6 +359,9 @@ lstm_status go(const Plan& p, GlrArgs a, void* scratch, cudaStream_t cs)
     static std::atomic<uint64_t> ready{0}, ready_map{0};
     typedef FwdTile<T, GATED, ROWS> C;
     typedef MapTile<T, GATED, ROWS> M;
+    typedef ShortTile<T, GATED, ROWS> Q;
+    static std::atomic<uint64_t> ready_short{0};
+    if (glr_short(p, C::V, Q::CTAS, &a)) return glr_launch_warps(p, glr_fwd_short_kernel<T, GATED, ROWS>, a, C::V, Q::SMEM, ready_short, cs);
     glr_cut(p, C::V, C::CTAS, scratch, &a);
     if (a.cut) {
         const lstm_status st = glr_launch(p, glr_fwd_map_kernel<T, GATED, ROWS>, a, C::V, M::SMEM, ready_map, cs);

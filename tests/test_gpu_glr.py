@@ -98,6 +98,7 @@ class Case:
         return w
 
 
+MANY = [int(v) for v in np.random.default_rng(8).integers(0, 151, 1000)]
 CASES = [
     # lengths, directions, H, dtype, cell, padded, layout, shift (elements off the buffer's start)
     ([1], 1, 1, "f32", "tied", False, "blocks", 0),
@@ -118,6 +119,13 @@ CASES = [
     ([2500, 2499], 1, 512, "f32", "tied", False, "blocks", 0),
     ([9000], 1, 64, "bf16", "gated", False, "blocks", 0),
     ([30] * 300, 2, 24, "f32", "tied", False, "blocks", 0),
+    # sequences of a tile or two, and many sequences: a warp each
+    ([16, 3, 0, 9, 1, 8], 2, 7, "bf16", "gated", False, "blocks", 1),
+    ([16, 3, 0, 9, 1, 8], 1, 33, "f32", "tied", False, "dirs", 0),
+    ([13, 0, 16, 2], 2, 40, "bf16", "tied", True, "blocks", 0),
+    (MANY, 2, 36, "f32", "gated", False, "blocks", 0),
+    (MANY, 2, 8, "bf16", "tied", False, "blocks", 0),
+    (MANY, 2, 5, "f32", "tied", False, "planes", 0),
     ([5, 0, 17, 70, 3], 2, 16, "f32", "gated", True, "blocks", 0),
     ([5, 0, 17, 170, 3], 2, 96, "bf16", "tied", True, "dirs", 0),
 ]
