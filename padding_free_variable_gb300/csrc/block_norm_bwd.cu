@@ -52,7 +52,7 @@ lstm_status launch_norm_bwd(NormArgs a, cudaStream_t cs)
 {
     const BwdShape s = bwd_shape(a.D);
     lstm_status st = LSTM_OK;
-    if (s.per == 1 && norm_full(a) && a.dn && a.dx_out && a.sums[0] && a.sums[2] && a.sums[3] &&
+    if ((s.per == 1 || (s.per == 2 && norm_whole(a))) && norm_full(a) && a.dn && a.dx_out && a.sums[0] && a.sums[2] && a.sums[3] &&
         (a.post == LSTM_NORM_LAYER) == (a.sums[1] != nullptr) && (a.post == LSTM_NORM_LAYER) == (a.sums[4] != nullptr))
         st = a.gate == LSTM_GATE_SILU ? norm_bwd_silu(a, s, cs) : a.gate == LSTM_GATE_SIGMOID ? norm_bwd_sigmoid(a, s, cs) : norm_bwd_none(a, s, cs);
     else

@@ -435,6 +435,7 @@ template <int KIND, int GATE, typename TB, typename TS> lstm_status run_block(No
     if (norm_whole(a)) {
         if (s.threads <= 128) return run<TB, TS, TB, 8, 1, R, 128, R == 2 ? 4 : 6, KIND, GATE>(a, s, cs);
         if (s.threads <= 256) return run<TB, TS, TB, 8, 1, R, 256, R == 2 ? 2 : 3, KIND, GATE>(a, s, cs);
+        if (s.per == 2) return run<TB, TS, TB, 8, 2, 1, 512, 1, KIND, GATE>(a, s, cs);
         return run<TB, TS, TB, 8, 1, R, 512, 1, KIND, GATE>(a, s, cs);
     }
     if (norm_shifted(a) && a.D + 7 <= 4096) {
