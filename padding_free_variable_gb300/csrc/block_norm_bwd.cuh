@@ -34,7 +34,7 @@ inline BwdShape bwd_shape(int D)
     s.per = wide <= 4096 ? 1 : wide <= 8192 ? 2 : 4;
     s.tpr = row_threads(ceil_div(wide, 8 * s.per));
     s.threads = s.tpr <= 32 ? 128 : s.tpr;
-    s.ctas = s.threads <= 128 ? 6 : s.threads <= 256 ? 3 : 1;
+    s.ctas = s.threads <= 128 ? 8 : s.threads <= 256 ? 4 : 2;       // at most
     return s;
 }
 
@@ -78,6 +78,9 @@ __device__ __forceinline__ void put_piece(T* base, int64_t row, const Cols<VEC, 
     for (int i = 0; i < Q; ++i)
         if (c.valid(k, n * Q + i)) base[row + c.at(k) + n * Q + i] = from_f32<T>(x[i]);
 }
+
+// Sums of a kind of block, and its parameters (with the mark of a row's own places).
+__host__ __device__ constexpr int bwd_vectors(int kind) { return kind == LSTM_NORM_RMS ? 3 : kSums; }
 
 // Means over a row of t xh (m1) and, for centred norms, of t (m0); sums: R of the one, R of the other.
 template <int R> __device__ __forceinline__ void row_means(RowSum& sum, float (&sums)[2 * R], bool centred, float inv, float (&m0)[R], float (&m1)[R])
@@ -125,8 +128,11 @@ __global__ void __launch_bounds__(THREADS, CTAS) norm_bwd_kernel(const NormArgs 
     RowSum sum{s_part, tpr, 0};
     const float inv = 1.f / (float)p.D;
     float* const out = p.part + (int64_t)blockIdx.x * kSums * p.D;
+    // a kind without biases keeps three sums; shifted rows' CTAs are as large as their rows need
+    auto slot = [](int which) { return KIND == LSTM_NORM_RMS ? (which + 1) / 2 : which; };
+    const int threads = SHIFT ? (int)blockDim.x : THREADS;
     auto place = [&](int which, int k, int n) {
-        return FAR ? out + which * p.D + c.at(k) + n * Q : s_sums + ((which * PER * N + k * N + n) * THREADS + (int)threadIdx.x) * Q;
+        return FAR ? out + which * p.D + c.at(k) + n * Q : s_sums + ((slot(which) * PER * N + k * N + n) * threads + (int)threadIdx.x) * Q;
     };
     auto add = [&](int which, int k, int n, const float (&x)[Q]) {
         float* at = place(which, k, n);
@@ -139,7 +145,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) norm_bwd_kernel(const NormArgs 
         }
     };
     // shifted columns' parameters, after the sums: w_post, scale, w_pre (1, b_post)
-    const OwnParams<SHIFT ? VEC : 4, PER> own{(float4*)(s_sums + kSums * PER * VEC * THREADS)};
+    const OwnParams<SHIFT ? VEC : 4, PER> own{(float4*)(s_sums + bwd_vectors(KIND) * PER * VEC * threads)};
     if constexpr (SHIFT) {
         c.shift = (int)((blockIdx.x * (uint64_t)groups + group) * (unsigned)p.D & 7u);
         own.fill(0, c, [&](int i) { return p.w.w_post[i]; });
@@ -153,7 +159,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) norm_bwd_kernel(const NormArgs 
     for (int which = 0; which < kSums; ++which)
 #pragma unroll
         for (int k = 0; k < PER; ++k)
-            if (!FAR || c.has(k))
+            if (wants(which) && (!FAR || c.has(k)))
 #pragma unroll
                 for (int n = 0; n < N; ++n)
 #pragma unroll
@@ -381,7 +387,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) norm_bwd_kernel(const NormArgs 
                 for (int g = 0; g < groups; ++g) {
                     const int shift = (int)((blockIdx.x * (uint64_t)groups + g) * (unsigned)p.D & 7u), at = i + shift;
                     const int n = at % VEC / Q, t = at / VEC;
-                    s += s_sums[((which * N + n) * THREADS + g * tpr + t) * Q + at % Q];
+                    s += s_sums[((slot(which) * N + n) * threads + g * tpr + t) * Q + at % Q];
                 }
                 out[which * p.D + i] = s;
             }
@@ -410,18 +416,27 @@ lstm_status run(NormArgs& a, const BwdShape& s, cudaStream_t cs)
     static std::atomic<uint64_t> ready{0};
     auto* fn = norm_bwd_kernel<TB, TS, TN, VEC, PER, R, THREADS, CTAS, KIND, GATE, SHIFT>;
     const int64_t groups = s.threads / s.tpr;
-    constexpr size_t SUMS = PER * VEC > 16 ? 0 : sizeof(float) * kSums * PER * VEC * THREADS;
-    constexpr size_t smem = SUMS + (SHIFT ? sizeof(float) * 5 * PER * VEC * THREADS : 0);
+    constexpr size_t VECTOR = sizeof(float) * PER * VEC;        // a thread's part of one sum or parameter
+    const size_t smem = PER * VEC > 16 ? 0 : VECTOR * bwd_vectors(KIND) * (SHIFT ? 2 * s.threads : THREADS);
     int dev = 0;
     LSTM_CUDA_TRY(cudaGetDevice(&dev));
     const uint64_t bit = 1ull << (dev & 63);
     if (!(ready.load(std::memory_order_acquire) & bit)) {
-        LSTM_CUDA_TRY(cudaFuncSetAttribute((const void*)fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
+        LSTM_CUDA_TRY(cudaFuncSetAttribute((const void*)fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                           (int)(PER * VEC > 16 ? 0 : VECTOR * bwd_vectors(KIND) * (SHIFT ? 2 : 1) * THREADS)));
         if (dev < 64) ready.fetch_or(bit, std::memory_order_release);
     }
-    // as many CTAs as stay resident
+    // as many CTAs as stay resident, asked for once for each size of a CTA
+    static std::atomic<int> resident[17];
+    std::atomic<int>& known = resident[s.threads / 32];
+    int fit = known.load(std::memory_order_relaxed);
+    if (fit == 0) {
+        LSTM_CUDA_TRY(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&fit, fn, s.threads, smem));
+        fit = std::max(fit, 1);
+        known.store(fit, std::memory_order_relaxed);
+    }
     const int64_t rows = (a.rows + R - 1) / R;
-    a.parts = (int)std::min<int64_t>(a.parts, std::min<int64_t>((rows + groups - 1) / groups, (int64_t)kSMs * CTAS));
+    a.parts = (int)std::min<int64_t>(a.parts, std::min<int64_t>((rows + groups - 1) / groups, (int64_t)kSMs * fit));
     if (SHIFT) a.parts = (int)shifted_blocks(a.parts);
     fn<<<a.parts, s.threads, smem, cs>>>(a, s.tpr);
     return cudaGetLastError() == cudaSuccess ? LSTM_OK : LSTM_ERR_CUDA;
@@ -436,11 +451,13 @@ template <int KIND, int GATE, typename TB, typename TS> lstm_status run_block(No
         if (s.threads <= 128) return run<TB, TS, TB, 8, 1, R, 128, R == 2 ? 4 : 6, KIND, GATE>(a, s, cs);
         if (s.threads <= 256) return run<TB, TS, TB, 8, 1, R, 256, R == 2 ? 2 : 3, KIND, GATE>(a, s, cs);
         if (s.per == 2) return run<TB, TS, TB, 8, 2, 1, 512, 1, KIND, GATE>(a, s, cs);
+        if (s.threads <= 384) return run<TB, TS, TB, 8, 1, 1, 384, 2, KIND, GATE>(a, s, cs);
         return run<TB, TS, TB, 8, 1, R, 512, 1, KIND, GATE>(a, s, cs);
     }
     if (norm_shifted(a) && a.D + 7 <= 4096) {
         if (s.threads <= 128) return run<TB, TS, TB, 8, 1, 1, 128, 5, KIND, GATE, true>(a, s, cs);
         if (s.threads <= 256) return run<TB, TS, TB, 8, 1, 1, 256, 3, KIND, GATE, true>(a, s, cs);
+        if (s.threads <= 384) return run<TB, TS, TB, 8, 1, 1, 384, 2, KIND, GATE, true>(a, s, cs);
         return run<TB, TS, TB, 8, 1, 1, 512, 1, KIND, GATE, true>(a, s, cs);
     }
     if (s.threads <= 128) return run<TB, TS, TB, 1, 8, 1, 128, 6, KIND, GATE>(a, s, cs);
