@@ -147,8 +147,7 @@ static bool glr_whole(const GlrArgs& a, int elem, int64_t bytes)
 
 GlrRows glr_rows(const GlrArgs& a, int elem)
 {
-    // fp32 rows of at most 32 units fill a warp with one unit a lane
-    if (glr_whole(a, elem, 16) && (elem == 2 || a.H > 32)) return GLR_WIDE;
+    if (glr_whole(a, elem, 16)) return a.H > 32 ? GLR_WIDE : GLR_PACKED;
     return glr_whole(a, elem, 4) ? GLR_NARROW : GLR_SINGLE;
 }
 
@@ -159,10 +158,11 @@ void glr_cut(const Plan& p, int V, int ctas, void* scratch, GlrArgs* a)
     // is cut (every piece's gates are then read twice), into pieces short enough to spread well and
     // long enough that starting them (about two iterations) does not show.
     const int64_t blocks = ceil_div(a->H, 32 * V), slots = (int64_t)p.num_sms * ctas;
-    const int64_t share = p.chunks * blocks * a->ndir / slots, longest = ceil_div(p.T, kScanChunk);
+    const int64_t steps = (int64_t)kScanChunk * a->groups, share = p.chunks / a->groups * blocks * a->ndir / slots;
+    const int64_t longest = (p.T + steps - 1) / steps;
     int l = p.levels - 1;
     if (scratch && longest > share * 3 / 2 + 12)
-        for (l = 0; l < p.levels - 1 && ((int64_t)kScanPiece << l) < kScanChunk * share / 5; ++l) {}
+        for (l = 0; l < p.levels - 1 && ((int64_t)kScanPiece << l) < steps * share / 5; ++l) {}
     a->pieces = p.d_pieces + p.level_first[l];
     a->count = p.level_count[l];
     a->cut = l < p.levels - 1;

@@ -11,6 +11,7 @@ namespace lstm {
 struct GlrArgs {
     int T = 0, B = 0, H = 0, ndir = 1;
     int padded = 0;
+    int groups = 1;                     // GLR_PACKED: groups of lanes, each with steps of its own
     const int4* pieces = nullptr;       // this level's
     int piece = 0;                      // its pieces' steps
     int count = 0;                      // and their number
@@ -175,7 +176,6 @@ template <typename T> __device__ __forceinline__ T from_f32(float v);
 template <> __device__ __forceinline__ float from_f32<float>(float v) { return v; }
 template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
-
 // ---------------------------------------------------------------- launch shape
 
 // Largest row stride (elements): strides in bytes stay within 32 bits, their products with a row are 64 bits wide.
@@ -183,6 +183,7 @@ constexpr int64_t kGlrMaxStride = 1 << 29;
 constexpr int kGlrWarps = 8;            // pieces of a CTA's 64 steps, one a warp
 constexpr int kGlrSteps = 8;            // consecutive steps of one thread
 static_assert(kGlrWarps * kGlrSteps == kScanChunk, "a CTA's iteration is one kept state");
+
 // ---------------------------------------------------------------- affine maps of V units
 
 // V values of a lane, in pairs.
@@ -223,6 +224,13 @@ template <int V> struct Vals {
     {
 #pragma unroll
         for (int v = 0; v < V / 2; ++v) sigmoid_pair2(q[v], s.q[v], c.q[v]);
+    }
+    __device__ __forceinline__ Vals from(int lane) const
+    {
+        Vals r;
+#pragma unroll
+        for (int v = 0; v < V / 2; ++v) r.q[v].v = __shfl_sync(0xffffffffu, q[v].v, lane);
+        return r;
     }
     template <typename G> __device__ __forceinline__ void each(G&& value)
     {
@@ -278,7 +286,8 @@ template <> struct WarpMap<1> {
 enum GlrRows {
     GLR_WIDE = 0,       // 2 units a lane; rows through shared memory in 16-byte pieces
     GLR_NARROW = 1,     // 4 bytes a lane (2 bf16 units or 1 fp32 unit), each lane its own
-    GLR_SINGLE = 2      // bf16 rows that are not aligned to 4 bytes: 1 unit a lane
+    GLR_SINGLE = 2,     // bf16 rows that are not aligned to 4 bytes: 1 unit a lane
+    GLR_PACKED = 3      // as wide rows, of at most 32 units: groups of 16 or 8 lanes take 8 steps each
 };
 
 // A warp's rows: 32 V units of each.  Wide rows reach the warp's own part of shared memory by
@@ -286,31 +295,44 @@ enum GlrRows {
 // rows and not by each lane of each row; the others are loaded by each lane into registers.
 template <typename T, int ROWS, int G> struct RowTile {
     static constexpr int S = kGlrSteps;
-    static constexpr int V = ROWS == GLR_WIDE ? 2 : ROWS == GLR_NARROW ? 4 / (int)sizeof(T) : 1;
+    static constexpr bool PACKED = ROWS == GLR_PACKED;
+    static constexpr int V = ROWS == GLR_WIDE || PACKED ? 2 : ROWS == GLR_NARROW ? 4 / (int)sizeof(T) : 1;
     static constexpr int OWN = V * (int)sizeof(T);              // bytes of a lane's units
     static constexpr int RB = 32 * OWN;                         // bytes of a row
-    static constexpr bool STAGED = ROWS == GLR_WIDE;
+    static constexpr bool STAGED = ROWS == GLR_WIDE || PACKED;
+    // Loads past a piece's end are left out where that gains: they are wasted reads (two sequences of 20 to
+    // 30 thousand frames x 512 fp32 backward 137 us with them, 132 us without), but the branch costs the
+    // bf16 kernels their schedule (40555 frames x 2 x 512 backward 89 us with them, 101 us without).
+    static constexpr bool BOUNDED = PACKED || sizeof(T) == 4;
     static constexpr int WIDTH = STAGED ? 16 : OWN;             // bytes a lane moves at a time
     static constexpr int LR = RB / WIDTH, RI = 32 / LR;         // lanes of a row, rows of one instruction
     static constexpr int BYTES = G * S * RB;                    // a warp's rows of one stage: [operand][step][RB]
 
     const char* src[G];
     unsigned ld[G];             // bytes from row to row
-    int at;                     // this lane's piece: byte in a row
+    int at;                     // this lane's piece: byte in a staged row
     bool writes;                // is it a piece of the row?
+    int lanes = 32;             // of a group
     char* in;                   // this warp's rows of stage 0
     Raw<T, V> raw[STAGED ? 1 : G][STAGED ? 1 : S];
 
     // lanes past the end of a row (of `end` bytes) read its last piece again: what they compute is not written
-    __device__ __forceinline__ void place(int lane, int end)
+    __device__ __forceinline__ void place(int lane, int end, int groups)
     {
         at = lane % LR * WIDTH;
-        writes = at < end;
-        const int from = min(at, end - WIDTH);
+        if (PACKED) lanes = 32 / groups;
+        writes = col() < end;
+        const int from = min(col(), end - WIDTH);
 #pragma unroll
         for (int x = 0; x < G; ++x) src[x] += from;
     }
-    // `rows`: lane k < 8 holds the packed row of the warp's step k; `any`: is there one to load?
+    __device__ __forceinline__ int unit_lane(int lane) const { return PACKED ? lane & (lanes - 1) : lane; }
+    __device__ __forceinline__ int group(int lane) const { return PACKED ? lane / lanes : 0; }
+    // the piece's byte in the row in memory (packed: the groups' rows are staged next to each other)
+    __device__ __forceinline__ int col() const { return PACKED ? at & (lanes * OWN - 1) : at; }
+    // the warp's step whose row the piece of staged row k + lane / LR is of
+    __device__ __forceinline__ int step(int lane, int k) const { return (PACKED ? at / (lanes * OWN) * S : 0) + k + lane / LR; }
+    // `rows`: lane k holds the packed row of the warp's step k; `any`: is there one to load?
     __device__ __forceinline__ void load(int lane, unsigned rows, int stage, bool any = true)
     {
         if (STAGED && !any) {       // (a branch around loads into registers would wait for them)
@@ -320,7 +342,7 @@ template <typename T, int ROWS, int G> struct RowTile {
         char* to = in + stage + lane / LR * RB + at;
 #pragma unroll
         for (int k = 0; k < S; k += RI) {
-            const unsigned row = __shfl_sync(0xffffffffu, rows, k + lane / LR);
+            const unsigned row = __shfl_sync(0xffffffffu, rows, step(lane, k));
 #pragma unroll
             for (int x = 0; x < G; ++x) {
                 const char* from = src[x] + (uint64_t)row * ld[x];
@@ -368,9 +390,11 @@ template <typename T, int ROWS, int G> struct RowTile {
 };
 
 GlrRows glr_rows(const GlrArgs& a, int elem);
+// Packed rows' groups of a warp: 64 places by 16 or 32 units.
+inline int glr_groups(int H) { return H > 16 ? 2 : 4; }
 // Whether to cut sequences into pieces that run side by side, and how long: fills the pieces' fields.
 // `ctas` is what an SM holds of the scan kernel, `scratch` the caller's (null: uncut).
-void glr_cut(const Plan& p, int V, int ctas, void* scratch, GlrArgs* a);
+void glr_cut(const Plan& p, int V, int ctas, void* scratch, GlrArgs* a);      // (groups set)
 size_t glr_scratch(const Plan& p, const lstm_glr_shape& s);
 // Whether each warp takes a sequence of its own (uncut: fills the pieces' fields).
 bool glr_short(const Plan& p, int V, int ctas, GlrArgs* a);
@@ -378,36 +402,21 @@ bool glr_short(const Plan& p, int V, int ctas, GlrArgs* a);
 lstm_status launch_glr_fwd(const Plan& p, const lstm_glr_shape& s, GlrArgs a, void* scratch, cudaStream_t cs);
 lstm_status launch_glr_bwd(const Plan& p, const lstm_glr_shape& s, GlrArgs a, void* scratch, cudaStream_t cs);
 
-// One launch of `fn` over all pieces, directions and blocks of units.  `ready`: a bit for each
-// device whose shared-memory limit is raised.
-template <typename F>
-lstm_status glr_launch(const Plan& p, F* fn, const GlrArgs& a, int V, size_t smem, std::atomic<uint64_t>& ready,
-                       cudaStream_t cs)
+// One launch of `fn` over all pieces, directions and blocks of units: an item a CTA, or (WARPS, the
+// kernel then takes their number too) an item a warp.  `ready`: a bit for each device whose
+// shared-memory limit is raised.
+template <bool WARPS = false, typename F>
+lstm_status glr_launch(const Plan& p, F* fn, const GlrArgs& a, int V, size_t smem, std::atomic<uint64_t>& ready, cudaStream_t cs)
 {
     const int64_t items = (int64_t)ceil_div(a.H, 32 * V) * a.ndir * a.count;
-    if (items > INT32_MAX) return LSTM_ERR_UNSUPPORTED;
+    if (items > INT32_MAX - kGlrWarps) return LSTM_ERR_UNSUPPORTED;
     const uint64_t bit = 1ull << (p.device & 63);
     if (!(ready.load(std::memory_order_acquire) & bit)) {
         LSTM_CUDA_TRY(cudaFuncSetAttribute((const void*)fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
         if (p.device < 64) ready.fetch_or(bit, std::memory_order_release);
     }
-    fn<<<(unsigned)items, 32 * kGlrWarps, smem, cs>>>(a);
-    trace_end(p, -1, cs, 1);
-    return cudaGetLastError() == cudaSuccess ? LSTM_OK : LSTM_ERR_CUDA;
-}
-
-// The same for a kernel whose warps take an item each.
-template <typename F>
-lstm_status glr_launch_warps(const Plan& p, F* fn, const GlrArgs& a, int V, size_t smem, std::atomic<uint64_t>& ready, cudaStream_t cs)
-{
-    const int64_t items = (int64_t)ceil_div(a.H, 32 * V) * a.ndir * a.count;
-    if (items > INT32_MAX) return LSTM_ERR_UNSUPPORTED;
-    const uint64_t bit = 1ull << (p.device & 63);
-    if (!(ready.load(std::memory_order_acquire) & bit)) {
-        LSTM_CUDA_TRY(cudaFuncSetAttribute((const void*)fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
-        if (p.device < 64) ready.fetch_or(bit, std::memory_order_release);
-    }
-    fn<<<(unsigned)((items + kGlrWarps - 1) / kGlrWarps), 32 * kGlrWarps, smem, cs>>>(a, (int)items);
+    if constexpr (WARPS) fn<<<(unsigned)((items + kGlrWarps - 1) / kGlrWarps), 32 * kGlrWarps, smem, cs>>>(a, (int)items);
+    else fn<<<(unsigned)items, 32 * kGlrWarps, smem, cs>>>(a);
     trace_end(p, -1, cs, 1);
     return cudaGetLastError() == cudaSuccess ? LSTM_OK : LSTM_ERR_CUDA;
 }
@@ -431,13 +440,28 @@ struct Place {
         const int blocks = (p.H + 32 * V - 1) / (32 * V);
         return (WarpMap<V>*)p.maps + ((int64_t)(first + k) * p.ndir + d) * blocks + block;
     }
-    // packed row of step s + lane % 8 of the direction's order (of the last step, past the end)
-    __device__ __forceinline__ unsigned row_of(const GlrArgs& p, int s, int lane) const
+    // packed row of step s + lane % 8 of the direction's order (of the last step, past the end); the
+    // next group of 8 is `gap` steps on
+    __device__ __forceinline__ unsigned row_of(const GlrArgs& p, int s, int lane, int gap) const
     {
-        s = max(0, min(s + lane % kGlrSteps, len - 1));
+        s = max(0, min(s + lane % kGlrSteps + lane / kGlrSteps * gap, len - 1));
         return (unsigned)(__ldg(p.off + (d ? len - 1 - s : s)) + j);
     }
 };
+
+// Maps of a warp's groups of lanes (`lanes` each), composed over the groups up to (UP) or from each one's: what a group's
+// own comes to behind (before) the others.  The total is the last (first) group's.
+template <bool UP, int V> __device__ __forceinline__ void compose_groups(int lane, int lanes, Vals<V>& A, Vals<V>& U)
+{
+    for (int o = lanes; o < 32; o *= 2) {
+        const Vals<V> a = A.from(UP ? lane - o : lane + o);
+        Vals<V> u = U.from(UP ? lane - o : lane + o);
+        if (UP ? lane < o : lane + o >= 32) continue;
+        u.mad(A, U);
+        U = u;
+        A.mul(a);
+    }
+}
 
 template <int V> __device__ __forceinline__ void identity(Vals<V>& A, Vals<V>& U)
 {

@@ -39,7 +39,7 @@ template <typename T, int ROWS, int G> __device__ __forceinline__ RowTile<T, ROW
     for (int x = 0; x < G - 1; ++x) t.ld[x] = (unsigned)p.ld * (unsigned)e;
     t.src[G - 1] = (const char*)p.dy + ((int64_t)c.d * p.H + c.u0) * e;
     t.ld[G - 1] = (unsigned)(p.ndir * p.H) * (unsigned)e;
-    t.place(lane, (p.H - c.u0) * (int)e);
+    t.place(lane, (p.H - c.u0) * (int)e, p.groups);
     return t;
 }
 
@@ -108,13 +108,16 @@ __global__ void __launch_bounds__(32 * kGlrWarps, BwdTile<T, GATED, ROWS>::CTAS)
     const int lane = threadIdx.x % 32, w = threadIdx.x / 32;
     // cut sequences: the pieces whose maps were formed last are the ones still in L2
     const Place c(p, p.cut ? gridDim.x - 1 - blockIdx.x : blockIdx.x, 32 * V);
-    const int u = c.u0 + lane * V, len = c.len;
+    auto tile = error_rows<T, ROWS, G>(p, c, lane);
+    // (packed: groups of lanes hold the same units, a group's 8 steps after the other's)
+    constexpr int GAP = C::PACKED ? S : 0;
+    const int groups = C::PACKED ? p.groups : 1, g = tile.group(lane), ul = tile.unit_lane(lane), chunk = groups * kScanChunk;
+    const int u = c.u0 + ul * V, len = c.len;
     const bool live = u < p.H;
     const int64_t state = ((int64_t)c.d * p.B + p.perm[c.j]) * p.H + u;
-    auto tile = error_rows<T, ROWS, G>(p, c, lane);
     tile.in = smem + w * C::BYTES;
     const unsigned gld = (unsigned)p.gld * (unsigned)sizeof(T);
-    const int64_t to = (c.d * p.gdstride + c.u0) * (int64_t)sizeof(T) + tile.at;
+    const int64_t to = (c.d * p.gdstride + c.u0) * (int64_t)sizeof(T) + tile.col();
     char* grad[G - 1];
     grad[0] = (char*)p.df + to;
     grad[1] = (char*)p.dz + to;
@@ -124,12 +127,12 @@ __global__ void __launch_bounds__(32 * kGlrWarps, BwdTile<T, GATED, ROWS>::CTAS)
     const int begin = p.cut ? c.piece * p.piece : 0, end = p.cut ? min(len, begin + p.piece) : len;
 
     if (len > 0) {
-        int base = (end - 1) / kScanChunk * kScanChunk;
+        int base = (end - 1) / chunk * chunk;
         unsigned rows[NS + 2];          // of the iterations from this one on
 #pragma unroll
-        for (int q = 0; q < NS + 2; ++q) rows[q] = c.row_of(p, base + w * S - q * kScanChunk, lane);
+        for (int q = 0; q < NS + 2; ++q) rows[q] = c.row_of(p, base + w * S * groups - q * chunk, lane, GAP);
 #pragma unroll
-        for (int q = 0; q < NS; ++q) tile.load(lane, rows[q], q * C::STAGE);
+        for (int q = 0; q < NS; ++q) tile.load(lane, rows[q], q * C::STAGE, !C::BOUNDED || base - q * chunk >= begin);
         // the states kept before each 64 steps
         const float* kept = p.ws + ((int64_t)(p.chunk[c.j] + base / kScanChunk) * p.ndir + c.d) * p.H + (live ? u : 0);
         Vals<V> start;
@@ -143,21 +146,21 @@ __global__ void __launch_bounds__(32 * kGlrWarps, BwdTile<T, GATED, ROWS>::CTAS)
 #pragma unroll 4
             for (int k = w * share; k < min(n, (w + 1) * share); ++k) {
                 Vals<V> a, b;
-                c.map<V>(p, last - k)->get(lane, a, b);
+                c.map<V>(p, last - k)->get(ul, a, b);
                 U.mad(a, b);
                 A.mul(a);
             }
-            now[w].put(lane, A, U);
+            now[w].put(ul, A, U);
             __syncthreads();
 #pragma unroll
-            for (int x = 0; x < W; ++x) now[x].apply(lane, e);
+            for (int x = 0; x < W; ++x) now[x].apply(ul, e);
         }
         identity(A, U);
-        before[w].put(lane, A, U);
+        before[w].put(ul, A, U);
         __syncthreads();
         int stage = 0;
-        for (; base >= begin; base -= kScanChunk) {
-            const int s0 = base + w * S;
+        for (; base >= begin; base -= chunk) {
+            const int s0 = base + w * S * groups, mine = s0 + g * S;
             if (C::STAGED) {
                 cp_async_wait<NS - 1>();
                 __syncwarp();
@@ -165,13 +168,13 @@ __global__ void __launch_bounds__(32 * kGlrWarps, BwdTile<T, GATED, ROWS>::CTAS)
                 tile.stash(lane);
                 tile.load(lane, rows[1], 0);
             }
-            if (s0 + S > len) {         // past the end no error enters
-                for (int k = max(0, len - s0); k < S; ++k)
+            if (s0 + S * groups > len) {        // past the end no error enters
+                for (int k = max(0, len - mine); k < S; ++k)
                     for (int x = 0; x < C::OWN; x += (int)sizeof(T)) *(T*)(tile.slot(lane, DY, k, stage) + x) = from_f32<T>(0.f);
                 __syncwarp();
             }
             Vals<V> a[S], n[S], b[S];               // a, 1 - a, b
-            step_parts<GATED>(tile, lane, stage, len - s0, a, n, b);
+            step_parts<GATED>(tile, lane, stage, len - mine, a, n, b);
             A = a[0];
             U = b[0];
 #pragma unroll
@@ -179,7 +182,18 @@ __global__ void __launch_bounds__(32 * kGlrWarps, BwdTile<T, GATED, ROWS>::CTAS)
                 U.mad(a[k], b[k]);
                 A.mul(a[k]);
             }
-            now[3 * W + w].put(lane, A, U);
+            Vals<V> AH, UH, AE;     // packed: of the steps before and after this group's
+            if constexpr (C::PACKED) {
+                AH = AE = A;
+                UH = U;
+                compose_groups<true>(lane, tile.lanes, AH, UH);
+                if (g == groups - 1) now[3 * W + w].put(ul, AH, UH);
+                AH = AH.from(lane - tile.lanes);
+                UH = UH.from(lane - tile.lanes);
+                if (g == 0) identity(AH, UH);
+            } else {
+                now[3 * W + w].put(lane, A, U);
+            }
             U = tile.held(lane, DY, S - 1, stage);
             U.mul(a[S - 1]);
 #pragma unroll
@@ -187,18 +201,30 @@ __global__ void __launch_bounds__(32 * kGlrWarps, BwdTile<T, GATED, ROWS>::CTAS)
                 U.add(tile.held(lane, DY, k, stage));
                 U.mul(a[k]);
             }
-            now[w].put(lane, A, U);
+            if constexpr (C::PACKED) {
+                compose_groups<false>(lane, tile.lanes, AE, U);
+                if (g == 0) now[w].put(ul, AE, U);
+                AE = AE.from(lane + tile.lanes);
+                U = U.from(lane + tile.lanes);
+                if (g == groups - 1) identity(AE, U);
+            } else {
+                now[w].put(lane, A, U);
+            }
             Vals<V> h = start;
             if (base > begin) {
-                kept -= (int64_t)p.ndir * p.H;
+                kept -= (int64_t)groups * p.ndir * p.H;
                 start.each([&](int v) { return live ? __ldg(kept + v) : 0.f; });
             }
             __syncthreads();
 #pragma unroll
-            for (int x = 1; x < W; ++x) (w - x >= 0 ? before + w - x : now + w - x + W)->apply(lane, e);
+            for (int x = 1; x < W; ++x) (w - x >= 0 ? before + w - x : now + w - x + W)->apply(ul, e);
 #pragma unroll
             for (int x = 0; x < W - 1; ++x)
-                if (x < w) now[3 * W + x].apply(lane, h);
+                if (x < w) now[3 * W + x].apply(ul, h);
+            if constexpr (C::PACKED) {
+                h.mad(AH, UH);
+                e.mad(AE, U);
+            }
             before = now;
             now = now == s_map + 2 * W ? s_map : now + W;
 #pragma unroll
@@ -226,29 +252,30 @@ __global__ void __launch_bounds__(32 * kGlrWarps, BwdTile<T, GATED, ROWS>::CTAS)
                     }
                 }
             }
+            if constexpr (C::PACKED) e = e.from(ul);
             if constexpr (C::STAGED) {
                 __syncwarp();
 #pragma unroll
                 for (int k = 0; k < S; k += C::RI) {
-                    const int s = k + lane / C::LR;
+                    const int s = tile.step(lane, k);
                     const uint64_t row = (uint64_t)__shfl_sync(0xffffffffu, rows_now, s) * gld;
 #pragma unroll
                     for (int x = 0; x < G - 1; ++x) {
-                        const uint4 q = *(const uint4*)(tile.in + stage + (x * S + s) * C::RB + tile.at);
+                        const uint4 q = *(const uint4*)(tile.in + stage + (x * S + k + lane / C::LR) * C::RB + tile.at);
                         if (s < m) *(uint4*)(grad[x] + row) = q;
                     }
                 }
                 __syncwarp();
-                tile.load(lane, rows[NS], stage);
+                tile.load(lane, rows[NS], stage, !C::BOUNDED || base - NS * chunk >= begin);
                 stage = stage == (NS - 1) * C::STAGE ? 0 : stage + C::STAGE;
             }
 #pragma unroll
             for (int q = 0; q < NS + 1; ++q) rows[q] = rows[q + 1];
-            rows[NS + 1] = c.row_of(p, s0 - (NS + 2) * kScanChunk, lane);
+            rows[NS + 1] = c.row_of(p, s0 - (NS + 2) * chunk, lane, GAP);
         }
         if (C::STAGED) cp_async_wait<0>();
     }
-    if (p.dh0 && live && w == 0 && c.piece == 0)
+    if (p.dh0 && live && g == 0 && w == 0 && c.piece == 0)
 #pragma unroll
         for (int v = 0; v < V; ++v) p.dh0[state + v] = e.get(v);
     if (p.padded && tile.writes && c.piece == 0)        // the padded comparator's rows past the end
@@ -288,7 +315,7 @@ __global__ void __launch_bounds__(32 * kGlrWarps, 2) glr_bwd_short_kernel(const 
     tile.in = smem + w * C::WARP;
     Vals<V>* const before = (Vals<V>*)(tile.in + NS * C::BYTES) + lane;     // [tile][lane]: states before the tiles
     const unsigned gld = (unsigned)p.gld * (unsigned)sizeof(T);
-    const int64_t to = (c.d * p.gdstride + c.u0) * (int64_t)sizeof(T) + tile.at;
+    const int64_t to = (c.d * p.gdstride + c.u0) * (int64_t)sizeof(T) + tile.col();
     char* grad[G - 1];
     grad[0] = (char*)p.df + to;
     grad[1] = (char*)p.dz + to;
@@ -307,7 +334,7 @@ __global__ void __launch_bounds__(32 * kGlrWarps, 2) glr_bwd_short_kernel(const 
             auto first = [&](int x) { return base + (sweep == 0 ? x : tiles - 1 - x) * S; };     // step of the x-th tile
             unsigned rows[NS + 2];
 #pragma unroll
-            for (int q = 0; q < NS + 2; ++q) rows[q] = c.row_of(p, first(q), lane);
+            for (int q = 0; q < NS + 2; ++q) rows[q] = c.row_of(p, first(q), lane, 0);
 #pragma unroll
             for (int q = 0; q < NS; ++q) tile.load(lane, rows[q], q * C::BYTES, q < count);
             int stage = 0;
@@ -378,7 +405,7 @@ __global__ void __launch_bounds__(32 * kGlrWarps, 2) glr_bwd_short_kernel(const 
                 }
 #pragma unroll
                 for (int q = 0; q < NS + 1; ++q) rows[q] = rows[q + 1];
-                rows[NS + 1] = c.row_of(p, first(x + NS + 2), lane);
+                rows[NS + 1] = c.row_of(p, first(x + NS + 2), lane, 0);
             }
             if (C::STAGED) cp_async_wait<0>();
         }
@@ -399,7 +426,8 @@ template <typename T, int ROWS> struct BwdMapTile : RowTile<T, ROWS, 2> {
     typedef RowTile<T, ROWS, 2> R;
     static constexpr int W = kGlrWarps;
     static constexpr int STAGE = R::STAGED ? W * R::BYTES : 0;
-    static constexpr int NS = !R::STAGED || 2 * STAGE > 72 * 1024 ? 1 : 2;
+    static constexpr int FIT = 72 * 1024 / (STAGE + 1);
+    static constexpr int NS = !R::STAGED ? 1 : FIT < 2 ? 2 : FIT > 4 ? 4 : FIT;
     static constexpr int SMEM = NS * STAGE;
 };
 
@@ -419,15 +447,17 @@ __global__ void __launch_bounds__(32 * kGlrWarps, 3) glr_bwd_map_kernel(const Gl
     tile.ld[0] = (unsigned)p.ld * (unsigned)el;
     tile.src[1] = (const char*)p.dy + ((int64_t)c.d * p.H + c.u0) * el;
     tile.ld[1] = (unsigned)(p.ndir * p.H) * (unsigned)el;
-    tile.place(lane, (p.H - c.u0) * (int)el);
+    tile.place(lane, (p.H - c.u0) * (int)el, p.groups);
     tile.in = smem + w * C::BYTES;
-    const int first = c.piece * p.piece + w * (p.piece / W);
-    int s0 = first + p.piece / W - S;
-    unsigned rows[NS + 1];
+    // (packed: each group of lanes its own part of the warp's)
+    const int groups = C::PACKED ? p.groups : 1, part = p.piece / (W * groups), gap = C::PACKED ? part : 0;
+    const int g = tile.group(lane), ul = tile.unit_lane(lane), first = c.piece * p.piece + w * groups * part;
+    int s0 = first + part - S;
+    unsigned rows[NS + 2];
 #pragma unroll
-    for (int q = 0; q < NS + 1; ++q) rows[q] = c.row_of(p, s0 - q * S, lane);
+    for (int q = 0; q < NS + 2; ++q) rows[q] = c.row_of(p, s0 - q * S, lane, gap);
 #pragma unroll
-    for (int q = 0; q < NS; ++q) tile.load(lane, rows[q], q * C::STAGE);
+    for (int q = 0; q < NS; ++q) tile.load(lane, rows[q], q * C::STAGE, s0 - q * S >= first);
     Vals<V> A, U;
     identity(A, U);
     int stage = 0;
@@ -445,38 +475,43 @@ __global__ void __launch_bounds__(32 * kGlrWarps, 3) glr_bwd_map_kernel(const Gl
             d[k].each([&](int v) { return rd.get(v); });
         }
         if (C::STAGED) __syncwarp();
-        tile.load(lane, rows[NS], stage);
-        rows[NS] = c.row_of(p, s0 - (NS + 1) * S, lane);
+        tile.load(lane, rows[NS], stage, s0 - NS * S >= first);
+#pragma unroll
+        for (int q = 0; q < NS + 1; ++q) rows[q] = rows[q + 1];
+        rows[NS + 1] = c.row_of(p, s0 - (NS + 2) * S, lane, gap);
         stage = stage == (NS - 1) * C::STAGE ? 0 : stage + C::STAGE;
 #pragma unroll
         for (int k = S - 1; k >= 0; --k) {
-            if (s0 + k >= c.len) continue;
+            if (s0 + g * gap + k >= c.len) continue;
             U.add(d[k]);
             U.mul(a[k]);
             A.mul(a[k]);
         }
     }
     if (C::STAGED) cp_async_wait<0>();
-    s_map[w].put(lane, A, U);
+    if constexpr (C::PACKED) compose_groups<false>(lane, tile.lanes, A, U);
+    if (g == 0) s_map[w].put(ul, A, U);
     __syncthreads();
     if (w < W - 1) return;
+    s_map[w].get(ul, A, U);
     for (int x = W - 2; x >= 0; --x) {
         Vals<V> a, b;
-        s_map[x].get(lane, a, b);
+        s_map[x].get(ul, a, b);
         U.mad(a, b);
         A.mul(a);
     }
-    c.map<V>(p, c.piece)->put(lane, A, U);
+    c.map<V>(p, c.piece)->put(ul, A, U);
 }
 
 template <typename T, bool GATED, int ROWS>
 lstm_status go(const Plan& p, GlrArgs a, void* scratch, cudaStream_t cs)
 {
-    static std::atomic<uint64_t> ready{0}, ready_map{0};
+    static std::atomic<uint64_t> ready{0}, ready_map{0}, ready_short{0};
     typedef BwdTile<T, GATED, ROWS> C;
-    typedef BwdShortTile<T, GATED, ROWS> Q;
-    static std::atomic<uint64_t> ready_short{0};
-    if (glr_short(p, C::V, Q::CTAS, &a)) return glr_launch_warps(p, glr_bwd_short_kernel<T, GATED, ROWS>, a, C::V, Q::SMEM, ready_short, cs);
+    constexpr int ALONE = ROWS == GLR_PACKED ? GLR_WIDE : ROWS;     // a warp a sequence: one group
+    typedef BwdShortTile<T, GATED, ALONE> Q;
+    if (glr_short(p, C::V, Q::CTAS, &a)) return glr_launch<true>(p, glr_bwd_short_kernel<T, GATED, ALONE>, a, C::V, Q::SMEM, ready_short, cs);
+    if (C::PACKED) a.groups = glr_groups(a.H);
     glr_cut(p, C::V, C::CTAS, scratch, &a);
     if (a.cut) {
         const lstm_status st = glr_launch(p, glr_bwd_map_kernel<T, ROWS>, a, C::V, BwdMapTile<T, ROWS>::SMEM, ready_map, cs);
@@ -490,6 +525,7 @@ lstm_status go(const Plan& p, const GlrArgs& a, void* scratch, cudaStream_t cs)
 {
     const GlrRows rows = glr_rows(a, (int)sizeof(T));
     if (rows == GLR_WIDE) return go<T, GATED, GLR_WIDE>(p, a, scratch, cs);
+    if (rows == GLR_PACKED) return go<T, GATED, GLR_PACKED>(p, a, scratch, cs);
     if constexpr (sizeof(T) == 2)
         if (rows == GLR_SINGLE) return go<T, GATED, GLR_SINGLE>(p, a, scratch, cs);
     return go<T, GATED, GLR_NARROW>(p, a, scratch, cs);

@@ -59,14 +59,14 @@ template <int V> __device__ __forceinline__ void compose(const Vals<V> (&a)[kGlr
 }
 
 // 8 rows of y that a warp has staged at `out` ([step][RB]), to memory in 16-byte pieces.
-template <typename Tile> __device__ __forceinline__ void flush_rows(const char* out, int lane, int at, char* y, unsigned yld, unsigned rows, int n)
+template <typename Tile> __device__ __forceinline__ void flush_rows(const Tile& t, const char* out, int lane, char* y, unsigned yld, unsigned rows, int n)
 {
     __syncwarp();
 #pragma unroll
     for (int k = 0; k < kGlrSteps; k += Tile::RI) {
-        const int s = k + lane / Tile::LR;
+        const int s = t.step(lane, k);
         const unsigned row = __shfl_sync(0xffffffffu, rows, s);
-        const uint4 q = *(const uint4*)(out + s * Tile::RB + at);
+        const uint4 q = *(const uint4*)(out + (k + lane / Tile::LR) * Tile::RB + t.at);
         if (s < n) *(uint4*)(y + (uint64_t)row * yld) = q;
     }
 }
@@ -80,7 +80,7 @@ template <typename T, int ROWS, int G> __device__ __forceinline__ RowTile<T, ROW
     if (G == 3) t.src[G - 1] = (const char*)p.i + from;
 #pragma unroll
     for (int x = 0; x < G; ++x) t.ld[x] = (unsigned)p.ld * (unsigned)sizeof(T);
-    t.place(lane, (p.H - c.u0) * (int)sizeof(T));
+    t.place(lane, (p.H - c.u0) * (int)sizeof(T), p.groups);
     return t;
 }
 
@@ -111,7 +111,8 @@ template <typename T, bool GATED, int ROWS> struct MapTile : RowTile<T, ROWS, GA
     typedef RowTile<T, ROWS, GATED ? 3 : 2> R;
     static constexpr int W = kGlrWarps;
     static constexpr int STAGE = R::STAGED ? W * R::BYTES : 0;
-    static constexpr int NS = !R::STAGED || 2 * STAGE > 72 * 1024 ? 1 : 2;
+    static constexpr int FIT = 72 * 1024 / (STAGE + 1);
+    static constexpr int NS = !R::STAGED ? 1 : FIT < 2 ? 2 : FIT > 4 ? 4 : FIT;
     static constexpr int SMEM = NS * STAGE;
 };
 
@@ -125,25 +126,28 @@ __global__ void __launch_bounds__(32 * kGlrWarps, FwdTile<T, GATED, ROWS>::CTAS)
     const int lane = threadIdx.x % 32, w = threadIdx.x / 32;
     // cut sequences: the pieces whose maps were formed last are the ones still in L2
     const Place c(p, p.cut ? gridDim.x - 1 - blockIdx.x : blockIdx.x, 32 * V);
-    const int u = c.u0 + lane * V, len = c.len;
+    auto tile = gate_rows<T, ROWS, GATED ? 3 : 2>(p, c, lane);
+    // (packed: groups of lanes hold the same units, a group's 8 steps after the other's)
+    constexpr int GAP = C::PACKED ? S : 0;
+    const int groups = C::PACKED ? p.groups : 1, g = tile.group(lane), ul = tile.unit_lane(lane), chunk = groups * kScanChunk;
+    const int u = c.u0 + ul * V, len = c.len;
     const bool live = u < p.H;
     const int64_t state = ((int64_t)c.d * p.B + p.perm[c.j]) * p.H + u;
-    auto tile = gate_rows<T, ROWS, GATED ? 3 : 2>(p, c, lane);
     tile.in = smem + w * C::BYTES;
     char* const out = smem + NS * C::STAGE + w * (S * C::RB);
     const unsigned yld = (unsigned)(p.ndir * p.H) * (unsigned)sizeof(T);
-    char* y = (char*)p.y + ((int64_t)c.d * p.H + c.u0) * (int64_t)sizeof(T) + tile.at;
+    char* y = (char*)p.y + ((int64_t)c.d * p.H + c.u0) * (int64_t)sizeof(T) + tile.col();
     Vals<V> h;
     h.each([&](int v) { return live && p.h0 ? p.h0[state + v] : 0.f; });
     const int begin = c.piece * (p.cut ? p.piece : 0), end = p.cut ? min(len, begin + p.piece) : len;
 
     if (len > 0) {
-        int s0 = begin + w * S;
+        int s0 = begin + w * S * groups;
         unsigned rows[NS + 2];          // of the iterations from this one on
 #pragma unroll
-        for (int q = 0; q < NS + 2; ++q) rows[q] = c.row_of(p, s0 + q * kScanChunk, lane);
+        for (int q = 0; q < NS + 2; ++q) rows[q] = c.row_of(p, s0 + q * chunk, lane, GAP);
 #pragma unroll
-        for (int q = 0; q < NS; ++q) tile.load(lane, rows[q], q * C::STAGE);
+        for (int q = 0; q < NS; ++q) tile.load(lane, rows[q], q * C::STAGE, !C::BOUNDED || begin + q * chunk < end);
         // maps of this iteration and of the one before (nothing, at first); a third set, as a warp
         // may write the next iteration's while another still reads these two
         WarpMap<V>*now = s_map, *before = s_map + 2 * W;
@@ -155,42 +159,52 @@ __global__ void __launch_bounds__(32 * kGlrWarps, FwdTile<T, GATED, ROWS>::CTAS)
 #pragma unroll 4
             for (int k = w * share; k < last; ++k) {
                 Vals<V> a, b;
-                c.map<V>(p, k)->get(lane, a, b);
+                c.map<V>(p, k)->get(ul, a, b);
                 U.mad(a, b);
                 A.mul(a);
             }
-            now[w].put(lane, A, U);
+            now[w].put(ul, A, U);
             __syncthreads();
 #pragma unroll
-            for (int x = 0; x < W; ++x) now[x].apply(lane, h);
+            for (int x = 0; x < W; ++x) now[x].apply(ul, h);
         }
         identity(A, U);
-        before[w].put(lane, A, U);
+        before[w].put(ul, A, U);
         __syncthreads();
         int stage = 0;
-        for (; s0 - w * S < end; s0 += kScanChunk) {
+        for (int base = begin; base < end; base += chunk, s0 += chunk) {
+            const int mine = s0 + g * S;
             Vals<V> a[S], b[S];
             if (C::STAGED) {
                 cp_async_wait<NS - 1>();
                 __syncwarp();
             }
-            step_maps<RowTile<T, ROWS, GATED ? 3 : 2>, GATED>(tile, lane, stage, len - s0, a, b);
+            step_maps<RowTile<T, ROWS, GATED ? 3 : 2>, GATED>(tile, lane, stage, len - mine, a, b);
             if (C::STAGED) __syncwarp();
-            tile.load(lane, rows[NS], stage);
+            tile.load(lane, rows[NS], stage, !C::BOUNDED || base + NS * chunk < end);
             stage = stage == (NS - 1) * C::STAGE ? 0 : stage + C::STAGE;
             const unsigned rows_now = rows[0];
 #pragma unroll
             for (int q = 0; q < NS + 1; ++q) rows[q] = rows[q + 1];
-            rows[NS + 1] = c.row_of(p, s0 + (NS + 2) * kScanChunk, lane);
+            rows[NS + 1] = c.row_of(p, s0 + (NS + 2) * chunk, lane, GAP);
             compose<V>(a, b, A, U);
-            now[w].put(lane, A, U);
+            if constexpr (C::PACKED) {
+                compose_groups<true>(lane, tile.lanes, A, U);
+                if (g == groups - 1) now[w].put(ul, A, U);
+                A = A.from(lane - tile.lanes);      // of the groups before this one
+                U = U.from(lane - tile.lanes);
+                if (g == 0) identity(A, U);
+            } else {
+                now[w].put(lane, A, U);
+            }
             __syncthreads();
 #pragma unroll
-            for (int x = 1; x < W; ++x) (w + x < W ? before + w + x : now + w + x - W)->apply(lane, h);
+            for (int x = 1; x < W; ++x) (w + x < W ? before + w + x : now + w + x - W)->apply(ul, h);
+            if constexpr (C::PACKED) h.mad(A, U);
             before = now;
             now = now == s_map + 2 * W ? s_map : now + W;
-            if (w == 0 && p.ws && live) {
-                float* ws = p.ws + ((int64_t)(p.chunk[c.j] + s0 / kScanChunk) * p.ndir + c.d) * p.H + u;
+            if ((C::PACKED ? mine % kScanChunk == 0 && mine < len : w == 0) && p.ws && live) {
+                float* ws = p.ws + ((int64_t)(p.chunk[c.j] + mine / kScanChunk) * p.ndir + c.d) * p.H + u;
 #pragma unroll
                 for (int v = 0; v < V; ++v) ws[v] = h.get(v);
             }
@@ -205,11 +219,12 @@ __global__ void __launch_bounds__(32 * kGlrWarps, FwdTile<T, GATED, ROWS>::CTAS)
                     if (k < n) store_values<T, V>(y + (uint64_t)row * yld, h);
                 }
             }
-            if constexpr (C::STAGED) flush_rows<C>(out, lane, tile.at, y, yld, rows_now, n);
+            if constexpr (C::PACKED) h = h.from((groups - 1) * tile.lanes + ul);
+            if constexpr (C::STAGED) flush_rows(tile, out, lane, y, yld, rows_now, n);
         }
         if (C::STAGED) cp_async_wait<0>();
     }
-    if (p.h_n && live && w == W - 1 && end == len)
+    if (p.h_n && live && g == 0 && w == W - 1 && end == len)
 #pragma unroll
         for (int v = 0; v < V; ++v) p.h_n[state + v] = h.get(v);
     if (p.padded && tile.writes && c.piece == 0) zero_past_end<T, C::WIDTH>(p, c, y, yld, w, W);
@@ -244,12 +259,12 @@ __global__ void __launch_bounds__(32 * kGlrWarps, 3) glr_fwd_short_kernel(const 
     tile.in = smem + w * C::WARP;
     char* const out = tile.in + (C::STAGED ? NS * C::BYTES : 0);
     const unsigned yld = (unsigned)(p.ndir * p.H) * (unsigned)sizeof(T);
-    char* y = (char*)p.y + ((int64_t)c.d * p.H + c.u0) * (int64_t)sizeof(T) + tile.at;
+    char* y = (char*)p.y + ((int64_t)c.d * p.H + c.u0) * (int64_t)sizeof(T) + tile.col();
     Vals<V> h;
     if (len > 0) {
         unsigned rows[NS + 2];          // of the tiles from this one on
 #pragma unroll
-        for (int q = 0; q < NS + 2; ++q) rows[q] = c.row_of(p, q * S, lane);
+        for (int q = 0; q < NS + 2; ++q) rows[q] = c.row_of(p, q * S, lane, 0);
 #pragma unroll
         for (int q = 0; q < NS; ++q) tile.load(lane, rows[q], q * C::BYTES, q * S < len);
         h.each([&](int v) { return live && p.h0 ? p.h0[state + v] : 0.f; });
@@ -267,7 +282,7 @@ __global__ void __launch_bounds__(32 * kGlrWarps, 3) glr_fwd_short_kernel(const 
             const unsigned rows_now = rows[0];
 #pragma unroll
             for (int q = 0; q < NS + 1; ++q) rows[q] = rows[q + 1];
-            rows[NS + 1] = c.row_of(p, s0 + (NS + 2) * S, lane);
+            rows[NS + 1] = c.row_of(p, s0 + (NS + 2) * S, lane, 0);
             if (p.ws && live && s0 % kScanChunk == 0) {
                 float* ws = p.ws + ((int64_t)(p.chunk[c.j] + s0 / kScanChunk) * p.ndir + c.d) * p.H + u;
 #pragma unroll
@@ -284,7 +299,7 @@ __global__ void __launch_bounds__(32 * kGlrWarps, 3) glr_fwd_short_kernel(const 
                     if (k < n) store_values<T, V>(y + (uint64_t)row * yld, h);
                 }
             }
-            if constexpr (C::STAGED) flush_rows<C>(out, lane, tile.at, y, yld, rows_now, n);
+            if constexpr (C::STAGED) flush_rows(tile, out, lane, y, yld, rows_now, n);
         }
         if (C::STAGED) cp_async_wait<0>();
     } else {
@@ -313,13 +328,15 @@ __global__ void __launch_bounds__(32 * kGlrWarps, 3) glr_fwd_map_kernel(const Gl
     if ((int64_t)(c.piece + 1) * p.piece >= c.len) return;
     auto tile = gate_rows<T, ROWS, GATED ? 3 : 2>(p, c, lane);
     tile.in = smem + w * C::BYTES;
-    int s0 = c.piece * p.piece + w * (p.piece / W);
-    const int end = s0 + p.piece / W;
-    unsigned rows[NS + 1];
+    // (packed: each group of lanes its own part of the warp's)
+    const int groups = C::PACKED ? p.groups : 1, part = p.piece / (W * groups), gap = C::PACKED ? part : 0, ul = tile.unit_lane(lane);
+    int s0 = c.piece * p.piece + w * groups * part;
+    const int end = s0 + part;
+    unsigned rows[NS + 2];
 #pragma unroll
-    for (int q = 0; q < NS + 1; ++q) rows[q] = c.row_of(p, s0 + q * S, lane);
+    for (int q = 0; q < NS + 2; ++q) rows[q] = c.row_of(p, s0 + q * S, lane, gap);
 #pragma unroll
-    for (int q = 0; q < NS; ++q) tile.load(lane, rows[q], q * C::STAGE);
+    for (int q = 0; q < NS; ++q) tile.load(lane, rows[q], q * C::STAGE, s0 + q * S < end);
     Vals<V> A, U;
     identity(A, U);
     int stage = 0;
@@ -331,8 +348,10 @@ __global__ void __launch_bounds__(32 * kGlrWarps, 3) glr_fwd_map_kernel(const Gl
         }
         step_maps<RowTile<T, ROWS, GATED ? 3 : 2>, GATED>(tile, lane, stage, S, a, b);
         if (C::STAGED) __syncwarp();
-        tile.load(lane, rows[NS], stage);
-        rows[NS] = c.row_of(p, s0 + (NS + 1) * S, lane);
+        tile.load(lane, rows[NS], stage, s0 + NS * S < end);
+#pragma unroll
+        for (int q = 0; q < NS + 1; ++q) rows[q] = rows[q + 1];
+        rows[NS + 1] = c.row_of(p, s0 + (NS + 2) * S, lane, gap);
         stage = stage == (NS - 1) * C::STAGE ? 0 : stage + C::STAGE;
 #pragma unroll
         for (int k = 0; k < S; ++k) {
@@ -341,27 +360,30 @@ __global__ void __launch_bounds__(32 * kGlrWarps, 3) glr_fwd_map_kernel(const Gl
         }
     }
     if (C::STAGED) cp_async_wait<0>();
-    s_map[w].put(lane, A, U);
+    if constexpr (C::PACKED) compose_groups<true>(lane, tile.lanes, A, U);
+    if (tile.group(lane) == groups - 1) s_map[w].put(ul, A, U);
     __syncthreads();
     if (w > 0) return;
+    s_map[0].get(ul, A, U);
     for (int x = 1; x < W; ++x) {
         Vals<V> a, b;
-        s_map[x].get(lane, a, b);
+        s_map[x].get(ul, a, b);
         U.mad(a, b);
         A.mul(a);
     }
-    c.map<V>(p, c.piece)->put(lane, A, U);
+    c.map<V>(p, c.piece)->put(ul, A, U);
 }
 
 template <typename T, bool GATED, int ROWS>
 lstm_status go(const Plan& p, GlrArgs a, void* scratch, cudaStream_t cs)
 {
-    static std::atomic<uint64_t> ready{0}, ready_map{0};
+    static std::atomic<uint64_t> ready{0}, ready_map{0}, ready_short{0};
     typedef FwdTile<T, GATED, ROWS> C;
     typedef MapTile<T, GATED, ROWS> M;
-    typedef ShortTile<T, GATED, ROWS> Q;
-    static std::atomic<uint64_t> ready_short{0};
-    if (glr_short(p, C::V, Q::CTAS, &a)) return glr_launch_warps(p, glr_fwd_short_kernel<T, GATED, ROWS>, a, C::V, Q::SMEM, ready_short, cs);
+    constexpr int ALONE = ROWS == GLR_PACKED ? GLR_WIDE : ROWS;     // a warp a sequence: one group
+    typedef ShortTile<T, GATED, ALONE> Q;
+    if (glr_short(p, C::V, Q::CTAS, &a)) return glr_launch<true>(p, glr_fwd_short_kernel<T, GATED, ALONE>, a, C::V, Q::SMEM, ready_short, cs);
+    if (C::PACKED) a.groups = glr_groups(a.H);
     glr_cut(p, C::V, C::CTAS, scratch, &a);
     if (a.cut) {
         const lstm_status st = glr_launch(p, glr_fwd_map_kernel<T, GATED, ROWS>, a, C::V, M::SMEM, ready_map, cs);
@@ -375,6 +397,7 @@ lstm_status go(const Plan& p, const GlrArgs& a, void* scratch, cudaStream_t cs)
 {
     const GlrRows rows = glr_rows(a, (int)sizeof(T));
     if (rows == GLR_WIDE) return go<T, GATED, GLR_WIDE>(p, a, scratch, cs);
+    if (rows == GLR_PACKED) return go<T, GATED, GLR_PACKED>(p, a, scratch, cs);
     if constexpr (sizeof(T) == 2)
         if (rows == GLR_SINGLE) return go<T, GATED, GLR_SINGLE>(p, a, scratch, cs);
     return go<T, GATED, GLR_NARROW>(p, a, scratch, cs);

@@ -138,6 +138,22 @@ def test_matches_definition(case):
     Case(lens, nd, H, dtype, cell, padded, layout=layout, shift=shift).check()
 
 
+LONG, SHORT = [5000, 257, 256, 255, 129, 33, 0, 8], [700, 255, 130, 1]
+
+
+@pytest.mark.parametrize("lens,nd,H,dtype,cell,padded,layout", [
+    (LONG, 2, 8, "bf16", "gated", False, "blocks"), (LONG, 1, 16, "bf16", "tied", False, "planes"),
+    (LONG, 2, 24, "bf16", "gated", False, "dirs"), (LONG, 1, 32, "bf16", "tied", False, "blocks"),
+    (LONG, 1, 4, "f32", "tied", False, "blocks"), (LONG, 2, 16, "f32", "gated", False, "dirs"),
+    (LONG, 2, 20, "f32", "tied", False, "blocks"), (LONG, 1, 32, "f32", "gated", False, "planes"),
+    (SHORT, 2, 8, "f32", "gated", False, "blocks"), (SHORT, 1, 24, "f32", "tied", True, "blocks"),
+    (SHORT, 2, 16, "bf16", "tied", True, "dirs"), (SHORT, 1, 32, "bf16", "gated", False, "blocks"),
+    ([70] * 40 + [300] * 3, 2, 12, "f32", "gated", False, "blocks")])
+def test_narrow_layers(lens, nd, H, dtype, cell, padded, layout):
+    # at most 32 units: the lanes of a warp divide among steps, cut into pieces and not
+    Case(lens, nd, H, dtype, cell, padded, layout=layout).check()
+
+
 @pytest.mark.parametrize("bias", [-9.0, 0.0, 6.0, 12.0])
 def test_gates_near_their_ends(bias):
     # forget gates close to 0 (nothing kept) and to 1 (a memory of thousands of frames): 1 - a keeps its digits
