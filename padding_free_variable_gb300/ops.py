@@ -39,7 +39,7 @@ class Plan:
         lens = np.ascontiguousarray(np.asarray(lengths, dtype=np.int32))
         self.lengths = lens
         self.padded = padded
-        self.scratch = {}       # sizes and device buffer of the gated linear recurrence's calls, by shape
+        self.scratch = {}       # of the gated linear recurrence: sizes by shape, device buffers by shape and stream
         h = ctypes.c_void_p()
         lp = lens.ctypes.data_as(ctypes.POINTER(ctypes.c_int32))
         if segments is not None:
@@ -653,16 +653,29 @@ def _glr_gates(key, f, z, i, rows, name):
     return _lib.GlrGates(f.data_ptr(), z.data_ptr(), i.data_ptr() if gated else None, ld, ds)
 
 
-def _glr_sizes(plan: Plan, shape, device=None):
-    """Workspace bytes, and the plan's scratch for this shape (kept with the plan, whose calls share it, one stream at a
-    time)."""
+def _glr_sizes(plan: Plan, shape):
+    """Bytes of the workspace and of the scratch (kept with the plan)."""
     got = plan.scratch.get(shape.key)
-    if got is None or (got[2] and got[1] is None and device is not None):
+    if got is None:
         lib = _lib.load()
-        need = int(lib.lstm_glr_scratch_bytes(plan.handle, shape.ref))
-        buf = torch.empty(need, dtype=torch.uint8, device=device) if need and device is not None else None
-        got = plan.scratch[shape.key] = (int(lib.lstm_glr_workspace_bytes(plan.handle, shape.ref)), buf, need)
+        got = plan.scratch[shape.key] = (int(lib.lstm_glr_workspace_bytes(plan.handle, shape.ref)),
+                                         int(lib.lstm_glr_scratch_bytes(plan.handle, shape.ref)))
     return got
+
+
+def _glr_scratch(plan: Plan, key, need: int, stream: int, device):
+    """The plan's scratch for calls of this shape on this stream: calls on different streams may run at the same time."""
+    if need == 0:
+        return None
+    buf = plan.scratch.get((key, stream))
+    if buf is None:
+        if stream == torch._C._cuda_getCurrentRawStream(device.index):
+            buf = torch.empty(need, dtype=torch.uint8, device=device)
+        else:       # memory that the allocator ties to the stream that uses it
+            with torch.cuda.stream(torch.cuda.ExternalStream(stream, device)):
+                buf = torch.empty(need, dtype=torch.uint8, device=device)
+        plan.scratch[key, stream] = buf
+    return buf.data_ptr()
 
 
 def glr_workspace_bytes(plan: Plan, shape) -> int:
@@ -676,11 +689,12 @@ def glr_forward(plan: Plan, shape, f, z, i, h0, y, h_n, workspace, stream=None):
     nd, H, dt, _ = key
     g = _glr_gates(key, f, z, i, rows, "gates")
     st = (nd, plan.batch, H)
-    need, scratch, _ = _glr_sizes(plan, shape, f.device)
+    need, most = _glr_sizes(plan, shape)
+    stream = _stream_of(stream, f)
     check(_lib.load().lstm_glr_fwd(
         plan.handle, shape.ref, ctypes.byref(g), _dense(h0, torch.float32, st, "h0"), _dense(y, dt, (rows, nd, H), "y"),
         _dense(h_n, torch.float32, st, "h_n"), _bytes(workspace, need, "workspace"),
-        None if scratch is None else scratch.data_ptr(), _stream_of(stream, f)), "lstm_glr_fwd")
+        _glr_scratch(plan, key, most, stream, f.device), stream), "lstm_glr_fwd")
 
 
 def glr_backward(plan: Plan, shape, f, z, i, workspace, dy, dh_n, df, dz, di, dh0, stream=None):
@@ -690,11 +704,12 @@ def glr_backward(plan: Plan, shape, f, z, i, workspace, dy, dh_n, df, dz, di, dh
     g = _glr_gates(key, f, z, i, rows, "gates")
     dg = _glr_gates(key, df, dz, di, rows, "gate gradients")
     st = (nd, plan.batch, H)
-    need, scratch, _ = _glr_sizes(plan, shape, f.device)
+    need, most = _glr_sizes(plan, shape)
+    stream = _stream_of(stream, f)
     check(_lib.load().lstm_glr_bwd(
         plan.handle, shape.ref, ctypes.byref(g), _bytes(workspace, need, "workspace"), _dense(dy, dt, (rows, nd, H), "dy"),
         _dense(dh_n, torch.float32, st, "dh_n"), ctypes.byref(dg), _dense(dh0, torch.float32, st, "dh0"),
-        None if scratch is None else scratch.data_ptr(), _stream_of(stream, f)), "lstm_glr_bwd")
+        _glr_scratch(plan, key, most, stream, f.device), stream), "lstm_glr_bwd")
 
 
 def glr_step(shape, f, z, i, state_in, state_out, y, slots=None, stream=None):

@@ -253,6 +253,26 @@ def test_on_another_stream_and_in_a_graph():
         assert all(torch.equal(a, b) for a, b in zip(want, (c.y, c.grads[0], c.dh0)))
 
 
+def test_one_plan_on_two_streams_at_once():
+    # sequences that are cut: their pieces' maps must not be shared between the streams
+    a, b = Case([6000, 5000], 2, 64, "f32", "gated", seed=1), Case([6000, 5000], 2, 64, "f32", "gated", seed=2)
+    b.plan = a.plan
+    want = []
+    for c in (a, b):
+        c.check()
+        want.append([t.clone() for t in (c.y, c.gbuf, c.h_n, c.dh0)])
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for c, s in zip((a, b), streams):
+            c.forward(s)
+            c.backward(s)
+    torch.cuda.synchronize()
+    for c, w in zip((a, b), want):
+        for got, t in zip((c.y, c.gbuf, c.h_n, c.dh0), w):
+            assert torch.equal(got.nan_to_num(7), t.nan_to_num(7))
+
+
 def test_windows_continue_the_recurrence():
     # forward direction: window after window, each from the last one's state, is the whole scan
     lens, H = [150, 20, 333, 0], 56
