@@ -6,7 +6,13 @@
 // the deviation costs no digits.  Bound by memory: 5 values of traffic against about 20 operations.
 // A warp takes a row of up to 1024 values (no barrier; many rows an SM hide the latency), wider
 // rows take a CTA; a call of few rows spreads each over as many threads as it has groups of
-// eight, since there only the time of one row counts.
+// eight, since there only the time of one row counts (8 rows of 1024: 2.5 us in a graph).
+//
+// Measured, cold L2: 40555 x 1024 bf16 70 us, 5.9 TB/s (88 % of the copy rate; 91 us with kinds and
+// types looked up at run time); 200000 x 128 fp32 74 us, 6.9 TB/s.  Odd widths: 9564 x 517 fp32 centred
+// 38 us, 2.6 TB/s, where the sums over three warps and the rows' ends cost more than the bytes (issue
+// 52 %, memory 22 %); value by value the same rows take 64 us.  A warp a row with four groups a
+// lane, and rows 8 apart sharing a CTA's parameters, were no faster (42 us).
 #include <algorithm>
 
 #include "block_norm.cuh"

@@ -11,8 +11,6 @@ namespace lstm {
 
 constexpr int kMaxCtasPerDir = 160;     // > 152 SMs; one flag per CTA
 constexpr int kRecThreads = 256;        // block size of the recurrent kernels
-constexpr int kScanPiece = 256;         // shortest piece that a sequence is cut into where its pieces run side by side
-constexpr int kScanChunk = 64;          // steps between the states that the linear recurrence keeps for its backward pass
 
 // Device status word layout (one int64 per plan):
 //   low 32 bits  lstm_status of the first failure (0 = none)
@@ -60,18 +58,11 @@ struct Plan {
     int32_t* h_perm = nullptr;      // [B]  caller index of slot j
     int32_t* h_len = nullptr;       // [B]  length of slot j
     int32_t* h_cstart = nullptr;    // [B+1] caller-order frame offsets
-    int64_t chunks = 0;             // pieces of at most kScanChunk steps of all sequences
-    // sequences cut into pieces of kScanPiece << level steps, the last level uncut (every sequence has a piece, if an empty one)
-    int32_t levels = 0;
-    int32_t level_first[24] = {};   // first entry of the level in d_pieces
-    int32_t level_count[25] = {};
     // device tables
     int32_t* d_bs = nullptr;
     int32_t* d_off = nullptr;
     int32_t* d_perm = nullptr;
     int32_t* d_len = nullptr;
-    int4* d_pieces = nullptr;       // (slot, piece, length of the sequence, entry of the slot's first piece in its level by slot)
-    int32_t* d_chunk = nullptr;     // [B+1] first piece of each slot (pieces of kScanChunk steps)
     int32_t* d_row_src = nullptr;   // [rows] caller-order frame of packed row (-1 = padding)
     int32_t* d_prev_fwd = nullptr;  // [rows] row holding h_{t-1} for the forward direction (-1 none)
     int32_t* d_prev_rev = nullptr;  // [rows] row holding the reverse direction's previous state

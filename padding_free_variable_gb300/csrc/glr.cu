@@ -10,8 +10,11 @@ namespace lstm {
 
 namespace {
 
-// V units of a stream a thread; threads of a block: x along the units, y along the streams.  Bound
-// by memory: gates and states read once, states and outputs written once.
+// One frame of many streams: V units of a stream a thread; threads of a block: x along the units, y
+// along the streams.  Bound by memory where streams are many (gates and states read once, states
+// and outputs written once: 4096 streams of 1024 fp32 units 19 us with a cold L2, 5.2 TB/s; one unit
+// a thread and a division for the stream took 35 us), by the launch where they are few (8 streams of
+// 512 bf16 units 1.3 us in a graph, 6.8 us as a call).
 template <typename T, bool GATED, int V>
 __global__ void __launch_bounds__(128) glr_step_kernel(const GlrArgs p, const int32_t* slots, int rows, int num_slots, const float* state_in,
                                                        float* state_out)
@@ -101,12 +104,13 @@ bool right_device(const Plan& p)
 
 bool fits(const void* p, int64_t bytes) { return ((uintptr_t)p & (bytes - 1)) == 0; }
 
-GlrArgs plan_args(const Plan& p, const lstm_glr_shape& s, const lstm_glr_gates& g)
+GlrArgs plan_args(const ScanPlan& sp, const lstm_glr_shape& s, const lstm_glr_gates& g)
 {
+    const Plan& p = sp.p;
     GlrArgs a;
     a.T = p.T; a.B = p.B; a.H = s.hidden_size; a.ndir = s.num_directions;
     a.padded = p.padded ? 1 : 0;
-    a.off = p.d_off; a.len = p.d_len; a.perm = p.d_perm; a.chunk = p.d_chunk;
+    a.off = p.d_off; a.len = p.d_len; a.perm = p.d_perm; a.chunk = sp.scan.d_chunk;
     a.f = g.f; a.z = g.z; a.i = g.i; a.ld = g.row_stride; a.dstride = g.dir_stride;
     return a;
 }
@@ -147,48 +151,56 @@ static bool glr_whole(const GlrArgs& a, int elem, int64_t bytes)
 
 GlrRows glr_rows(const GlrArgs& a, int elem)
 {
+    // 40555 frames of 2 x 512 bf16 units forward / backward: wide 52 / 89 us, narrow (rows 4 bytes
+    // off) 64 / 105 us, single (2 bytes off) 85 / 154 us; 70 k frames of 2 x 256 fp32, three gates: wide
+    // 91 / 158 us, narrow 107 / 206 us.  Packed against wide: 74 sequences of 21099 frames of 8 bf16
+    // units 113 / 168 against 326 / 480 us, 60 of 19 to 211 frames of 2 x 16 units 9 / 11 against 13 / 15.
     if (glr_whole(a, elem, 16)) return a.H > 32 ? GLR_WIDE : GLR_PACKED;
     return glr_whole(a, elem, 4) ? GLR_NARROW : GLR_SINGLE;
 }
 
-void glr_cut(const Plan& p, int V, int ctas, void* scratch, GlrArgs* a)
+void glr_cut(const ScanPlan& p, int V, int ctas, void* scratch, GlrArgs* a)
 {
     // An uncut sequence takes T/64 iterations one after another; all of them, spread evenly over
     // the CTAs that the GPU holds, `share`.  Where the longest sequence would run far past that, it
     // is cut (every piece's gates are then read twice), into pieces short enough to spread well and
-    // long enough that starting them (about two iterations) does not show.
-    const int64_t blocks = ceil_div(a->H, 32 * V), slots = (int64_t)p.num_sms * ctas;
-    const int64_t steps = (int64_t)kScanChunk * a->groups, share = p.chunks / a->groups * blocks * a->ndir / slots;
-    const int64_t longest = (p.T + steps - 1) / steps;
-    int l = p.levels - 1;
+    // long enough that starting them (about two iterations) does not show.  One sequence of 65536
+    // frames of 1024 bf16 units, tied, forward: 132 us cut, 752 us uncut; two of 20 to 30 thousand frames
+    // of 512 fp32 units forward / backward 91 / 132 against 367 / 871 us; 32 of 200 to 2400 frames of 256
+    // bf16 units, just past the rule's edge, 31 / 44 against 33 / 58 us.
+    const int64_t blocks = ceil_div(a->H, 32 * V), slots = (int64_t)p.p.num_sms * ctas;
+    const int64_t steps = (int64_t)kScanChunk * a->groups, share = p.scan.chunks / a->groups * blocks * a->ndir / slots;
+    const int64_t longest = (p.p.T + steps - 1) / steps;
+    int l = p.scan.levels - 1;
     if (scratch && longest > share * 3 / 2 + 12)
-        for (l = 0; l < p.levels - 1 && ((int64_t)kScanPiece << l) < steps * share / 5; ++l) {}
-    a->pieces = p.d_pieces + p.level_first[l];
-    a->count = p.level_count[l];
-    a->cut = l < p.levels - 1;
+        for (l = 0; l < p.scan.levels - 1 && ((int64_t)kScanPiece << l) < steps * share / 5; ++l) {}
+    a->pieces = p.scan.d_pieces + p.scan.level_first[l];
+    a->count = p.scan.level_count[l];
+    a->cut = l < p.scan.levels - 1;
     a->piece = a->cut ? kScanPiece << l : INT32_MAX;
     a->maps = (float4*)scratch;
 }
 
-bool glr_short(const Plan& p, int V, int ctas, GlrArgs* a)
+bool glr_short(const ScanPlan& p, int V, int ctas, GlrArgs* a)
 {
     // A warp takes 8 steps at a time, all warps that the GPU holds at once: the longest sequence's
-    // tiles against an even share.  A CTA's 64 steps cost it as much for a sequence of 8.
-    const int64_t items = (int64_t)ceil_div(a->H, 32 * V) * a->ndir * p.B, warps = (int64_t)p.num_sms * ctas * kGlrWarps;
-    const int64_t longest = ceil_div(p.T, kGlrSteps), share = p.rows / kGlrSteps * (items / p.B) / warps;
+    // tiles against an even share.  A CTA's 64 steps cost it as much for a sequence of 8.  512
+    // directions of 70 frames of 1024 bf16 units forward / backward: 42 / 87 us, a CTA each 76 / 136 us.
+    const int64_t items = (int64_t)ceil_div(a->H, 32 * V) * a->ndir * p.p.B, warps = (int64_t)p.p.num_sms * ctas * kGlrWarps;
+    const int64_t longest = ceil_div(p.p.T, kGlrSteps), share = p.p.rows / kGlrSteps * (items / p.p.B) / warps;
     if (longest > 2 && (items * 2 < warps || longest > 2 * share + 8)) return false;
-    const int l = p.levels - 1;
-    a->pieces = p.d_pieces + p.level_first[l];
-    a->count = p.level_count[l];
+    const int l = p.scan.levels - 1;
+    a->pieces = p.scan.d_pieces + p.scan.level_first[l];
+    a->count = p.scan.level_count[l];
     a->cut = false;
     a->piece = INT32_MAX;
     return true;
 }
 
-size_t glr_scratch(const Plan& p, const lstm_glr_shape& s)
+size_t glr_scratch(const ScanPlan& p, const lstm_glr_shape& s)
 {
     // the finest level's maps, 8 bytes a unit, in blocks of at most 64 units
-    return p.levels < 2 ? 0 : (size_t)p.level_count[0] * s.num_directions * (size_t)ceil_div(s.hidden_size, 64) * 64 * 8;
+    return p.scan.levels < 2 ? 0 : (size_t)p.scan.level_count[0] * s.num_directions * (size_t)ceil_div(s.hidden_size, 64) * 64 * 8;
 }
 
 }  // namespace lstm
@@ -200,14 +212,14 @@ extern "C" {
 size_t lstm_glr_workspace_bytes(const lstm_plan* plan, const lstm_glr_shape* shape)
 {
     if (!plan || check_glr_shape(shape) != LSTM_OK) return 0;
-    const size_t n = (size_t)plan->p.chunks * shape->num_directions * shape->hidden_size * sizeof(float);
+    const size_t n = (size_t)static_cast<const ScanPlan*>(plan)->scan.chunks * shape->num_directions * shape->hidden_size * sizeof(float);
     return n > 16 ? n : 16;
 }
 
 size_t lstm_glr_scratch_bytes(const lstm_plan* plan, const lstm_glr_shape* shape)
 {
     if (!plan || check_glr_shape(shape) != LSTM_OK) return 0;
-    return glr_scratch(plan->p, *shape);
+    return glr_scratch(*static_cast<const ScanPlan*>(plan), *shape);
 }
 
 lstm_status lstm_glr_fwd(const lstm_plan* plan, const lstm_glr_shape* shape, const lstm_glr_gates* gates,
@@ -216,7 +228,8 @@ lstm_status lstm_glr_fwd(const lstm_plan* plan, const lstm_glr_shape* shape, con
     if (!plan || !gates) return LSTM_ERR_INVALID_ARG;
     lstm_status st = check_glr_shape(shape);
     if (st != LSTM_OK) return st;
-    const Plan& p = plan->p;
+    const ScanPlan& sp = *static_cast<const ScanPlan*>(plan);
+    const Plan& p = sp.p;
     const lstm_glr_shape& s = *shape;
     cudaStream_t cs = (cudaStream_t)stream;
     if (!aligned(h0, 4) || !aligned(h_n, 4) || !aligned(workspace, 16) || !aligned(scratch, 16) || !right_device(p)) return LSTM_ERR_INVALID_ARG;
@@ -225,9 +238,9 @@ lstm_status lstm_glr_fwd(const lstm_plan* plan, const lstm_glr_shape* shape, con
         !good_gates(s, gates->f, gates->z, gates->i, gates->row_stride, gates->dir_stride))
         return LSTM_ERR_INVALID_ARG;
     if (gates->row_stride > kGlrMaxStride) return LSTM_ERR_UNSUPPORTED;
-    GlrArgs a = plan_args(p, s, *gates);
+    GlrArgs a = plan_args(sp, s, *gates);
     a.h0 = h0; a.y = y; a.h_n = h_n; a.ws = (float*)workspace;
-    return launch_glr_fwd(p, s, a, scratch, cs);
+    return launch_glr_fwd(sp, s, a, scratch, cs);
 }
 
 lstm_status lstm_glr_bwd(const lstm_plan* plan, const lstm_glr_shape* shape, const lstm_glr_gates* gates,
@@ -237,7 +250,8 @@ lstm_status lstm_glr_bwd(const lstm_plan* plan, const lstm_glr_shape* shape, con
     if (!plan || !gates || !grads) return LSTM_ERR_INVALID_ARG;
     lstm_status st = check_glr_shape(shape);
     if (st != LSTM_OK) return st;
-    const Plan& p = plan->p;
+    const ScanPlan& sp = *static_cast<const ScanPlan*>(plan);
+    const Plan& p = sp.p;
     const lstm_glr_shape& s = *shape;
     cudaStream_t cs = (cudaStream_t)stream;
     if (!aligned(dh_n, 4) || !aligned(dh0, 4) || !aligned(workspace, 16) || !aligned(scratch, 16) || !right_device(p)) return LSTM_ERR_INVALID_ARG;
@@ -247,10 +261,10 @@ lstm_status lstm_glr_bwd(const lstm_plan* plan, const lstm_glr_shape* shape, con
         !good_gates(s, grads->f, grads->z, grads->i, grads->row_stride, grads->dir_stride))
         return LSTM_ERR_INVALID_ARG;
     if (gates->row_stride > kGlrMaxStride || grads->row_stride > kGlrMaxStride) return LSTM_ERR_UNSUPPORTED;
-    GlrArgs a = plan_args(p, s, *gates);
+    GlrArgs a = plan_args(sp, s, *gates);
     a.ws = (float*)const_cast<void*>(workspace); a.dy = dy; a.dh_n = dh_n; a.dh0 = dh0;
     a.df = grads->f; a.dz = grads->z; a.di = grads->i; a.gld = grads->row_stride; a.gdstride = grads->dir_stride;
-    return launch_glr_bwd(p, s, a, scratch, cs);
+    return launch_glr_bwd(sp, s, a, scratch, cs);
 }
 
 lstm_status lstm_glr_step(const lstm_glr_shape* shape, const lstm_glr_gates* gates, int32_t rows,

@@ -3,7 +3,7 @@
 
 #include <atomic>
 
-#include "common.cuh"
+#include "scan_plan.cuh"
 
 namespace lstm {
 
@@ -180,7 +180,7 @@ template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(flo
 
 // Largest row stride (elements): strides in bytes stay within 32 bits, their products with a row are 64 bits wide.
 constexpr int64_t kGlrMaxStride = 1 << 29;
-constexpr int kGlrWarps = 8;            // pieces of a CTA's 64 steps, one a warp
+constexpr int kGlrWarps = 8;            // parts of a CTA's 64 steps, one a warp
 constexpr int kGlrSteps = 8;            // consecutive steps of one thread
 static_assert(kGlrWarps * kGlrSteps == kScanChunk, "a CTA's iteration is one kept state");
 
@@ -394,13 +394,13 @@ GlrRows glr_rows(const GlrArgs& a, int elem);
 inline int glr_groups(int H) { return H > 16 ? 2 : 4; }
 // Whether to cut sequences into pieces that run side by side, and how long: fills the pieces' fields.
 // `ctas` is what an SM holds of the scan kernel, `scratch` the caller's (null: uncut).
-void glr_cut(const Plan& p, int V, int ctas, void* scratch, GlrArgs* a);      // (groups set)
-size_t glr_scratch(const Plan& p, const lstm_glr_shape& s);
+void glr_cut(const ScanPlan& p, int V, int ctas, void* scratch, GlrArgs* a);      // (groups set)
+size_t glr_scratch(const ScanPlan& p, const lstm_glr_shape& s);
 // Whether each warp takes a sequence of its own (uncut: fills the pieces' fields).
-bool glr_short(const Plan& p, int V, int ctas, GlrArgs* a);
+bool glr_short(const ScanPlan& p, int V, int ctas, GlrArgs* a);
 
-lstm_status launch_glr_fwd(const Plan& p, const lstm_glr_shape& s, GlrArgs a, void* scratch, cudaStream_t cs);
-lstm_status launch_glr_bwd(const Plan& p, const lstm_glr_shape& s, GlrArgs a, void* scratch, cudaStream_t cs);
+lstm_status launch_glr_fwd(const ScanPlan& p, const lstm_glr_shape& s, GlrArgs a, void* scratch, cudaStream_t cs);
+lstm_status launch_glr_bwd(const ScanPlan& p, const lstm_glr_shape& s, GlrArgs a, void* scratch, cudaStream_t cs);
 
 // One launch of `fn` over all pieces, directions and blocks of units: an item a CTA, or (WARPS, the
 // kernel then takes their number too) an item a warp.  `ready`: a bit for each device whose

@@ -7,6 +7,14 @@
 // before its next 8 steps is the one after its last 8, taken through the maps in between, so no
 // thread carries more than its own state and an iteration needs one barrier.  Every order is
 // fixed by the shape and the plan: the result does not depend on timing.
+//
+// Why so: about ten operations and two transcendentals a unit against 6 to 16 bytes, so memory is
+// the bound once T steps do not run one after another (a thread a unit did: 40555 frames of 2 x 512
+// bf16 units, three gates, 1084 us; here 66 us).  8 warps by 8 steps: 16 values of a thread fit the
+// registers with three CTAs an SM.  Measured, forward, cold L2: 70 k frames of 2 x 256 fp32 units, three
+// gates, 91 us, 6.3 TB/s (95 % of the copy rate); 40555 frames of 2 x 512 bf16 units three gates 66 us,
+// 5.5 TB/s, two gates 52 us, 5.3 TB/s.  fp32 is at the memory's rate; bf16 halves the bytes but not the
+// instructions, and the schedulers issue in 62 % of their cycles.
 #include "glr.cuh"
 
 namespace lstm {
@@ -234,6 +242,7 @@ __global__ void __launch_bounds__(32 * kGlrWarps, FwdTile<T, GATED, ROWS>::CTAS)
 
 // Many sequences, or very short ones: a warp walks a sequence 8 steps at a time by itself, running
 // the steps as they come.  No maps, no barriers, and no warp idles past a short sequence's end.
+// 512 directions of 70 frames of 1024 bf16 units: 42 us, 5.4 TB/s.
 template <typename T, bool GATED, int ROWS> struct ShortTile : RowTile<T, ROWS, GATED ? 3 : 2> {
     typedef RowTile<T, ROWS, GATED ? 3 : 2> R;
     static constexpr int W = kGlrWarps, CTAS = 3;
@@ -314,8 +323,11 @@ __global__ void __launch_bounds__(32 * kGlrWarps, 3) glr_fwd_short_kernel(const 
 // ---------------------------------------------------------------- a piece's map
 
 // Where sequences are cut, every piece but a sequence's last is first reduced to its map: warp w
-// composes its eighth of the piece in order, reading rows two loads ahead, with no barrier until
-// the warps' maps meet.
+// composes its eighth of the piece in order, its rows up to four loads ahead, with no barrier until
+// the warps' maps meet.  Gates are so read twice, partly out of L2, which the memory's rate bounds: a
+// 65536-frame sequence of 1024 bf16 units takes 55 us here (4.9 TB/s) of 132 us in all.  Passing the
+// state on between CTAs that hold a piece each would read them once, but waits: clusters in lockstep,
+// tried, lose 2 to 3 us every 64 steps a CTA and took 190 to 290 us.
 template <typename T, bool GATED, int ROWS>
 __global__ void __launch_bounds__(32 * kGlrWarps, 3) glr_fwd_map_kernel(const GlrArgs p)
 {
@@ -375,25 +387,25 @@ __global__ void __launch_bounds__(32 * kGlrWarps, 3) glr_fwd_map_kernel(const Gl
 }
 
 template <typename T, bool GATED, int ROWS>
-lstm_status go(const Plan& p, GlrArgs a, void* scratch, cudaStream_t cs)
+lstm_status go(const ScanPlan& p, GlrArgs a, void* scratch, cudaStream_t cs)
 {
     static std::atomic<uint64_t> ready{0}, ready_map{0}, ready_short{0};
     typedef FwdTile<T, GATED, ROWS> C;
     typedef MapTile<T, GATED, ROWS> M;
     constexpr int ALONE = ROWS == GLR_PACKED ? GLR_WIDE : ROWS;     // a warp a sequence: one group
     typedef ShortTile<T, GATED, ALONE> Q;
-    if (glr_short(p, C::V, Q::CTAS, &a)) return glr_launch<true>(p, glr_fwd_short_kernel<T, GATED, ALONE>, a, C::V, Q::SMEM, ready_short, cs);
+    if (glr_short(p, C::V, Q::CTAS, &a)) return glr_launch<true>(p.p, glr_fwd_short_kernel<T, GATED, ALONE>, a, C::V, Q::SMEM, ready_short, cs);
     if (C::PACKED) a.groups = glr_groups(a.H);
     glr_cut(p, C::V, C::CTAS, scratch, &a);
     if (a.cut) {
-        const lstm_status st = glr_launch(p, glr_fwd_map_kernel<T, GATED, ROWS>, a, C::V, M::SMEM, ready_map, cs);
+        const lstm_status st = glr_launch(p.p, glr_fwd_map_kernel<T, GATED, ROWS>, a, C::V, M::SMEM, ready_map, cs);
         if (st != LSTM_OK) return st;
     }
-    return glr_launch(p, glr_fwd_kernel<T, GATED, ROWS>, a, C::V, C::SMEM, ready, cs);
+    return glr_launch(p.p, glr_fwd_kernel<T, GATED, ROWS>, a, C::V, C::SMEM, ready, cs);
 }
 
 template <typename T, bool GATED>
-lstm_status go(const Plan& p, const GlrArgs& a, void* scratch, cudaStream_t cs)
+lstm_status go(const ScanPlan& p, const GlrArgs& a, void* scratch, cudaStream_t cs)
 {
     const GlrRows rows = glr_rows(a, (int)sizeof(T));
     if (rows == GLR_WIDE) return go<T, GATED, GLR_WIDE>(p, a, scratch, cs);
@@ -405,7 +417,7 @@ lstm_status go(const Plan& p, const GlrArgs& a, void* scratch, cudaStream_t cs)
 
 }  // namespace
 
-lstm_status launch_glr_fwd(const Plan& p, const lstm_glr_shape& s, GlrArgs a, void* scratch, cudaStream_t cs)
+lstm_status launch_glr_fwd(const ScanPlan& p, const lstm_glr_shape& s, GlrArgs a, void* scratch, cudaStream_t cs)
 {
     const bool gated = s.cell == LSTM_GLR_GATED;
     if (s.dtype == LSTM_BF16) return gated ? go<__nv_bfloat16, true>(p, a, scratch, cs) : go<__nv_bfloat16, false>(p, a, scratch, cs);

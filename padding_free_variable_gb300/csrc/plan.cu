@@ -13,7 +13,7 @@
 #include <numeric>
 #include <vector>
 
-#include "common.cuh"
+#include "scan_plan.cuh"
 
 namespace lstm {
 
@@ -118,7 +118,7 @@ static void free_plan(Plan& p)
     free(p.h_bs); free(p.h_off); free(p.h_perm); free(p.h_len); free(p.h_cstart);
     cudaFree(p.d_bs); cudaFree(p.d_off); cudaFree(p.d_perm); cudaFree(p.d_len);
     cudaFree(p.d_row_src); cudaFree(p.d_prev_fwd); cudaFree(p.d_prev_rev); cudaFree(p.d_row_slot);
-    cudaFree(p.d_row_dst); cudaFree(p.d_chunk); cudaFree(p.d_pieces);
+    cudaFree(p.d_row_dst);
     cudaFree(p.d_flags); cudaFree(p.d_status);
     p = Plan();
 }
@@ -196,6 +196,46 @@ struct FrameMap {
     int64_t frames = 0;
 };
 
+// The tables of the gated linear recurrence, in one upload.
+static cudaError_t upload_scan_tables(const Plan& p, ScanTables* t)
+{
+    std::vector<int4> pieces;       // of each level, the first pieces of all slots before their second ones
+    std::vector<int32_t> first(p.B);
+    for (int32_t l = 0; ; ++l) {
+        const int64_t len = (int64_t)kScanPiece << l;
+        int32_t most = 1, sum = 0;
+        for (int32_t j = 0; j < p.B; ++j) {
+            const int32_t n = std::max<int32_t>(1, (int32_t)((p.h_len[j] + len - 1) / len));
+            first[j] = sum;
+            sum += n;
+            most = std::max(most, n);
+        }
+        t->level_first[l] = (int32_t)pieces.size();
+        t->level_count[l] = sum;
+        for (int32_t k = 0; k < most; ++k)
+            for (int32_t j = 0; j < p.B; ++j) {
+                if (k > 0 && (int64_t)p.h_len[j] <= k * len) {
+                    if (!p.padded) break;       // sorted: no later slot is longer
+                    continue;
+                }
+                pieces.push_back(make_int4(j, k, p.h_len[j], first[j]));
+            }
+        t->levels = l + 1;
+        if (most == 1) break;
+    }
+    const size_t count = pieces.size();
+    pieces.resize(count + (p.B + 4) / 4);
+    int32_t* const chunk = (int32_t*)(pieces.data() + count);
+    for (int32_t j = 0; j < p.B; ++j) {
+        chunk[j] = (int32_t)t->chunks;
+        t->chunks += (p.h_len[j] + kScanChunk - 1) / kScanChunk;
+    }
+    chunk[p.B] = (int32_t)t->chunks;
+    const cudaError_t e = upload(&t->d_pieces, pieces.data(), pieces.size());
+    t->d_chunk = (int32_t*)(t->d_pieces + count);
+    return e;
+}
+
 static lstm_status create_plan(const int32_t* lengths, int32_t B, bool padded, lstm_plan** out,
                                const FrameMap* fm = nullptr)
 {
@@ -208,7 +248,7 @@ static lstm_status create_plan(const int32_t* lengths, int32_t B, bool padded, l
     if (st != LSTM_OK) return st;
     if (fm) frames = fm->frames;
 
-    lstm_plan* hp = new lstm_plan();
+    ScanPlan* hp = new ScanPlan();
     Plan& p = hp->p;
     p.B = B; p.T = T; p.rows = rows; p.frames = frames; p.padded = padded;
     p.tracer = new Tracer();
@@ -245,42 +285,7 @@ static lstm_status create_plan(const int32_t* lengths, int32_t B, bool padded, l
     if (e == cudaSuccess && fm) e = upload(&p.d_row_dst, row_dst.data(), (size_t)rows);
     if (e == cudaSuccess) e = upload(&p.d_prev_fwd, prev_fwd.data(), (size_t)rows);
     if (e == cudaSuccess) e = upload(&p.d_prev_rev, prev_rev.data(), (size_t)rows);
-    {   // first kScanChunk-step piece of each slot
-        std::vector<int32_t> chunk(B + 1);
-        for (int32_t j = 0; j < B; ++j) {
-            chunk[j] = (int32_t)p.chunks;
-            p.chunks += (p.h_len[j] + kScanChunk - 1) / kScanChunk;
-        }
-        chunk[B] = (int32_t)p.chunks;
-        if (e == cudaSuccess) e = upload(&p.d_chunk, chunk.data(), (size_t)B + 1);
-    }
-    {   // pieces of each level, the first pieces of all slots before their second ones
-        std::vector<int4> pieces;
-        std::vector<int32_t> first(B);
-        for (int32_t l = 0; ; ++l) {
-            const int64_t len = (int64_t)kScanPiece << l;
-            int32_t most = 1, sum = 0;
-            for (int32_t j = 0; j < B; ++j) {
-                const int32_t n = std::max<int32_t>(1, (int32_t)((p.h_len[j] + len - 1) / len));
-                first[j] = sum;
-                sum += n;
-                most = std::max(most, n);
-            }
-            p.level_first[l] = (int32_t)pieces.size();
-            p.level_count[l] = sum;
-            for (int32_t k = 0; k < most; ++k)
-                for (int32_t j = 0; j < B; ++j) {
-                    if (k > 0 && (int64_t)p.h_len[j] <= k * len) {
-                        if (!padded) break;         // sorted: no later slot is longer
-                        continue;
-                    }
-                    pieces.push_back(make_int4(j, k, p.h_len[j], first[j]));
-                }
-            p.levels = l + 1;
-            if (most == 1) break;
-        }
-        if (e == cudaSuccess) e = upload(&p.d_pieces, pieces.data(), pieces.size());
-    }
+    if (e == cudaSuccess) e = upload_scan_tables(p, &hp->scan);
     {   // sorted slot of each packed row (row off[t] + j holds slot j)
         std::vector<int32_t> row_slot(rows);
         for (int t = 0; t < T; ++t)
@@ -293,6 +298,7 @@ static lstm_status create_plan(const int32_t* lengths, int32_t B, bool padded, l
     if (e == cudaSuccess) e = cudaMemset(p.d_status, 0, sizeof(DeviceStatus));
     if (e != cudaSuccess) {
         free_plan(p);
+        cudaFree(hp->scan.d_pieces);
         delete hp;
         return LSTM_ERR_CUDA;
     }
@@ -438,8 +444,10 @@ lstm_status lstm_plan_compute_host(const int32_t* lengths_host, int32_t B, int32
 lstm_status lstm_plan_destroy(lstm_plan* plan)
 {
     if (!plan) return LSTM_OK;
-    lstm::free_plan(plan->p);
-    delete plan;
+    lstm::ScanPlan* full = static_cast<lstm::ScanPlan*>(plan);
+    lstm::free_plan(full->p);
+    cudaFree(full->scan.d_pieces);
+    delete full;
     return LSTM_OK;
 }
 
