@@ -41,7 +41,7 @@ inline BwdShape bwd_shape(int D)
     s.per = wide <= 4096 ? 1 : wide <= 8192 ? 2 : 4;
     s.tpr = row_threads(ceil_div(wide, 8 * s.per));
     s.threads = s.tpr <= 32 ? 128 : s.tpr;
-    s.ctas = s.threads <= 128 ? 8 : s.threads <= 256 ? 4 : 2;       // at most
+    s.ctas = s.threads <= 64 ? 16 : s.threads <= 128 ? 8 : s.threads <= 256 ? 4 : 2;       // at most
     return s;
 }
 
@@ -452,10 +452,13 @@ lstm_status run(NormArgs& a, const BwdShape& s, cudaStream_t cs)
 // A whole block of one kind and gate, by types: y's, x's (dn has y's).
 template <int KIND, int GATE, typename TB, typename TS> lstm_status run_block(NormArgs& a, const BwdShape& s, cudaStream_t cs)
 {
-    // rows of 2-byte values two at a time: fp32 rows twice over do not fit the registers
-    constexpr int R = sizeof(TB) + sizeof(TS) == 4 ? 2 : 1;
+    // rows with 2-byte values two at a time (40000 x 1024 bf16 beside an fp32 stream 156 us, 183 one at a
+    // time; centred 183 and 225 us); fp32 rows twice over do not fit the registers.  Four CTAs of 128 for
+    // two rows and for the centred fp32 block (80000 x 512: 266 us, six CTAs of 80 registers 345), six for
+    // the other (200000 x 320: 375 us, four 407).
+    constexpr int R = sizeof(TB) == 2 ? 2 : 1;
     if (norm_whole(a)) {
-        if (s.threads <= 128) return run<TB, TS, TB, 8, 1, R, 128, R == 2 ? 4 : 6, KIND, GATE>(a, s, cs);
+        if (s.threads <= 128) return run<TB, TS, TB, 8, 1, R, 128, R == 2 || KIND == LSTM_NORM_LAYER ? 4 : 6, KIND, GATE>(a, s, cs);
         if (s.threads <= 256) return run<TB, TS, TB, 8, 1, R, 256, R == 2 ? 2 : 3, KIND, GATE>(a, s, cs);
         if (s.per == 2) return run<TB, TS, TB, 8, 2, 1, 512, 1, KIND, GATE>(a, s, cs);
         if (s.threads <= 384) return run<TB, TS, TB, 8, 1, 1, 384, 2, KIND, GATE>(a, s, cs);

@@ -153,9 +153,9 @@ GlrRows glr_rows(const GlrArgs& a, int elem)
 {
     // 40555 frames of 2 x 512 bf16 units forward / backward: wide 52 / 89 us, narrow (rows 4 bytes
     // off) 64 / 105 us, single (2 bytes off) 85 / 154 us; 70 k frames of 2 x 256 fp32, three gates: wide
-    // 91 / 158 us, narrow 107 / 206 us.  Packed against wide: 74 sequences of 21099 frames of 8 bf16
+    // 91 / 158 us, narrow 107 / 206 us.  Grouped against wide: 74 sequences of 21099 frames of 8 bf16
     // units 113 / 168 against 326 / 480 us, 60 of 19 to 211 frames of 2 x 16 units 9 / 11 against 13 / 15.
-    if (glr_whole(a, elem, 16)) return a.H > 32 ? GLR_WIDE : GLR_PACKED;
+    if (glr_whole(a, elem, 16)) return a.H > 32 ? GLR_WIDE : GLR_GROUPED;
     return glr_whole(a, elem, 4) ? GLR_NARROW : GLR_SINGLE;
 }
 

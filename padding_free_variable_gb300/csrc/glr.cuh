@@ -11,7 +11,7 @@ namespace lstm {
 struct GlrArgs {
     int T = 0, B = 0, H = 0, ndir = 1;
     int padded = 0;
-    int groups = 1;                     // GLR_PACKED: groups of lanes, each with steps of its own
+    int groups = 1;                     // GLR_GROUPED: groups of lanes, each with steps of its own
     const int4* pieces = nullptr;       // this level's
     int piece = 0;                      // its pieces' steps
     int count = 0;                      // and their number
@@ -287,7 +287,7 @@ enum GlrRows {
     GLR_WIDE = 0,       // 2 units a lane; rows through shared memory in 16-byte pieces
     GLR_NARROW = 1,     // 4 bytes a lane (2 bf16 units or 1 fp32 unit), each lane its own
     GLR_SINGLE = 2,     // bf16 rows that are not aligned to 4 bytes: 1 unit a lane
-    GLR_PACKED = 3      // as wide rows, of at most 32 units: groups of 16 or 8 lanes take 8 steps each
+    GLR_GROUPED = 3      // as wide rows, of at most 32 units: groups of 16 or 8 lanes take 8 steps each
 };
 
 // A warp's rows: 32 V units of each.  Wide rows reach the warp's own part of shared memory by
@@ -295,15 +295,15 @@ enum GlrRows {
 // rows and not by each lane of each row; the others are loaded by each lane into registers.
 template <typename T, int ROWS, int G> struct RowTile {
     static constexpr int S = kGlrSteps;
-    static constexpr bool PACKED = ROWS == GLR_PACKED;
-    static constexpr int V = ROWS == GLR_WIDE || PACKED ? 2 : ROWS == GLR_NARROW ? 4 / (int)sizeof(T) : 1;
+    static constexpr bool GROUPED = ROWS == GLR_GROUPED;
+    static constexpr int V = ROWS == GLR_WIDE || GROUPED ? 2 : ROWS == GLR_NARROW ? 4 / (int)sizeof(T) : 1;
     static constexpr int OWN = V * (int)sizeof(T);              // bytes of a lane's units
     static constexpr int RB = 32 * OWN;                         // bytes of a row
-    static constexpr bool STAGED = ROWS == GLR_WIDE || PACKED;
+    static constexpr bool STAGED = ROWS == GLR_WIDE || GROUPED;
     // Loads past a piece's end are left out where that gains: they are wasted reads (two sequences of 20 to
     // 30 thousand frames x 512 fp32 backward 137 us with them, 132 us without), but the branch costs the
     // bf16 kernels their schedule (40555 frames x 2 x 512 backward 89 us with them, 101 us without).
-    static constexpr bool BOUNDED = PACKED || sizeof(T) == 4;
+    static constexpr bool BOUNDED = GROUPED || sizeof(T) == 4;
     static constexpr int WIDTH = STAGED ? 16 : OWN;             // bytes a lane moves at a time
     static constexpr int LR = RB / WIDTH, RI = 32 / LR;         // lanes of a row, rows of one instruction
     static constexpr int BYTES = G * S * RB;                    // a warp's rows of one stage: [operand][step][RB]
@@ -320,18 +320,18 @@ template <typename T, int ROWS, int G> struct RowTile {
     __device__ __forceinline__ void place(int lane, int end, int groups)
     {
         at = lane % LR * WIDTH;
-        if (PACKED) lanes = 32 / groups;
+        if (GROUPED) lanes = 32 / groups;
         writes = col() < end;
         const int from = min(col(), end - WIDTH);
 #pragma unroll
         for (int x = 0; x < G; ++x) src[x] += from;
     }
-    __device__ __forceinline__ int unit_lane(int lane) const { return PACKED ? lane & (lanes - 1) : lane; }
-    __device__ __forceinline__ int group(int lane) const { return PACKED ? lane / lanes : 0; }
-    // the piece's byte in the row in memory (packed: the groups' rows are staged next to each other)
-    __device__ __forceinline__ int col() const { return PACKED ? at & (lanes * OWN - 1) : at; }
+    __device__ __forceinline__ int unit_lane(int lane) const { return GROUPED ? lane & (lanes - 1) : lane; }
+    __device__ __forceinline__ int group(int lane) const { return GROUPED ? lane / lanes : 0; }
+    // the piece's byte in the row in memory (grouped: the groups' rows are staged next to each other)
+    __device__ __forceinline__ int col() const { return GROUPED ? at & (lanes * OWN - 1) : at; }
     // the warp's step whose row the piece of staged row k + lane / LR is of
-    __device__ __forceinline__ int step(int lane, int k) const { return (PACKED ? at / (lanes * OWN) * S : 0) + k + lane / LR; }
+    __device__ __forceinline__ int step(int lane, int k) const { return (GROUPED ? at / (lanes * OWN) * S : 0) + k + lane / LR; }
     // `rows`: lane k holds the packed row of the warp's step k; `any`: is there one to load?
     __device__ __forceinline__ void load(int lane, unsigned rows, int stage, bool any = true)
     {
@@ -390,7 +390,7 @@ template <typename T, int ROWS, int G> struct RowTile {
 };
 
 GlrRows glr_rows(const GlrArgs& a, int elem);
-// Packed rows' groups of a warp: 64 places by 16 or 32 units.
+// Groups of a warp of grouped rows: 64 places by 16 or 32 units.
 inline int glr_groups(int H) { return H > 16 ? 2 : 4; }
 // Whether to cut sequences into pieces that run side by side, and how long: fills the pieces' fields.
 // `ctas` is what an SM holds of the scan kernel, `scratch` the caller's (null: uncut).

@@ -113,9 +113,9 @@ __global__ void __launch_bounds__(32 * kGlrWarps, BwdTile<T, GATED, ROWS>::CTAS)
     // cut sequences: the pieces whose maps were formed last are the ones still in L2
     const Place c(p, p.cut ? gridDim.x - 1 - blockIdx.x : blockIdx.x, 32 * V);
     auto tile = error_rows<T, ROWS, G>(p, c, lane);
-    // (packed: groups of lanes hold the same units, a group's 8 steps after the other's)
-    constexpr int GAP = C::PACKED ? S : 0;
-    const int groups = C::PACKED ? p.groups : 1, g = tile.group(lane), ul = tile.unit_lane(lane), chunk = groups * kScanChunk;
+    // (grouped: groups of lanes hold the same units, a group's 8 steps after the other's)
+    constexpr int GAP = C::GROUPED ? S : 0;
+    const int groups = C::GROUPED ? p.groups : 1, g = tile.group(lane), ul = tile.unit_lane(lane), chunk = groups * kScanChunk;
     const int u = c.u0 + ul * V, len = c.len;
     const bool live = u < p.H;
     const int64_t state = ((int64_t)c.d * p.B + p.perm[c.j]) * p.H + u;
@@ -186,8 +186,8 @@ __global__ void __launch_bounds__(32 * kGlrWarps, BwdTile<T, GATED, ROWS>::CTAS)
                 U.mad(a[k], b[k]);
                 A.mul(a[k]);
             }
-            Vals<V> AH, UH, AE;     // packed: of the steps before and after this group's
-            if constexpr (C::PACKED) {
+            Vals<V> AH, UH, AE;     // grouped: of the steps before and after this group's
+            if constexpr (C::GROUPED) {
                 AH = AE = A;
                 UH = U;
                 compose_groups<true>(lane, tile.lanes, AH, UH);
@@ -205,7 +205,7 @@ __global__ void __launch_bounds__(32 * kGlrWarps, BwdTile<T, GATED, ROWS>::CTAS)
                 U.add(tile.held(lane, DY, k, stage));
                 U.mul(a[k]);
             }
-            if constexpr (C::PACKED) {
+            if constexpr (C::GROUPED) {
                 compose_groups<false>(lane, tile.lanes, AE, U);
                 if (g == 0) now[w].put(ul, AE, U);
                 AE = AE.from(lane + tile.lanes);
@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(32 * kGlrWarps, BwdTile<T, GATED, ROWS>::CTAS)
 #pragma unroll
             for (int x = 0; x < W - 1; ++x)
                 if (x < w) now[3 * W + x].apply(ul, h);
-            if constexpr (C::PACKED) {
+            if constexpr (C::GROUPED) {
                 h.mad(AH, UH);
                 e.mad(AE, U);
             }
@@ -256,7 +256,7 @@ __global__ void __launch_bounds__(32 * kGlrWarps, BwdTile<T, GATED, ROWS>::CTAS)
                     }
                 }
             }
-            if constexpr (C::PACKED) e = e.from(ul);
+            if constexpr (C::GROUPED) e = e.from(ul);
             if constexpr (C::STAGED) {
                 __syncwarp();
 #pragma unroll
@@ -453,8 +453,8 @@ __global__ void __launch_bounds__(32 * kGlrWarps, 3) glr_bwd_map_kernel(const Gl
     tile.ld[1] = (unsigned)(p.ndir * p.H) * (unsigned)el;
     tile.place(lane, (p.H - c.u0) * (int)el, p.groups);
     tile.in = smem + w * C::BYTES;
-    // (packed: each group of lanes its own part of the warp's)
-    const int groups = C::PACKED ? p.groups : 1, part = p.piece / (W * groups), gap = C::PACKED ? part : 0;
+    // (grouped: each group of lanes its own part of the warp's)
+    const int groups = C::GROUPED ? p.groups : 1, part = p.piece / (W * groups), gap = C::GROUPED ? part : 0;
     const int g = tile.group(lane), ul = tile.unit_lane(lane), first = c.piece * p.piece + w * groups * part;
     int s0 = first + part - S;
     unsigned rows[NS + 2];
@@ -493,7 +493,7 @@ __global__ void __launch_bounds__(32 * kGlrWarps, 3) glr_bwd_map_kernel(const Gl
         }
     }
     if (C::STAGED) cp_async_wait<0>();
-    if constexpr (C::PACKED) compose_groups<false>(lane, tile.lanes, A, U);
+    if constexpr (C::GROUPED) compose_groups<false>(lane, tile.lanes, A, U);
     if (g == 0) s_map[w].put(ul, A, U);
     __syncthreads();
     if (w < W - 1) return;
@@ -512,10 +512,10 @@ lstm_status go(const ScanPlan& p, GlrArgs a, void* scratch, cudaStream_t cs)
 {
     static std::atomic<uint64_t> ready{0}, ready_map{0}, ready_short{0};
     typedef BwdTile<T, GATED, ROWS> C;
-    constexpr int ALONE = ROWS == GLR_PACKED ? GLR_WIDE : ROWS;     // a warp a sequence: one group
+    constexpr int ALONE = ROWS == GLR_GROUPED ? GLR_WIDE : ROWS;     // a warp a sequence: one group
     typedef BwdShortTile<T, GATED, ALONE> Q;
     if (glr_short(p, C::V, Q::CTAS, &a)) return glr_launch<true>(p.p, glr_bwd_short_kernel<T, GATED, ALONE>, a, C::V, Q::SMEM, ready_short, cs);
-    if (C::PACKED) a.groups = glr_groups(a.H);
+    if (C::GROUPED) a.groups = glr_groups(a.H);
     glr_cut(p, C::V, C::CTAS, scratch, &a);
     if (a.cut) {
         const lstm_status st = glr_launch(p.p, glr_bwd_map_kernel<T, ROWS>, a, C::V, BwdMapTile<T, ROWS>::SMEM, ready_map, cs);
@@ -529,7 +529,7 @@ lstm_status go(const ScanPlan& p, const GlrArgs& a, void* scratch, cudaStream_t 
 {
     const GlrRows rows = glr_rows(a, (int)sizeof(T));
     if (rows == GLR_WIDE) return go<T, GATED, GLR_WIDE>(p, a, scratch, cs);
-    if (rows == GLR_PACKED) return go<T, GATED, GLR_PACKED>(p, a, scratch, cs);
+    if (rows == GLR_GROUPED) return go<T, GATED, GLR_GROUPED>(p, a, scratch, cs);
     if constexpr (sizeof(T) == 2)
         if (rows == GLR_SINGLE) return go<T, GATED, GLR_SINGLE>(p, a, scratch, cs);
     return go<T, GATED, GLR_NARROW>(p, a, scratch, cs);

@@ -135,9 +135,9 @@ __global__ void __launch_bounds__(32 * kGlrWarps, FwdTile<T, GATED, ROWS>::CTAS)
     // cut sequences: the pieces whose maps were formed last are the ones still in L2
     const Place c(p, p.cut ? gridDim.x - 1 - blockIdx.x : blockIdx.x, 32 * V);
     auto tile = gate_rows<T, ROWS, GATED ? 3 : 2>(p, c, lane);
-    // (packed: groups of lanes hold the same units, a group's 8 steps after the other's)
-    constexpr int GAP = C::PACKED ? S : 0;
-    const int groups = C::PACKED ? p.groups : 1, g = tile.group(lane), ul = tile.unit_lane(lane), chunk = groups * kScanChunk;
+    // (grouped: groups of lanes hold the same units, a group's 8 steps after the other's)
+    constexpr int GAP = C::GROUPED ? S : 0;
+    const int groups = C::GROUPED ? p.groups : 1, g = tile.group(lane), ul = tile.unit_lane(lane), chunk = groups * kScanChunk;
     const int u = c.u0 + ul * V, len = c.len;
     const bool live = u < p.H;
     const int64_t state = ((int64_t)c.d * p.B + p.perm[c.j]) * p.H + u;
@@ -196,7 +196,7 @@ __global__ void __launch_bounds__(32 * kGlrWarps, FwdTile<T, GATED, ROWS>::CTAS)
             for (int q = 0; q < NS + 1; ++q) rows[q] = rows[q + 1];
             rows[NS + 1] = c.row_of(p, s0 + (NS + 2) * chunk, lane, GAP);
             compose<V>(a, b, A, U);
-            if constexpr (C::PACKED) {
+            if constexpr (C::GROUPED) {
                 compose_groups<true>(lane, tile.lanes, A, U);
                 if (g == groups - 1) now[w].put(ul, A, U);
                 A = A.from(lane - tile.lanes);      // of the groups before this one
@@ -208,10 +208,10 @@ __global__ void __launch_bounds__(32 * kGlrWarps, FwdTile<T, GATED, ROWS>::CTAS)
             __syncthreads();
 #pragma unroll
             for (int x = 1; x < W; ++x) (w + x < W ? before + w + x : now + w + x - W)->apply(ul, h);
-            if constexpr (C::PACKED) h.mad(A, U);
+            if constexpr (C::GROUPED) h.mad(A, U);
             before = now;
             now = now == s_map + 2 * W ? s_map : now + W;
-            if ((C::PACKED ? mine % kScanChunk == 0 && mine < len : w == 0) && p.ws && live) {
+            if ((C::GROUPED ? mine % kScanChunk == 0 && mine < len : w == 0) && p.ws && live) {
                 float* ws = p.ws + ((int64_t)(p.chunk[c.j] + mine / kScanChunk) * p.ndir + c.d) * p.H + u;
 #pragma unroll
                 for (int v = 0; v < V; ++v) ws[v] = h.get(v);
@@ -227,7 +227,7 @@ __global__ void __launch_bounds__(32 * kGlrWarps, FwdTile<T, GATED, ROWS>::CTAS)
                     if (k < n) store_values<T, V>(y + (uint64_t)row * yld, h);
                 }
             }
-            if constexpr (C::PACKED) h = h.from((groups - 1) * tile.lanes + ul);
+            if constexpr (C::GROUPED) h = h.from((groups - 1) * tile.lanes + ul);
             if constexpr (C::STAGED) flush_rows(tile, out, lane, y, yld, rows_now, n);
         }
         if (C::STAGED) cp_async_wait<0>();
@@ -340,8 +340,8 @@ __global__ void __launch_bounds__(32 * kGlrWarps, 3) glr_fwd_map_kernel(const Gl
     if ((int64_t)(c.piece + 1) * p.piece >= c.len) return;
     auto tile = gate_rows<T, ROWS, GATED ? 3 : 2>(p, c, lane);
     tile.in = smem + w * C::BYTES;
-    // (packed: each group of lanes its own part of the warp's)
-    const int groups = C::PACKED ? p.groups : 1, part = p.piece / (W * groups), gap = C::PACKED ? part : 0, ul = tile.unit_lane(lane);
+    // (grouped: each group of lanes its own part of the warp's)
+    const int groups = C::GROUPED ? p.groups : 1, part = p.piece / (W * groups), gap = C::GROUPED ? part : 0, ul = tile.unit_lane(lane);
     int s0 = c.piece * p.piece + w * groups * part;
     const int end = s0 + part;
     unsigned rows[NS + 2];
@@ -372,7 +372,7 @@ __global__ void __launch_bounds__(32 * kGlrWarps, 3) glr_fwd_map_kernel(const Gl
         }
     }
     if (C::STAGED) cp_async_wait<0>();
-    if constexpr (C::PACKED) compose_groups<true>(lane, tile.lanes, A, U);
+    if constexpr (C::GROUPED) compose_groups<true>(lane, tile.lanes, A, U);
     if (tile.group(lane) == groups - 1) s_map[w].put(ul, A, U);
     __syncthreads();
     if (w > 0) return;
@@ -392,10 +392,10 @@ lstm_status go(const ScanPlan& p, GlrArgs a, void* scratch, cudaStream_t cs)
     static std::atomic<uint64_t> ready{0}, ready_map{0}, ready_short{0};
     typedef FwdTile<T, GATED, ROWS> C;
     typedef MapTile<T, GATED, ROWS> M;
-    constexpr int ALONE = ROWS == GLR_PACKED ? GLR_WIDE : ROWS;     // a warp a sequence: one group
+    constexpr int ALONE = ROWS == GLR_GROUPED ? GLR_WIDE : ROWS;     // a warp a sequence: one group
     typedef ShortTile<T, GATED, ALONE> Q;
     if (glr_short(p, C::V, Q::CTAS, &a)) return glr_launch<true>(p.p, glr_fwd_short_kernel<T, GATED, ALONE>, a, C::V, Q::SMEM, ready_short, cs);
-    if (C::PACKED) a.groups = glr_groups(a.H);
+    if (C::GROUPED) a.groups = glr_groups(a.H);
     glr_cut(p, C::V, C::CTAS, scratch, &a);
     if (a.cut) {
         const lstm_status st = glr_launch(p.p, glr_fwd_map_kernel<T, GATED, ROWS>, a, C::V, M::SMEM, ready_map, cs);
@@ -409,7 +409,7 @@ lstm_status go(const ScanPlan& p, const GlrArgs& a, void* scratch, cudaStream_t 
 {
     const GlrRows rows = glr_rows(a, (int)sizeof(T));
     if (rows == GLR_WIDE) return go<T, GATED, GLR_WIDE>(p, a, scratch, cs);
-    if (rows == GLR_PACKED) return go<T, GATED, GLR_PACKED>(p, a, scratch, cs);
+    if (rows == GLR_GROUPED) return go<T, GATED, GLR_GROUPED>(p, a, scratch, cs);
     if constexpr (sizeof(T) == 2)
         if (rows == GLR_SINGLE) return go<T, GATED, GLR_SINGLE>(p, a, scratch, cs);
     return go<T, GATED, GLR_NARROW>(p, a, scratch, cs);
