@@ -17,7 +17,7 @@
 // schedulers busy in 54 % of their cycles and 128 registers leave 16 warps an SM to hide the rest;
 // 200000 x 128 fp32 137 us, 6.0 TB/s; 5000 x 8192 bf16 196 us (344 us with everything looked up at run
 // time); odd, 9564 x 517 fp32 centred, 77 us, 2.1 TB/s, value by value 83 us; 30000 x 1001 bf16 beside
-// an fp32 stream 220 us, value by value 320 us.
+// an fp32 stream 191 us, 3.5 TB/s.
 #pragma once
 
 #include <algorithm>
@@ -41,7 +41,7 @@ inline BwdShape bwd_shape(int D)
     s.per = wide <= 4096 ? 1 : wide <= 8192 ? 2 : 4;
     s.tpr = row_threads(ceil_div(wide, 8 * s.per));
     s.threads = s.tpr <= 32 ? 128 : s.tpr;
-    s.ctas = s.threads <= 64 ? 16 : s.threads <= 128 ? 8 : s.threads <= 256 ? 4 : 2;       // at most
+    s.ctas = s.threads <= 64 ? 16 : s.threads <= 96 ? 10 : s.threads <= 128 ? 8 : s.threads <= 256 ? 4 : 2;       // at most
     return s;
 }
 
@@ -465,10 +465,13 @@ template <int KIND, int GATE, typename TB, typename TS> lstm_status run_block(No
         return run<TB, TS, TB, 8, 1, R, 512, 1, KIND, GATE>(a, s, cs);
     }
     if (norm_shifted(a) && a.D + 7 <= 4096) {
-        if (s.threads <= 128) return run<TB, TS, TB, 8, 1, 1, 128, 5, KIND, GATE, true>(a, s, cs);
+        // more warps gain more than more registers until these run out: seven CTAs of 128 threads an SM, five
+        // for centred rows (60000 x 511 bf16: 244 us, five 308; centred, beside an fp32 stream, 355 us, seven
+        // 402).  Rows of a CTA of 512, which leaves no second one, two at a time (9000 x 3501 bf16 269 and 308 us).
+        if (s.threads <= 128) return run<TB, TS, TB, 8, 1, 1, 128, KIND == LSTM_NORM_RMS ? 7 : 5, KIND, GATE, true>(a, s, cs);
         if (s.threads <= 256) return run<TB, TS, TB, 8, 1, 1, 256, 3, KIND, GATE, true>(a, s, cs);
         if (s.threads <= 384) return run<TB, TS, TB, 8, 1, 1, 384, 2, KIND, GATE, true>(a, s, cs);
-        return run<TB, TS, TB, 8, 1, 1, 512, 1, KIND, GATE, true>(a, s, cs);
+        return run<TB, TS, TB, 8, 1, R, 512, 1, KIND, GATE, true>(a, s, cs);
     }
     if (s.threads <= 128) return run<TB, TS, TB, 1, 8, 1, 128, 6, KIND, GATE>(a, s, cs);
     if (s.threads <= 256) return run<TB, TS, TB, 1, 8, 1, 256, 3, KIND, GATE>(a, s, cs);
