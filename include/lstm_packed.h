@@ -764,8 +764,8 @@ size_t lstm_glr_scratch_bytes(const lstm_plan* plan, const lstm_glr_shape* shape
  *              (h0 for a sequence of length 0); NULL to skip
  *   workspace  lstm_glr_workspace_bytes, kept for lstm_glr_bwd; NULL when no
  *              backward pass follows
- *   scratch    lstm_glr_scratch_bytes; NULL: no sequence is cut (slower for
- *              few long ones)
+ *   scratch    lstm_glr_scratch_bytes, one for each call that may run at the
+ *              same time; NULL: no sequence is cut (slower for few long ones)
  * The plan's device must be the current one (else LSTM_ERR_INVALID_ARG).
  */
 lstm_status lstm_glr_fwd(const lstm_plan* plan, const lstm_glr_shape* shape, const lstm_glr_gates* gates,

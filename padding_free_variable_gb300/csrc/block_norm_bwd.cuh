@@ -26,14 +26,14 @@
 
 namespace lstm {
 
+constexpr int kSMs = 152;
+
 struct BwdShape {
     int per, tpr, threads, ctas;        // values of a thread / 8, threads of a row and of a CTA, CTAs an SM
 };
 
 // Eight values a thread while a row then fits a CTA of 512.  (7 columns more than a row has: shifted
 // rows may need a group more.)
-constexpr int kSMs = 152;
-
 inline BwdShape bwd_shape(int D)
 {
     BwdShape s;
