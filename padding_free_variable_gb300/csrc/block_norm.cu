@@ -82,8 +82,9 @@ bool norm_whole(const NormArgs& a)
 
 bool norm_shifted(const NormArgs& a)
 {
+    // (a row but the last reads up to 7 values past its end, which the next row must have)
     const int64_t D = a.D;
-    return norm_full(a) && a.D % 8 != 0 && (a.ldy - D) % 8 == 0 && (!a.g || (a.ldg - D) % 8 == 0) && (!a.dy || (a.lddy - D) % 8 == 0) &&
+    return norm_full(a) && D >= 7 && D % 8 != 0 && (a.ldy - D) % 8 == 0 && (!a.g || (a.ldg - D) % 8 == 0) && (!a.dy || (a.lddy - D) % 8 == 0) &&
            (!a.dg || (a.lddg - D) % 8 == 0) && norm_aligned(a);
 }
 
