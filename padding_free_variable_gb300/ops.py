@@ -23,10 +23,22 @@ def _stream(stream=None) -> ctypes.c_void_p:
     return ctypes.c_void_p(s.cuda_stream)
 
 
-def _stream_of(stream, t) -> int:
-    """The stream's handle, by default the current one of t's device.  (torch.cuda.current_stream builds an object of
+def _device_of(t, name) -> int:
+    """The device that a call runs on: its first tensor's, which has to be the current one (launches go there)."""
+    dev = t.get_device()
+    if dev < 0 or dev != torch._C._cuda_getDevice():
+        raise ValueError(f"{name}: expected a tensor on the current CUDA device, got one on {t.device}")
+    return dev
+
+
+def _stream_of(stream, dev: int) -> int:
+    """The stream's handle, by default the device's current one.  (torch.cuda.current_stream builds an object of
     several microseconds, more than a small launch takes; torch's own compiled code asks for the bare handle.)"""
-    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(t.device.index)
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    if stream.device_index != dev:
+        raise ValueError(f"stream: expected one of cuda:{dev}, got one of cuda:{stream.device_index}")
+    return stream.cuda_stream
 
 
 class Plan:
@@ -605,20 +617,21 @@ def _need(ok, what):
         raise ValueError(what)
 
 
-def _dense(t, dtype, shape, name):
-    """Address of a contiguous tensor of this type and shape (None: none)."""
+def _dense(t, dtype, shape, name, dev):
+    """Address of a contiguous tensor of this type and shape on the call's device (None: none)."""
     if t is None:
         return None
-    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)} on cuda:{dev}, "
+                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
     return t.data_ptr()
 
 
-def _bytes(t, need, name):
+def _bytes(t, need, name, dev):
     if t is None:
         return None
-    if not t.is_contiguous() or t.numel() * t.element_size() < need:
-        raise ValueError(f"{name}: {need} contiguous bytes are needed")
+    if t.get_device() != dev or not t.is_contiguous() or t.numel() * t.element_size() < need:
+        raise ValueError(f"{name}: {need} contiguous bytes on cuda:{dev} are needed")
     return t.data_ptr()
 
 
@@ -632,7 +645,7 @@ def glr_shape(hidden_size, num_directions, bf16: bool, cell: str = "tied") -> _l
     return s
 
 
-def _glr_gates(key, f, z, i, rows, name):
+def _glr_gates(key, f, z, i, rows, name, dev):
     """lstm_glr_gates of [rows, ndir, H] tensors that share their row and direction strides."""
     nd, H, dt, gated = key
     want = (rows, nd, H)
@@ -647,6 +660,8 @@ def _glr_gates(key, f, z, i, rows, name):
     # the stride of a single row, direction or unit is never stepped over
     ld, ds = ld if rows > 1 else H, ds if nd > 1 else H
     for t in (f, z, i) if gated else (f, z):
+        if t.get_device() != dev:
+            raise ValueError(f"{name}: expected tensors on cuda:{dev}, got one on {t.device}")
         a, b, c = t.stride()
         if (a != ld and rows > 1) or (b != ds and nd > 1) or (c != 1 and H > 1):
             raise ValueError(f"{name}: units have to lie next to each other, and all gates to have the same strides")
@@ -687,13 +702,14 @@ def glr_forward(plan: Plan, shape, f, z, i, h0, y, h_n, workspace, stream=None):
     y [rows, ndir, H]; workspace: a buffer of glr_workspace_bytes that glr_backward reads, or None."""
     key, rows = shape.key, plan.rows
     nd, H, dt, _ = key
-    g = _glr_gates(key, f, z, i, rows, "gates")
+    dev = _device_of(f, "gates")
+    g = _glr_gates(key, f, z, i, rows, "gates", dev)
     st = (nd, plan.batch, H)
     need, most = _glr_sizes(plan, shape)
-    stream = _stream_of(stream, f)
+    stream = _stream_of(stream, dev)
     check(_lib.load().lstm_glr_fwd(
-        plan.handle, shape.ref, ctypes.byref(g), _dense(h0, torch.float32, st, "h0"), _dense(y, dt, (rows, nd, H), "y"),
-        _dense(h_n, torch.float32, st, "h_n"), _bytes(workspace, need, "workspace"),
+        plan.handle, shape.ref, ctypes.byref(g), _dense(h0, torch.float32, st, "h0", dev), _dense(y, dt, (rows, nd, H), "y", dev),
+        _dense(h_n, torch.float32, st, "h_n", dev), _bytes(workspace, need, "workspace", dev),
         _glr_scratch(plan, key, most, stream, f.device), stream), "lstm_glr_fwd")
 
 
@@ -701,14 +717,15 @@ def glr_backward(plan: Plan, shape, f, z, i, workspace, dy, dh_n, df, dz, di, dh
     """lstm_glr_bwd: dy [rows, ndir, H], dh_n / dh0 [ndir, B, H] fp32 or None, df, dz, di [rows, ndir, H] views."""
     key, rows = shape.key, plan.rows
     nd, H, dt, _ = key
-    g = _glr_gates(key, f, z, i, rows, "gates")
-    dg = _glr_gates(key, df, dz, di, rows, "gate gradients")
+    dev = _device_of(f, "gates")
+    g = _glr_gates(key, f, z, i, rows, "gates", dev)
+    dg = _glr_gates(key, df, dz, di, rows, "gate gradients", dev)
     st = (nd, plan.batch, H)
     need, most = _glr_sizes(plan, shape)
-    stream = _stream_of(stream, f)
+    stream = _stream_of(stream, dev)
     check(_lib.load().lstm_glr_bwd(
-        plan.handle, shape.ref, ctypes.byref(g), _bytes(workspace, need, "workspace"), _dense(dy, dt, (rows, nd, H), "dy"),
-        _dense(dh_n, torch.float32, st, "dh_n"), ctypes.byref(dg), _dense(dh0, torch.float32, st, "dh0"),
+        plan.handle, shape.ref, ctypes.byref(g), _bytes(workspace, need, "workspace", dev), _dense(dy, dt, (rows, nd, H), "dy", dev),
+        _dense(dh_n, torch.float32, st, "dh_n", dev), ctypes.byref(dg), _dense(dh0, torch.float32, st, "dh0", dev),
         _glr_scratch(plan, key, most, stream, f.device), stream), "lstm_glr_bwd")
 
 
@@ -716,12 +733,12 @@ def glr_step(shape, f, z, i, state_in, state_out, y, slots=None, stream=None):
     """lstm_glr_step: one frame of each of f.shape[0] streams; state_in / state_out [slots, H] fp32 (may be the same),
     y [rows, 1, H]; slots: int32 [rows] state row of each stream (outside the cache: idle), None for stream r in row r."""
     key, rows, n = shape.key, f.shape[0], state_in.shape[0]
-    H = key[1]
-    g = _glr_gates(key, f, z, i, rows, "gates")
+    H, dev = key[1], _device_of(f, "gates")
+    g = _glr_gates(key, f, z, i, rows, "gates", dev)
     check(_lib.load().lstm_glr_step(
-        shape.ref, ctypes.byref(g), rows, _dense(slots, torch.int32, (rows,), "slots"), n,
-        _dense(state_in, torch.float32, (n, H), "state_in"), _dense(state_out, torch.float32, (n, H), "state_out"),
-        _dense(y, key[2], (rows, 1, H), "y"), _stream_of(stream, f)), "lstm_glr_step")
+        shape.ref, ctypes.byref(g), rows, _dense(slots, torch.int32, (rows,), "slots", dev), n,
+        _dense(state_in, torch.float32, (n, H), "state_in", dev), _dense(state_out, torch.float32, (n, H), "state_out", dev),
+        _dense(y, key[2], (rows, 1, H), "y", dev), _stream_of(stream, dev)), "lstm_glr_step")
 
 
 def block_norm_shape(width, kind: str = "rms", gate: str = "silu", branch_bf16: bool = False, stream_bf16: bool = False,
@@ -738,28 +755,29 @@ def block_norm_shape(width, kind: str = "rms", gate: str = "silu", branch_bf16: 
     return s
 
 
-def _norm_params(shape, p):
+def _norm_params(shape, p, dev):
     """w_post, b_post, scale, w_pre, b_pre of a dict that may lack any of them."""
     d, f32, get = shape.row, torch.float32, p.get
-    return _lib.BlockNormParams(_dense(get("w_post"), f32, d, "w_post"), _dense(get("b_post"), f32, d, "b_post"),
-                                _dense(get("scale"), f32, d, "scale"), _dense(get("w_pre"), f32, d, "w_pre"),
-                                _dense(get("b_pre"), f32, d, "b_pre"))
+    return _lib.BlockNormParams(_dense(get("w_post"), f32, d, "w_post", dev), _dense(get("b_post"), f32, d, "b_post", dev),
+                                _dense(get("scale"), f32, d, "scale", dev), _dense(get("w_pre"), f32, d, "w_pre", dev),
+                                _dense(get("b_pre"), f32, d, "b_pre", dev))
 
 
-def _rows(t, dtype, shape, name):
+def _rows(t, dtype, shape, name, dev):
     """(address, row stride) of a [rows, width] tensor whose columns lie next to each other (None: none)."""
     if t is None:
         return None, 0
     ld, one = t.stride() if t.dim() == 2 else (0, 0)
-    if t.dtype is not dtype or t.shape != shape or (one != 1 and shape[1] > 1):
-        raise ValueError(f"{name}: expected a {dtype} tensor of shape {tuple(shape)} with adjacent columns")
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or (one != 1 and shape[1] > 1):
+        raise ValueError(f"{name}: expected a {dtype} tensor of shape {tuple(shape)} with adjacent columns on cuda:{dev}, "
+                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
     return t.data_ptr(), ld if shape[0] > 1 else shape[1]
 
 
-def _norm_rows(types, shape, x, y, gate, names):
-    yp, yst = _rows(y, types[0], shape, names[1])
-    gp, gst = _rows(gate, types[0], shape, names[2])
-    return _lib.BlockNormInputs(_dense(x, types[1], shape, names[0]), yp, gp, yst, gst)
+def _norm_rows(types, shape, x, y, gate, names, dev):
+    yp, yst = _rows(y, types[0], shape, names[1], dev)
+    gp, gst = _rows(gate, types[0], shape, names[2], dev)
+    return _lib.BlockNormInputs(_dense(x, types[1], shape, names[0], dev), yp, gp, yst, gst)
 
 
 _FORWARD_ROWS, _BACKWARD_ROWS = ("x", "y", "gate"), ("dx", "dy", "dgate")
@@ -771,11 +789,12 @@ def block_norm_forward(shape, x, y, gate, params: dict, x_out, n, stats=None, st
     backward pass."""
     rows, types = x.shape[0], shape.types
     rd = (rows, shape.width)
-    rin = _norm_rows(types, rd, x, y, gate, _FORWARD_ROWS)
-    p = _norm_params(shape, params)
+    dev = _device_of(x, "x")
+    rin = _norm_rows(types, rd, x, y, gate, _FORWARD_ROWS, dev)
+    p = _norm_params(shape, params, dev)
     check(_lib.load().lstm_block_norm_fwd(
-        shape.ref, ctypes.byref(p), ctypes.byref(rin), rows, _dense(x_out, types[1], rd, "x_out"), _dense(n, types[2], rd, "n"),
-        _dense(stats, torch.float32, (rows, 4), "stats"), _stream_of(stream, x)), "lstm_block_norm_fwd")
+        shape.ref, ctypes.byref(p), ctypes.byref(rin), rows, _dense(x_out, types[1], rd, "x_out", dev), _dense(n, types[2], rd, "n", dev),
+        _dense(stats, torch.float32, (rows, 4), "stats", dev), _stream_of(stream, dev)), "lstm_block_norm_fwd")
 
 
 def block_norm_scratch_bytes(shape, rows: int) -> int:
@@ -788,10 +807,11 @@ def block_norm_backward(shape, x, y, gate, params: dict, stats, dx_out, dn, dx, 
     dgate and the gradients of the parameters that `grads` names."""
     rows, types = x.shape[0], shape.types
     rd = (rows, shape.width)
-    rin = _norm_rows(types, rd, x, y, gate, _FORWARD_ROWS)
-    din = _norm_rows(types, rd, dx, dy, dgate, _BACKWARD_ROWS)
-    p, g = _norm_params(shape, params), _norm_params(shape, grads)
+    dev = _device_of(x, "x")
+    rin = _norm_rows(types, rd, x, y, gate, _FORWARD_ROWS, dev)
+    din = _norm_rows(types, rd, dx, dy, dgate, _BACKWARD_ROWS, dev)
+    p, g = _norm_params(shape, params, dev), _norm_params(shape, grads, dev)
     check(_lib.load().lstm_block_norm_bwd(
-        shape.ref, ctypes.byref(p), ctypes.byref(rin), rows, _dense(stats, torch.float32, (rows, 4), "stats"),
-        _dense(dx_out, types[1], rd, "dx_out"), _dense(dn, types[2], rd, "dn"), ctypes.byref(din), ctypes.byref(g),
-        _bytes(scratch, block_norm_scratch_bytes(shape, rows), "scratch"), _stream_of(stream, x)), "lstm_block_norm_bwd")
+        shape.ref, ctypes.byref(p), ctypes.byref(rin), rows, _dense(stats, torch.float32, (rows, 4), "stats", dev),
+        _dense(dx_out, types[1], rd, "dx_out", dev), _dense(dn, types[2], rd, "dn", dev), ctypes.byref(din), ctypes.byref(g),
+        _bytes(scratch, block_norm_scratch_bytes(shape, rows), "scratch", dev), _stream_of(stream, dev)), "lstm_block_norm_bwd")
