@@ -755,7 +755,8 @@ size_t lstm_glr_workspace_bytes(const lstm_plan* plan, const lstm_glr_shape* sha
 
 /* Bytes of the transient scratch of lstm_glr_fwd and lstm_glr_bwd (the maps
  * of the pieces that few long sequences are cut into, so that their pieces
- * run side by side); 0 where none is needed, and on a bad argument. */
+ * run side by side, and a copy of a state that is carried in place); 0 where
+ * none is needed, and on a bad argument. */
 size_t lstm_glr_scratch_bytes(const lstm_plan* plan, const lstm_glr_shape* shape);
 
 /*
@@ -763,7 +764,9 @@ size_t lstm_glr_scratch_bytes(const lstm_plan* plan, const lstm_glr_shape* shape
  *   h0         [ndir][B][H] fp32, caller order; NULL = zero
  *   y          [rows][ndir*H] dtype: h of every row
  *   h_n        [ndir][B][H] fp32: the states after each sequence's last step
- *              (h0 for a sequence of length 0); NULL to skip
+ *              (h0 for a sequence of length 0); NULL to skip.  May be h0
+ *              itself (a state carried in place), but not overlap it otherwise
+ *              (LSTM_ERR_INVALID_ARG)
  *   workspace  lstm_glr_workspace_bytes, kept for lstm_glr_bwd; NULL when no
  *              backward pass follows
  *   scratch    lstm_glr_scratch_bytes, one for each call that may run at the
@@ -782,7 +785,7 @@ lstm_status lstm_glr_fwd(const lstm_plan* plan, const lstm_glr_shape* shape, con
  *   dh_n       [ndir][B][H] fp32, caller order; NULL = zero
  *   grads      dL/df, dL/dz and (gated cell) dL/di
  *   dh0        [ndir][B][H] fp32: dL/dh0 (dh_n for a sequence of length 0);
- *              NULL to skip
+ *              NULL to skip.  May be dh_n itself, but not overlap it otherwise
  *   scratch    as for lstm_glr_fwd
  */
 lstm_status lstm_glr_bwd(const lstm_plan* plan, const lstm_glr_shape* shape, const lstm_glr_gates* gates,
@@ -798,8 +801,8 @@ lstm_status lstm_glr_bwd(const lstm_plan* plan, const lstm_glr_shape* shape, con
  *              slot is outside 0..num_slots-1 is idle: its y is zero and no
  *              state is read or written.  Two live rows must not name the
  *              same slot.
- *   state_in, state_out  [num_slots][H] fp32; may be the same array.  Slots
- *              that no row names are not written.
+ *   state_in, state_out  [num_slots][H] fp32; may be the same array, but not
+ *              overlap otherwise.  Slots that no row names are not written.
  *   y          [rows][H] dtype
  */
 lstm_status lstm_glr_step(const lstm_glr_shape* shape, const lstm_glr_gates* gates, int32_t rows,

@@ -128,10 +128,22 @@ void dispatch(const lstm_glr_shape& s, F&& go)
     }
 }
 
+size_t state_bytes(const ScanPlan& p, int ndir, int H) { return sizeof(float) * ndir * p.p.B * H; }
+
+// The state that comes in and the one that goes out: one array or two, but not parts of each other.
+bool same_or_apart(const float* in, const float* out, size_t bytes)
+{
+    const uintptr_t a = (uintptr_t)in, b = (uintptr_t)out;
+    return !in || !out || in == out || a + bytes <= b || b + bytes <= a;
+}
+
+// Bytes of the finest level's maps, 8 a unit, in blocks of at most 64 units.
+size_t map_bytes(const ScanPlan& p, int ndir, int H) { return (size_t)p.scan.level_count[0] * ndir * (size_t)ceil_div(H, 64) * 64 * 8; }
+
 // Every sequence is empty: what comes in as the state (or its error) goes out unchanged.
 lstm_status pass_through(const float* in, float* out, size_t bytes, cudaStream_t cs)
 {
-    if (!out) return LSTM_OK;
+    if (!out || out == in) return LSTM_OK;
     LSTM_CUDA_TRY(in ? cudaMemcpyAsync(out, in, bytes, cudaMemcpyDeviceToDevice, cs) : cudaMemsetAsync(out, 0, bytes, cs));
     return LSTM_OK;
 }
@@ -199,8 +211,18 @@ bool glr_short(const ScanPlan& p, int V, int ctas, GlrArgs* a)
 
 size_t glr_scratch(const ScanPlan& p, const lstm_glr_shape& s)
 {
-    // the finest level's maps, 8 bytes a unit, in blocks of at most 64 units
-    return p.scan.levels < 2 ? 0 : (size_t)p.scan.level_count[0] * s.num_directions * (size_t)ceil_div(s.hidden_size, 64) * 64 * 8;
+    // the maps, and behind them a copy of the states (glr_carry)
+    const int nd = s.num_directions, H = s.hidden_size;
+    return p.scan.levels < 2 ? 0 : map_bytes(p, nd, H) + state_bytes(p, nd, H);
+}
+
+lstm_status glr_carry(const ScanPlan& p, const GlrArgs& a, const float** in, const float* out, void* scratch, cudaStream_t cs)
+{
+    if (!a.cut || *in != out || !out) return LSTM_OK;
+    float* const copy = (float*)((char*)scratch + map_bytes(p, a.ndir, a.H));
+    LSTM_CUDA_TRY(cudaMemcpyAsync(copy, out, state_bytes(p, a.ndir, a.H), cudaMemcpyDeviceToDevice, cs));
+    *in = copy;
+    return LSTM_OK;
 }
 
 }  // namespace lstm
@@ -233,7 +255,9 @@ lstm_status lstm_glr_fwd(const lstm_plan* plan, const lstm_glr_shape* shape, con
     const lstm_glr_shape& s = *shape;
     cudaStream_t cs = (cudaStream_t)stream;
     if (!aligned(h0, 4) || !aligned(h_n, 4) || !aligned(workspace, 16) || !aligned(scratch, 16) || !right_device(p)) return LSTM_ERR_INVALID_ARG;
-    if (p.rows == 0) return pass_through(h0, h_n, sizeof(float) * s.num_directions * p.B * s.hidden_size, cs);
+    const size_t states = state_bytes(sp, s.num_directions, s.hidden_size);
+    if (!same_or_apart(h0, h_n, states)) return LSTM_ERR_INVALID_ARG;
+    if (p.rows == 0) return pass_through(h0, h_n, states, cs);
     if (!y || !aligned(y, s.dtype == LSTM_BF16 ? 2 : 4) ||
         !good_gates(s, gates->f, gates->z, gates->i, gates->row_stride, gates->dir_stride))
         return LSTM_ERR_INVALID_ARG;
@@ -255,7 +279,9 @@ lstm_status lstm_glr_bwd(const lstm_plan* plan, const lstm_glr_shape* shape, con
     const lstm_glr_shape& s = *shape;
     cudaStream_t cs = (cudaStream_t)stream;
     if (!aligned(dh_n, 4) || !aligned(dh0, 4) || !aligned(workspace, 16) || !aligned(scratch, 16) || !right_device(p)) return LSTM_ERR_INVALID_ARG;
-    if (p.rows == 0) return pass_through(dh_n, dh0, sizeof(float) * s.num_directions * p.B * s.hidden_size, cs);
+    const size_t states = state_bytes(sp, s.num_directions, s.hidden_size);
+    if (!same_or_apart(dh_n, dh0, states)) return LSTM_ERR_INVALID_ARG;
+    if (p.rows == 0) return pass_through(dh_n, dh0, states, cs);
     if (!workspace || !dy || !aligned(dy, s.dtype == LSTM_BF16 ? 2 : 4) ||
         !good_gates(s, gates->f, gates->z, gates->i, gates->row_stride, gates->dir_stride) ||
         !good_gates(s, grads->f, grads->z, grads->i, grads->row_stride, grads->dir_stride))
@@ -279,6 +305,7 @@ lstm_status lstm_glr_step(const lstm_glr_shape* shape, const lstm_glr_gates* gat
     if (rows == 0) return LSTM_OK;
     if (!y || !aligned(y, s.dtype == LSTM_BF16 ? 2 : 4) || !aligned(slots, 4) || !aligned(state_in, 4) ||
         !aligned(state_out, 4) || (num_slots > 0 && (!state_in || !state_out)) ||
+        !same_or_apart(state_in, state_out, sizeof(float) * num_slots * s.hidden_size) ||
         !good_gates(s, gates->f, gates->z, gates->i, gates->row_stride, gates->dir_stride))
         return LSTM_ERR_INVALID_ARG;
     GlrArgs a;

@@ -396,6 +396,9 @@ inline int glr_groups(int H) { return H > 16 ? 2 : 4; }
 // `ctas` is what an SM holds of the scan kernel, `scratch` the caller's (null: uncut).
 void glr_cut(const ScanPlan& p, int V, int ctas, void* scratch, GlrArgs* a);      // (groups set)
 size_t glr_scratch(const ScanPlan& p, const lstm_glr_shape& s);
+// Every piece of a cut sequence reads the state that comes in, whichever piece writes the one that goes out: where both are
+// one array, `in` becomes a copy of it in the scratch.
+lstm_status glr_carry(const ScanPlan& p, const GlrArgs& a, const float** in, const float* out, void* scratch, cudaStream_t cs);
 // Whether each warp takes a sequence of its own (uncut: fills the pieces' fields).
 bool glr_short(const ScanPlan& p, int V, int ctas, GlrArgs* a);
 

@@ -398,7 +398,9 @@ lstm_status go(const ScanPlan& p, GlrArgs a, void* scratch, cudaStream_t cs)
     if (C::GROUPED) a.groups = glr_groups(a.H);
     glr_cut(p, C::V, C::CTAS, scratch, &a);
     if (a.cut) {
-        const lstm_status st = glr_launch(p.p, glr_fwd_map_kernel<T, GATED, ROWS>, a, C::V, M::SMEM, ready_map, cs);
+        lstm_status st = glr_carry(p, a, &a.h0, a.h_n, scratch, cs);
+        if (st != LSTM_OK) return st;
+        st = glr_launch(p.p, glr_fwd_map_kernel<T, GATED, ROWS>, a, C::V, M::SMEM, ready_map, cs);
         if (st != LSTM_OK) return st;
     }
     return glr_launch(p.p, glr_fwd_kernel<T, GATED, ROWS>, a, C::V, C::SMEM, ready, cs);

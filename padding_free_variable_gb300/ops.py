@@ -698,8 +698,8 @@ def glr_workspace_bytes(plan: Plan, shape) -> int:
 
 
 def glr_forward(plan: Plan, shape, f, z, i, h0, y, h_n, workspace, stream=None):
-    """lstm_glr_fwd: f, z and (gated cell) i [rows, ndir, H] views, h0 / h_n [ndir, B, H] fp32 in caller order or None,
-    y [rows, ndir, H]; workspace: a buffer of glr_workspace_bytes that glr_backward reads, or None."""
+    """lstm_glr_fwd: f, z and (gated cell) i [rows, ndir, H] views, h0 / h_n [ndir, B, H] fp32 in caller order or None
+    (they may be one tensor), y [rows, ndir, H]; workspace: a buffer of glr_workspace_bytes that glr_backward reads, or None."""
     key, rows = shape.key, plan.rows
     nd, H, dt, _ = key
     dev = _device_of(f, "gates")
@@ -714,7 +714,8 @@ def glr_forward(plan: Plan, shape, f, z, i, h0, y, h_n, workspace, stream=None):
 
 
 def glr_backward(plan: Plan, shape, f, z, i, workspace, dy, dh_n, df, dz, di, dh0, stream=None):
-    """lstm_glr_bwd: dy [rows, ndir, H], dh_n / dh0 [ndir, B, H] fp32 or None, df, dz, di [rows, ndir, H] views."""
+    """lstm_glr_bwd: dy [rows, ndir, H], dh_n / dh0 [ndir, B, H] fp32 or None (they may be one
+    tensor), df, dz, di [rows, ndir, H] views."""
     key, rows = shape.key, plan.rows
     nd, H, dt, _ = key
     dev = _device_of(f, "gates")
