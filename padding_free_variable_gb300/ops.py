@@ -5,6 +5,7 @@ PyTorch is used for device memory and streams only; every step of the path
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 
 import numpy as np
@@ -678,28 +679,35 @@ def _glr_sizes(plan: Plan, shape):
     return got
 
 
-def _glr_scratch(plan: Plan, key, need: int, stream: int, device):
-    """The plan's scratch for calls of this shape on this stream: calls on different streams may run at the same time."""
+def _glr_scratch(plan: Plan, key, need: int, stream: int, dev: int):
+    """A scratch that no call of this plan on another stream shares (None: none is needed).  Calls that a graph captures,
+    whose replays may run on any stream, get one each, from the graph's own memory; the others of a stream and shape, which
+    run one after another, share one that the plan keeps."""
     if need == 0:
         return None
-    buf = plan.scratch.get((key, stream))
-    if buf is None:
-        if stream == torch._C._cuda_getCurrentRawStream(device.index):
-            buf = torch.empty(need, dtype=torch.uint8, device=device)
-        else:       # memory that the allocator ties to the stream that uses it
-            with torch.cuda.stream(torch.cuda.ExternalStream(stream, device)):
-                buf = torch.empty(need, dtype=torch.uint8, device=device)
-        plan.scratch[key, stream] = buf
-    return buf.data_ptr()
+    here = stream == torch._C._cuda_getCurrentRawStream(dev)
+    with contextlib.nullcontext() if here else torch.cuda.stream(torch.cuda.ExternalStream(stream, dev)):
+        if torch.cuda.is_current_stream_capturing():
+            return torch.empty(need, dtype=torch.uint8, device=dev)
+        buf = plan.scratch.get((key, stream))
+        if buf is None:
+            buf = plan.scratch[key, stream] = torch.empty(need, dtype=torch.uint8, device=dev)
+        return buf
 
 
 def glr_workspace_bytes(plan: Plan, shape) -> int:
     return _glr_sizes(plan, shape)[0]
 
 
-def glr_forward(plan: Plan, shape, f, z, i, h0, y, h_n, workspace, stream=None):
+def glr_scratch_bytes(plan: Plan, shape) -> int:
+    """Bytes of the scratch that glr_forward and glr_backward take (0: none is used)."""
+    return _glr_sizes(plan, shape)[1]
+
+
+def glr_forward(plan: Plan, shape, f, z, i, h0, y, h_n, workspace, stream=None, scratch=None):
     """lstm_glr_fwd: f, z and (gated cell) i [rows, ndir, H] views, h0 / h_n [ndir, B, H] fp32 in caller order or None
-    (they may be one tensor), y [rows, ndir, H]; workspace: a buffer of glr_workspace_bytes that glr_backward reads, or None."""
+    (they may be one tensor), y [rows, ndir, H]; workspace: a buffer of glr_workspace_bytes that glr_backward reads, or None; scratch: a
+    buffer of glr_scratch_bytes for this call alone while it runs, or None for one of the plan's."""
     key, rows = shape.key, plan.rows
     nd, H, dt, _ = key
     dev = _device_of(f, "gates")
@@ -707,15 +715,17 @@ def glr_forward(plan: Plan, shape, f, z, i, h0, y, h_n, workspace, stream=None):
     st = (nd, plan.batch, H)
     need, most = _glr_sizes(plan, shape)
     stream = _stream_of(stream, dev)
+    if scratch is None:
+        scratch = _glr_scratch(plan, key, most, stream, dev)
     check(_lib.load().lstm_glr_fwd(
         plan.handle, shape.ref, ctypes.byref(g), _dense(h0, torch.float32, st, "h0", dev), _dense(y, dt, (rows, nd, H), "y", dev),
         _dense(h_n, torch.float32, st, "h_n", dev), _bytes(workspace, need, "workspace", dev),
-        _glr_scratch(plan, key, most, stream, f.device), stream), "lstm_glr_fwd")
+        _bytes(scratch, most, "scratch", dev), stream), "lstm_glr_fwd")
 
 
-def glr_backward(plan: Plan, shape, f, z, i, workspace, dy, dh_n, df, dz, di, dh0, stream=None):
+def glr_backward(plan: Plan, shape, f, z, i, workspace, dy, dh_n, df, dz, di, dh0, stream=None, scratch=None):
     """lstm_glr_bwd: dy [rows, ndir, H], dh_n / dh0 [ndir, B, H] fp32 or None (they may be one
-    tensor), df, dz, di [rows, ndir, H] views."""
+    tensor), df, dz, di [rows, ndir, H] views; scratch as for glr_forward."""
     key, rows = shape.key, plan.rows
     nd, H, dt, _ = key
     dev = _device_of(f, "gates")
@@ -724,10 +734,12 @@ def glr_backward(plan: Plan, shape, f, z, i, workspace, dy, dh_n, df, dz, di, dh
     st = (nd, plan.batch, H)
     need, most = _glr_sizes(plan, shape)
     stream = _stream_of(stream, dev)
+    if scratch is None:
+        scratch = _glr_scratch(plan, key, most, stream, dev)
     check(_lib.load().lstm_glr_bwd(
         plan.handle, shape.ref, ctypes.byref(g), _bytes(workspace, need, "workspace", dev), _dense(dy, dt, (rows, nd, H), "dy", dev),
         _dense(dh_n, torch.float32, st, "dh_n", dev), ctypes.byref(dg), _dense(dh0, torch.float32, st, "dh0", dev),
-        _glr_scratch(plan, key, most, stream, f.device), stream), "lstm_glr_bwd")
+        _bytes(scratch, most, "scratch", dev), stream), "lstm_glr_bwd")
 
 
 def glr_step(shape, f, z, i, state_in, state_out, y, slots=None, stream=None):
