@@ -508,8 +508,8 @@ lstm_status lstm_plan_recurrent_groups(const lstm_plan* plan, int32_t pass, int3
  * split the gate errors between them; else per-step launches), 0 = per-step
  * launches both ways, 1 = the persistent kernels both ways where they apply
  * (either form), 2 = the persistent kernels without thread-block clusters
- * (forward: every CTA reads each operand tile from L2 itself instead of
- * sharing it by multicast; backward: every CTA streams all 4H gate errors).
+ * (forward: the same kernel, launched without them; backward: every CTA
+ * streams all 4H gate errors).
  * lstm_plan_recurrent_config reports the persistent kernels' cluster size in
  * `variant`.  LSTM_ERR_INVALID_ARG outside -1..2. */
 lstm_status lstm_debug_wide_recurrence(lstm_plan* plan, int32_t mode);

@@ -15,10 +15,11 @@
 //    a double-buffered global array that L2 holds; a CTA streams the part it
 //    needs in 128-row x 64-column TMA tiles through a ring of up to 4 stages
 //    into tcgen05.mma (M = 128 rows of the batch per tile, fp32 accumulator in
-//    tensor memory).  Forward, every CTA needs all of h_{t-1}: CTAs are grouped
-//    in clusters of CS (4 when the device co-schedules them), each tile is read
-//    from L2 once per cluster and multicast into all CS CTAs, and each CTA's
-//    MMA completion frees the ring stage in all of them (multicast commit).
+//    tensor memory).  Forward, every CTA needs all of h_{t-1} and loads every
+//    tile itself: sharing each tile's load among the CTAs of a cluster of four
+//    was no faster (H = 1024, 256 sequences: 1.85 ms a layer shared, 1.83
+//    ms unshared), and so the library has no load that more than one CTA
+//    receives.
 //  * Backward, R^T da needs all 4H gate errors for every unit.  In clusters of
 //    four CTAs, CTA r takes only gate r's H errors against R^T rows of the
 //    cluster's 64 units (64 x H resident, N = 64), so it streams a quarter of
@@ -192,34 +193,26 @@ struct RingPos {
 // One step's product: D[tile m][rows][N] = sum over the KB blocks of A (the operand tiles of
 // columns x0 + 64 kb, streamed from rows ybase + 128 m) times the resident weight slice (B, N
 // rows per block).
-// Thread 0 arms the ring and issues its share of the TMA tiles (with CS > 1: tile i by
-// cluster rank i mod CS, multicast to the whole cluster), thread 32 issues the MMAs and frees
-// each stage in every CTA of the cluster; prod / cons carry the ring position across
-// steps (each only in its own thread).
-template <int CS>
+// Thread 0 arms the ring and issues the TMA tiles, thread 32 issues the MMAs and frees each
+// stage; prod / cons carry the ring position across steps (each only in its own thread).
 __device__ __forceinline__ bool wide_product(const WideSmem& m, const CUtensorMap* mapA, int x0, int ybase, int MT,
                                              int KB, int N, uint32_t tmem, const WideArgs& a, RingPos& prod,
-                                             RingPos& cons, bool& w_ready, unsigned where, int crank)
+                                             RingPos& cons, bool& w_ready, unsigned where)
 {
     bool ok = true;
-    constexpr uint16_t kMask = (uint16_t)((1u << CS) - 1u);
     if (threadIdx.x == 0) {
         fence_async_global();
         for (int t = 0; t < MT && ok; ++t)
             for (int kb = 0; kb < KB; ++kb, prod.advance(m.stages)) {
                 const int st = prod.st;
-                // the stage's previous tile has been consumed by every CTA of the cluster
+                // the stage's previous tile has been consumed
                 if (prod.it >= (uint32_t)m.stages && !tc::mbar_wait(&m.empty[st], prod.ph ^ 1u, a.wait_limit_ns)) {
                     record_failure(a.status, LSTM_ERR_TIMEOUT, where | 0x1000u);
                     ok = false;
                     break;
                 }
                 tc::mbar_arrive_expect_tx(&m.full[st], kWTile);
-                if (CS == 1)
-                    tc::tma_load_2d(m.ring + (size_t)st * kWTile, mapA, &m.full[st], x0 + kb * 64, ybase + t * 128);
-                else if ((t * KB + kb) % CS == crank)
-                    tc::tma_load_2d_multicast(m.ring + (size_t)st * kWTile, mapA, &m.full[st], x0 + kb * 64,
-                                              ybase + t * 128, kMask);
+                tc::tma_load_2d(m.ring + (size_t)st * kWTile, mapA, &m.full[st], x0 + kb * 64, ybase + t * 128);
                 m.counters[0] = (int)prod.it + 1;
             }
     } else if (threadIdx.x == 32) {
@@ -247,8 +240,7 @@ __device__ __forceinline__ bool wide_product(const WideSmem& m, const CUtensorMa
                 for (int kk = 0; kk < 4; ++kk)
                     tc::mma_bf16_ss(tmem + (uint32_t)(t * N), tc::sdesc_sw128(a0 + kk * 32), tc::sdesc_sw128(b0 + kk * 32),
                                     idesc, (kb | kk) != 0 ? 1u : 0u);
-                if (CS == 1) tc::mma_commit(&m.empty[st]);
-                else tc::mma_commit_multicast(&m.empty[st], kMask);
+                tc::mma_commit(&m.empty[st]);
                 m.counters[1] = (int)cons.it + 1;
             }
         tc::mma_commit(m.mma_bar);
@@ -260,12 +252,10 @@ __device__ __forceinline__ bool wide_product(const WideSmem& m, const CUtensorMa
 }
 
 // Before a CTA leaves: no TMA tile may still be landing in its shared memory, no MMA may
-// still use its tensor memory, and (clusters) no peer's stage-release or partial product may
-// still be on its way to it -- every wait bounded.  A clean run waits only for the peers'
-// releases of the ring's last uses; after a timeout the CTA also waits for the tiles it armed
-// and then gives any multicast tile already issued by a peer a millisecond to land.
-// MC: CTAs sharing each operand tile (multicast); CL: the launch has clusters.
-template <int MC, bool CL>
+// still use its tensor memory, and (CL: the CTAs of a cluster exchange partial products) no
+// peer's partial product may still be on its way to it -- every wait bounded.  After a timeout
+// the CTA waits for the tiles it armed.
+template <bool CL>
 __device__ __forceinline__ void wide_finish(const WideSmem& m, uint32_t it_prod, uint32_t mma_phase, bool failed)
 {
     if (threadIdx.x == 0) {
@@ -276,16 +266,6 @@ __device__ __forceinline__ void wide_finish(const WideSmem& m, uint32_t it_prod,
             tc::mbar_wait(m.mma_bar, (mma_phase - 1) & 1, kWTeardownNs);
         }
         tc::mbar_wait(m.w_bar, 0, kWTeardownNs);
-        if (MC > 1) {
-            // each stage's last use released by every CTA of the cluster
-            for (uint32_t it = it_prod > ns ? it_prod - ns : 0u; it < it_prod; ++it)
-                tc::mbar_wait(&m.empty[it % ns], (it / ns) & 1, failed ? 1000000ull : kWTeardownNs);
-            if (failed) {
-                const unsigned long long t0 = global_timer_ns();
-                while (global_timer_ns() - t0 < 1000000ull) {
-                }
-            }
-        }
     }
     if (CL) {
         __syncthreads();
@@ -298,7 +278,6 @@ __device__ __forceinline__ void wide_finish(const WideSmem& m, uint32_t it_prod,
 // Forward.  Operand array a.xbuf: [ndir][2][B][H] bf16, step s reads parity s & 1 and
 // writes parity (s + 1) & 1.  Tensor maps: mapW = R as [ndir*4H][H] (boxes 16 rows x 64),
 // mapA = a.xbuf as [ndir*2*B][H] (boxes 128 rows x 64).
-template <int CS>
 __global__ void __launch_bounds__(kWT, 1) lstm_rec_fwd_wide_kernel(WideArgs a, const __grid_constant__ CUtensorMap mapW,
                                                                   const __grid_constant__ CUtensorMap mapA)
 {
@@ -308,14 +287,13 @@ __global__ void __launch_bounds__(kWT, 1) lstm_rec_fwd_wide_kernel(WideArgs a, c
     const int nd4H = a.ndir * 4 * H, ndH = a.ndir * H;
     const WideSmem m = wide_smem(KB, 64, a.stages, 0);
     const int warp = threadIdx.x >> 5;
-    const int crank = CS > 1 ? (int)cooperative_groups::this_cluster().block_rank() : 0;
     const int tile = threadIdx.x >> 7, j = threadIdx.x;      // this thread's row of the batch
     unsigned* ctr = a.ctr + dir;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < a.stages; ++s) {
             tc::mbar_init(&m.full[s], 1);
-            tc::mbar_init(&m.empty[s], CS);          // one release from each CTA of the cluster
+            tc::mbar_init(&m.empty[s], 1);
         }
         tc::mbar_init(m.mma_bar, 1);
         tc::mbar_init(m.w_bar, 1);
@@ -342,7 +320,6 @@ __global__ void __launch_bounds__(kWT, 1) lstm_rec_fwd_wide_kernel(WideArgs a, c
     tc::tc_fence_before_sync();
     __syncthreads();
     tc::tc_fence_after_sync();
-    if (CS > 1) cooperative_groups::this_cluster().sync();   // every peer's barriers exist before any multicast
     const uint32_t tmem = *m.tmem_slot;
 
     float creg[kWU];                                  // c of this thread's row, step to step
@@ -381,8 +358,8 @@ __global__ void __launch_bounds__(kWT, 1) lstm_rec_fwd_wide_kernel(WideArgs a, c
         wstamp(a, false, dir, cta, s, 1);
         const int MT = (n_prev + 127) / 128;
         if (MT > 0) {
-            bool ok = wide_product<CS>(m, &mapA, 0, (dir * 2 + (s & 1)) * B, MT, KB, 64, tmem, a, prod, cons,
-                                       w_ready, 0xA0000u | (unsigned)(s & 0xfff), crank);
+            bool ok = wide_product(m, &mapA, 0, (dir * 2 + (s & 1)) * B, MT, KB, 64, tmem, a, prod, cons, w_ready,
+                                   0xA0000u | (unsigned)(s & 0xfff));
             ++mma_phase;
             // one thread polls the product's completion; the others wait at the barrier below
             if (threadIdx.x == 0) ok = tc::mbar_wait(m.mma_bar, (mma_phase - 1) & 1, a.wait_limit_ns) && ok;
@@ -471,7 +448,7 @@ __global__ void __launch_bounds__(kWT, 1) lstm_rec_fwd_wide_kernel(WideArgs a, c
                 }
         }
     }
-    wide_finish<CS, (CS > 1)>(m, prod.it, mma_phase, failed);
+    wide_finish<false>(m, prod.it, mma_phase, failed);
     tc::tc_fence_before_sync();
     __syncthreads();
     if (warp == 0) {
@@ -603,8 +580,8 @@ __global__ void __launch_bounds__(kWT, 1) lstm_rec_bwd_wide_kernel(WideArgs a, c
         // R^T da of the step after this one (recurrence order), for the rows that have one
         const int MT = (n_next + 127) / 128;
         if (MT > 0) {
-            bool ok = wide_product<1>(m, &mapA, x0, (dir * 2 + (s & 1)) * B, MT, KB, NU, tmem, a, prod, cons,
-                                      w_ready, 0xD0000u | (unsigned)(s & 0xfff), 0);
+            bool ok = wide_product(m, &mapA, x0, (dir * 2 + (s & 1)) * B, MT, KB, NU, tmem, a, prod, cons, w_ready,
+                                   0xD0000u | (unsigned)(s & 0xfff));
             ++mma_phase;
             if (threadIdx.x == 0) ok = tc::mbar_wait(m.mma_bar, (mma_phase - 1) & 1, a.wait_limit_ns) && ok;
             if (__syncthreads_or(!ok)) {
@@ -748,7 +725,7 @@ __global__ void __launch_bounds__(kWT, 1) lstm_rec_bwd_wide_kernel(WideArgs a, c
                 for (int k = 0; k < kWU; ++k) a.dc0[so + k] = dcc[k];
         }
     }
-    wide_finish<1, KS>(m, prod.it, mma_phase, failed);
+    wide_finish<KS>(m, prod.it, mma_phase, failed);
     tc::tc_fence_before_sync();
     __syncthreads();
     if (warp == 0) {
@@ -759,7 +736,7 @@ __global__ void __launch_bounds__(kWT, 1) lstm_rec_bwd_wide_kernel(WideArgs a, c
 
 // ------------------------------------------------------------------------- configuration
 
-constexpr int kWCluster = 4;     // forward: CTAs sharing each operand tile; backward: the K split
+constexpr int kWCluster = 4;     // backward: the K split
 
 static int optin_smem(const Plan& p)
 {
@@ -873,11 +850,10 @@ lstm_status rec_wide_fwd_launch(const Plan& p, WideArgs a, const void* R, cudaSt
         !make_map_bf16_sw128(&mapA, a.xbuf, a.ndir * 2 * a.B, a.H, a.H, 128))
         return LSTM_ERR_UNSUPPORTED;
     const int KB = a.H / 64, ns = wide_stages(p, KB, 64, 0);
-    const WideForm f1 = {(const void*)lstm_rec_fwd_wide_kernel<1>, wide_smem_bytes(KB, 64, ns, 0), ns};
-    const WideForm f4 = {(const void*)lstm_rec_fwd_wide_kernel<kWCluster>, f1.smem, ns};
+    const WideForm form = {(const void*)lstm_rec_fwd_wide_kernel, wide_smem_bytes(KB, 64, ns, 0), ns};
     trace_begin(p, K_REC_FWD, s);
     int cs = 0;
-    const lstm_status st = wide_launch(p, f1, f4, true, a, mapW, mapA, s, &cs);
+    const lstm_status st = wide_launch(p, form, form, true, a, mapW, mapA, s, &cs);
     trace_end(p, K_REC_FWD, s, st == LSTM_OK ? 1 : 0);
     p.last_rec_variant[0] = cs;
     p.last_rec_stages[0] = st == LSTM_OK ? a.stages : 0;

@@ -112,7 +112,7 @@ class Plan:
         kind = ("none", "grid", "cluster", "step_launches", "persistent_wide")[k.value]
         out = {"kernel": kind, "ctas_per_direction": g.value, "product": ("cuda_cores", "mma_sync", "tcgen05")[m.value]}
         if kind == "persistent_wide":
-            out["cluster_size"] = v.value            # CTAs sharing each operand tile by multicast
+            out["cluster_size"] = v.value            # CTAs of a cluster of the launch
         else:
             out.update({"exchange": "bulk" if v.value & 1 else "barrier", "tma_tiles": bool(v.value & 2)})
         return out
