@@ -707,7 +707,8 @@ lstm_status lstm_md_bwd(const lstm_md_plan* plan, const lstm_md_shape* shape, co
  *
  * Arithmetic: the state, the gates and every product are fp32 whatever the
  * dtype; outputs are rounded once.  The order of every sum is fixed by the
- * plan and the shape: repeated calls agree bitwise.
+ * plan and the shape: repeated calls agree bitwise.  sig(f) and products of
+ * such gates are at least 2^-126: an infinite state stays infinite.
  *
  * Device pointers of this section need the alignment of their element type
  * only, workspaces 16 bytes; rows whose pointers, strides and widths allow

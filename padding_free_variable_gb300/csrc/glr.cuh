@@ -85,6 +85,12 @@ __device__ __forceinline__ float min_nan(float a, float b)
     asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
     return r;
 }
+__device__ __forceinline__ float max_nan(float a, float b)
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
 
 // Gates: with e = exp(-x), sig(x) = 1 / (1 + e) and 1 - sig(x) = e / (1 + e).  Both are formed
 // from e, neither by subtracting the other from 1, so a gate near 1 keeps the digits of 1 - a and
@@ -97,6 +103,14 @@ __device__ __forceinline__ F2 sigmoid2(F2 x)
 {
     const F2 t = x * F2(kNegLog2e, kNegLog2e);
     const F2 d = F2(ex2_approx(t.lo()), ex2_approx(t.hi())) + F2(1.f, 1.f);
+    return F2(rcp_approx(d.lo()), rcp_approx(d.hi()));
+}
+
+// The gate of a state: sig(x), at least 2^-126, so that no gate makes a NaN of an infinite state.
+__device__ __forceinline__ F2 forget2(F2 x)
+{
+    const F2 t = x * F2(kNegLog2e, kNegLog2e);
+    const F2 d = F2(ex2_approx(min_nan(t.lo(), 126.f)), ex2_approx(min_nan(t.hi(), 126.f))) + F2(1.f, 1.f);
     return F2(rcp_approx(d.lo()), rcp_approx(d.hi()));
 }
 
@@ -186,6 +200,11 @@ static_assert(kGlrWarps * kGlrSteps == kScanChunk, "a CTA's iteration is one kep
 
 // ---------------------------------------------------------------- affine maps of V units
 
+// Products of gates are held at the smallest normal number (`hold`, before a map is applied or
+// passed on): one that underflowed to 0 would make NaN of an infinite state, which frame by frame
+// stays infinite.  A finite state h gains at most 2^-126 |h| from it.
+constexpr float kLeast = 1.17549435e-38f;
+
 // V values of a lane, in pairs.
 template <int V> struct Vals {
     F2 q[V / 2];
@@ -220,6 +239,16 @@ template <int V> struct Vals {
 #pragma unroll
         for (int v = 0; v < V / 2; ++v) q[v] = sigmoid2(q[v]);
     }
+    __device__ __forceinline__ void forget()
+    {
+#pragma unroll
+        for (int v = 0; v < V / 2; ++v) q[v] = forget2(q[v]);
+    }
+    __device__ __forceinline__ void hold()
+    {
+#pragma unroll
+        for (int v = 0; v < V / 2; ++v) q[v] = F2(max_nan(q[v].lo(), kLeast), max_nan(q[v].hi(), kLeast));
+    }
     __device__ __forceinline__ void sigmoids(Vals& s, Vals& c) const
     {
 #pragma unroll
@@ -247,6 +276,8 @@ template <> struct Vals<1> {
     __device__ __forceinline__ void add(const Vals& a) { q += a.q; }
     __device__ __forceinline__ void sub(const Vals& a) { q -= a.q; }
     __device__ __forceinline__ void sigmoid() { q = rcp_approx(1.f + ex2_approx(q * kNegLog2e)); }
+    __device__ __forceinline__ void forget() { q = rcp_approx(1.f + ex2_approx(min_nan(q * kNegLog2e, 126.f))); }
+    __device__ __forceinline__ void hold() { q = max_nan(q, kLeast); }
     __device__ __forceinline__ void sigmoids(Vals& s, Vals& c) const { sigmoid_pair(q, s.q, c.q); }
     template <typename G> __device__ __forceinline__ void each(G&& value) { q = value(0); }
 };
@@ -463,6 +494,7 @@ template <bool UP, int V> __device__ __forceinline__ void compose_groups(int lan
         u.mad(A, U);
         U = u;
         A.mul(a);
+        A.hold();
     }
 }
 

@@ -154,6 +154,7 @@ __global__ void __launch_bounds__(32 * kGlrWarps, BwdTile<T, GATED, ROWS>::CTAS)
                 U.mad(a, b);
                 A.mul(a);
             }
+            A.hold();
             now[w].put(ul, A, U);
             __syncthreads();
 #pragma unroll
@@ -186,6 +187,7 @@ __global__ void __launch_bounds__(32 * kGlrWarps, BwdTile<T, GATED, ROWS>::CTAS)
                 U.mad(a[k], b[k]);
                 A.mul(a[k]);
             }
+            A.hold();
             Vals<V> AH, UH, AE;     // grouped: of the steps before and after this group's
             if constexpr (C::GROUPED) {
                 AH = AE = A;
@@ -475,7 +477,7 @@ __global__ void __launch_bounds__(32 * kGlrWarps, 3) glr_bwd_map_kernel(const Gl
         for (int k = 0; k < S; ++k) {
             const Raw<T, V> rf = tile.value(lane, 0, k, stage), rd = tile.value(lane, 1, k, stage);
             a[k].each([&](int v) { return rf.get(v); });
-            a[k].sigmoid();
+            a[k].forget();
             d[k].each([&](int v) { return rd.get(v); });
         }
         if (C::STAGED) __syncwarp();
@@ -492,6 +494,7 @@ __global__ void __launch_bounds__(32 * kGlrWarps, 3) glr_bwd_map_kernel(const Gl
             A.mul(a[k]);
         }
     }
+    A.hold();
     if (C::STAGED) cp_async_wait<0>();
     if constexpr (C::GROUPED) compose_groups<false>(lane, tile.lanes, A, U);
     if (g == 0) s_map[w].put(ul, A, U);
@@ -504,6 +507,7 @@ __global__ void __launch_bounds__(32 * kGlrWarps, 3) glr_bwd_map_kernel(const Gl
         U.mad(a, b);
         A.mul(a);
     }
+    A.hold();
     c.map<V>(p, c.piece)->put(ul, A, U);
 }
 

@@ -31,7 +31,7 @@ __device__ __forceinline__ void step_maps(const Tile& t, int lane, int stage, in
     for (int k = 0; k < S; k += V == 1 ? 2 : 1) {
         F2 s, c;
         if (GATED) {
-            s = sigmoid2(t.two(lane, 0, k, stage));
+            s = forget2(t.two(lane, 0, k, stage));
             c = sigmoid2(t.two(lane, 2, k, stage));
         } else {
             sigmoid_pair2(t.two(lane, 0, k, stage), s, c);
@@ -64,6 +64,7 @@ template <int V> __device__ __forceinline__ void compose(const Vals<V> (&a)[kGlr
         U.mad(a[k], b[k]);
         A.mul(a[k]);
     }
+    A.hold();
 }
 
 // 8 rows of y that a warp has staged at `out` ([step][RB]), to memory in 16-byte pieces.
@@ -171,6 +172,7 @@ __global__ void __launch_bounds__(32 * kGlrWarps, FwdTile<T, GATED, ROWS>::CTAS)
                 U.mad(a, b);
                 A.mul(a);
             }
+            A.hold();
             now[w].put(ul, A, U);
             __syncthreads();
 #pragma unroll
@@ -371,6 +373,7 @@ __global__ void __launch_bounds__(32 * kGlrWarps, 3) glr_fwd_map_kernel(const Gl
             A.mul(a[k]);
         }
     }
+    A.hold();
     if (C::STAGED) cp_async_wait<0>();
     if constexpr (C::GROUPED) compose_groups<true>(lane, tile.lanes, A, U);
     if (tile.group(lane) == groups - 1) s_map[w].put(ul, A, U);
@@ -383,6 +386,7 @@ __global__ void __launch_bounds__(32 * kGlrWarps, 3) glr_fwd_map_kernel(const Gl
         U.mad(a, b);
         A.mul(a);
     }
+    A.hold();
     c.map<V>(p, c.piece)->put(ul, A, U);
 }
 
