@@ -5,7 +5,6 @@ PyTorch is used for device memory and streams only; every step of the path
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 
 import numpy as np
@@ -631,7 +630,7 @@ def _dense(t, dtype, shape, name, dev):
 def _bytes(t, need, name, dev):
     if t is None:
         return None
-    if t.get_device() != dev or not t.is_contiguous() or t.numel() * t.element_size() < need:
+    if t.get_device() != dev or not t.is_contiguous() or t.nbytes < need:
         raise ValueError(f"{name}: {need} contiguous bytes on cuda:{dev} are needed")
     return t.data_ptr()
 
@@ -657,16 +656,18 @@ def _glr_gates(key, f, z, i, rows, name, dev):
             raise ValueError(f"{name}: the gated cell has a third one, i, like f and z")
     elif i is not None:
         raise ValueError(f"{name}: i belongs to the gated cell")
-    ld, ds, us = f.stride()
+    if f.get_device() != dev or z.get_device() != dev or (gated and i.get_device() != dev):
+        raise ValueError(f"{name}: expected tensors on cuda:{dev}")
+    strides = f.stride()
+    ld, ds, us = strides
     # the stride of a single row, direction or unit is never stepped over
     ld, ds = ld if rows > 1 else H, ds if nd > 1 else H
-    for t in (f, z, i) if gated else (f, z):
-        if t.get_device() != dev:
-            raise ValueError(f"{name}: expected tensors on cuda:{dev}, got one on {t.device}")
-        a, b, c = t.stride()
-        if (a != ld and rows > 1) or (b != ds and nd > 1) or (c != 1 and H > 1):
-            raise ValueError(f"{name}: units have to lie next to each other, and all gates to have the same strides")
-    return _lib.GlrGates(f.data_ptr(), z.data_ptr(), i.data_ptr() if gated else None, ld, ds)
+    if us != 1 or z.stride() != strides or (gated and i.stride() != strides):
+        for t in (f, z, i) if gated else (f, z):
+            a, b, c = t.stride()
+            if (a != ld and rows > 1) or (b != ds and nd > 1) or (c != 1 and H > 1):
+                raise ValueError(f"{name}: units have to lie next to each other, and all gates to have the same strides")
+    return _lib.pack_rows(f.data_ptr(), z.data_ptr(), i.data_ptr() if gated else 0, ld, ds)
 
 
 def _glr_sizes(plan: Plan, shape):
@@ -680,19 +681,18 @@ def _glr_sizes(plan: Plan, shape):
 
 
 def _glr_scratch(plan: Plan, key, need: int, stream: int, dev: int):
-    """A scratch that no call of this plan on another stream shares (None: none is needed).  Calls that a graph captures,
-    whose replays may run on any stream, get one each, from the graph's own memory; the others of a stream and shape, which
-    run one after another, share one that the plan keeps."""
-    if need == 0:
-        return None
-    here = stream == torch._C._cuda_getCurrentRawStream(dev)
-    with contextlib.nullcontext() if here else torch.cuda.stream(torch.cuda.ExternalStream(stream, dev)):
-        if torch.cuda.is_current_stream_capturing():
-            return torch.empty(need, dtype=torch.uint8, device=dev)
-        buf = plan.scratch.get((key, stream))
-        if buf is None:
-            buf = plan.scratch[key, stream] = torch.empty(need, dtype=torch.uint8, device=dev)
-        return buf
+    """A scratch that no call of this plan on another stream shares.  Calls that a graph captures, whose replays may run on
+    any stream, get one each, from the graph's own memory; the others of a stream and shape, which run one after another,
+    share one that the plan keeps."""
+    if stream != torch._C._cuda_getCurrentRawStream(dev):       # memory that the allocator ties to the stream that uses it
+        with torch.cuda.stream(torch.cuda.ExternalStream(stream, dev)):
+            return _glr_scratch(plan, key, need, stream, dev)
+    if torch._C._cuda_isCurrentStreamCapturing():
+        return torch.empty(need, dtype=torch.uint8, device=dev)
+    buf = plan.scratch.get((key, stream))
+    if buf is None:
+        buf = plan.scratch[key, stream] = torch.empty(need, dtype=torch.uint8, device=dev)
+    return buf
 
 
 def glr_workspace_bytes(plan: Plan, shape) -> int:
@@ -715,10 +715,10 @@ def glr_forward(plan: Plan, shape, f, z, i, h0, y, h_n, workspace, stream=None, 
     st = (nd, plan.batch, H)
     need, most = _glr_sizes(plan, shape)
     stream = _stream_of(stream, dev)
-    if scratch is None:
+    if scratch is None and most > 0:
         scratch = _glr_scratch(plan, key, most, stream, dev)
     check(_lib.load().lstm_glr_fwd(
-        plan.handle, shape.ref, ctypes.byref(g), _dense(h0, torch.float32, st, "h0", dev), _dense(y, dt, (rows, nd, H), "y", dev),
+        plan.handle, shape.ref, g, _dense(h0, torch.float32, st, "h0", dev), _dense(y, dt, (rows, nd, H), "y", dev),
         _dense(h_n, torch.float32, st, "h_n", dev), _bytes(workspace, need, "workspace", dev),
         _bytes(scratch, most, "scratch", dev), stream), "lstm_glr_fwd")
 
@@ -734,11 +734,11 @@ def glr_backward(plan: Plan, shape, f, z, i, workspace, dy, dh_n, df, dz, di, dh
     st = (nd, plan.batch, H)
     need, most = _glr_sizes(plan, shape)
     stream = _stream_of(stream, dev)
-    if scratch is None:
+    if scratch is None and most > 0:
         scratch = _glr_scratch(plan, key, most, stream, dev)
     check(_lib.load().lstm_glr_bwd(
-        plan.handle, shape.ref, ctypes.byref(g), _bytes(workspace, need, "workspace", dev), _dense(dy, dt, (rows, nd, H), "dy", dev),
-        _dense(dh_n, torch.float32, st, "dh_n", dev), ctypes.byref(dg), _dense(dh0, torch.float32, st, "dh0", dev),
+        plan.handle, shape.ref, g, _bytes(workspace, need, "workspace", dev), _dense(dy, dt, (rows, nd, H), "dy", dev),
+        _dense(dh_n, torch.float32, st, "dh_n", dev), dg, _dense(dh0, torch.float32, st, "dh0", dev),
         _bytes(scratch, most, "scratch", dev), stream), "lstm_glr_bwd")
 
 
@@ -749,7 +749,7 @@ def glr_step(shape, f, z, i, state_in, state_out, y, slots=None, stream=None):
     H, dev = key[1], _device_of(f, "gates")
     g = _glr_gates(key, f, z, i, rows, "gates", dev)
     check(_lib.load().lstm_glr_step(
-        shape.ref, ctypes.byref(g), rows, _dense(slots, torch.int32, (rows,), "slots", dev), n,
+        shape.ref, g, rows, _dense(slots, torch.int32, (rows,), "slots", dev), n,
         _dense(state_in, torch.float32, (n, H), "state_in", dev), _dense(state_out, torch.float32, (n, H), "state_out", dev),
         _dense(y, key[2], (rows, 1, H), "y", dev), _stream_of(stream, dev)), "lstm_glr_step")
 
@@ -765,35 +765,36 @@ def block_norm_shape(width, kind: str = "rms", gate: str = "silu", branch_bf16: 
                             int(bool(norm_bf16)), float(eps))
     s.types = tuple(torch.bfloat16 if b else torch.float32 for b in (branch_bf16, stream_bf16, norm_bf16))
     s.row, s.ref = (s.width,), ctypes.byref(s)
+    s.scratch = (0, 0)      # rows and bytes of the last backward call's scratch
     return s
 
 
 def _norm_params(shape, p, dev):
     """w_post, b_post, scale, w_pre, b_pre of a dict that may lack any of them."""
-    d, f32, get = shape.row, torch.float32, p.get
-    return _lib.BlockNormParams(_dense(get("w_post"), f32, d, "w_post", dev), _dense(get("b_post"), f32, d, "b_post", dev),
-                                _dense(get("scale"), f32, d, "scale", dev), _dense(get("w_pre"), f32, d, "w_pre", dev),
-                                _dense(get("b_pre"), f32, d, "b_pre", dev))
+    d, f32 = shape.row, torch.float32
+    return _lib.pack_params(*[_dense(p[k], f32, d, k, dev) or 0 if k in p else 0 for k in _PARAMS])
 
 
 def _rows(t, dtype, shape, name, dev):
-    """(address, row stride) of a [rows, width] tensor whose columns lie next to each other (None: none)."""
+    """(address, row stride) of a [rows, width] tensor whose columns lie next to each other (None: 0, 0)."""
     if t is None:
-        return None, 0
-    ld, one = t.stride() if t.dim() == 2 else (0, 0)
-    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or (one != 1 and shape[1] > 1):
-        raise ValueError(f"{name}: expected a {dtype} tensor of shape {tuple(shape)} with adjacent columns on cuda:{dev}, "
-                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
-    return t.data_ptr(), ld if shape[0] > 1 else shape[1]
+        return 0, 0
+    if t.dtype is dtype and t.shape == shape and t.get_device() == dev:
+        ld, one = t.stride()
+        if one == 1 or shape[1] == 1:
+            return t.data_ptr(), ld if shape[0] > 1 else shape[1]
+    raise ValueError(f"{name}: expected a {dtype} tensor of shape {tuple(shape)} with adjacent columns on cuda:{dev}, "
+                     f"got {t.dtype} {tuple(t.shape)} on {t.device}")
 
 
 def _norm_rows(types, shape, x, y, gate, names, dev):
     yp, yst = _rows(y, types[0], shape, names[1], dev)
     gp, gst = _rows(gate, types[0], shape, names[2], dev)
-    return _lib.BlockNormInputs(_dense(x, types[1], shape, names[0], dev), yp, gp, yst, gst)
+    return _lib.pack_rows(_dense(x, types[1], shape, names[0], dev) or 0, yp, gp, yst, gst)
 
 
 _FORWARD_ROWS, _BACKWARD_ROWS = ("x", "y", "gate"), ("dx", "dy", "dgate")
+_PARAMS = ("w_post", "b_post", "scale", "w_pre", "b_pre")
 
 
 def block_norm_forward(shape, x, y, gate, params: dict, x_out, n, stats=None, stream=None):
@@ -801,12 +802,12 @@ def block_norm_forward(shape, x, y, gate, params: dict, x_out, n, stats=None, st
     b_post, scale, w_pre, b_pre (fp32 [D], any may be absent); writes x_out and n, and stats [rows, 4] fp32 for the
     backward pass."""
     rows, types = x.shape[0], shape.types
-    rd = (rows, shape.width)
+    rd = (rows, shape.row[0])
     dev = _device_of(x, "x")
     rin = _norm_rows(types, rd, x, y, gate, _FORWARD_ROWS, dev)
     p = _norm_params(shape, params, dev)
     check(_lib.load().lstm_block_norm_fwd(
-        shape.ref, ctypes.byref(p), ctypes.byref(rin), rows, _dense(x_out, types[1], rd, "x_out", dev), _dense(n, types[2], rd, "n", dev),
+        shape.ref, p, rin, rows, _dense(x_out, types[1], rd, "x_out", dev), _dense(n, types[2], rd, "n", dev),
         _dense(stats, torch.float32, (rows, 4), "stats", dev), _stream_of(stream, dev)), "lstm_block_norm_fwd")
 
 
@@ -819,12 +820,16 @@ def block_norm_backward(shape, x, y, gate, params: dict, stats, dx_out, dn, dx, 
     """lstm_block_norm_bwd: x, y, gate, params, stats of the forward call; dx_out and dn [rows, D] or None; writes dx, dy,
     dgate and the gradients of the parameters that `grads` names."""
     rows, types = x.shape[0], shape.types
-    rd = (rows, shape.width)
+    rd = (rows, shape.row[0])
     dev = _device_of(x, "x")
     rin = _norm_rows(types, rd, x, y, gate, _FORWARD_ROWS, dev)
     din = _norm_rows(types, rd, dx, dy, dgate, _BACKWARD_ROWS, dev)
     p, g = _norm_params(shape, params, dev), _norm_params(shape, grads, dev)
+    known, need = shape.scratch
+    if known != rows:
+        need = block_norm_scratch_bytes(shape, rows)
+        shape.scratch = (rows, need)
     check(_lib.load().lstm_block_norm_bwd(
-        shape.ref, ctypes.byref(p), ctypes.byref(rin), rows, _dense(stats, torch.float32, (rows, 4), "stats", dev),
-        _dense(dx_out, types[1], rd, "dx_out", dev), _dense(dn, types[2], rd, "dn", dev), ctypes.byref(din), ctypes.byref(g),
-        _bytes(scratch, block_norm_scratch_bytes(shape, rows), "scratch", dev), _stream_of(stream, dev)), "lstm_block_norm_bwd")
+        shape.ref, p, rin, rows, _dense(stats, torch.float32, (rows, 4), "stats", dev),
+        _dense(dx_out, types[1], rd, "dx_out", dev), _dense(dn, types[2], rd, "dn", dev), din, g,
+        _bytes(scratch, need, "scratch", dev), _stream_of(stream, dev)), "lstm_block_norm_bwd")
