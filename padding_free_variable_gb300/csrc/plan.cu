@@ -196,10 +196,13 @@ struct FrameMap {
     int64_t frames = 0;
 };
 
-// The tables of the gated linear recurrence, in one upload.
-static cudaError_t upload_scan_tables(const Plan& p, ScanTables* t)
+// The lengths by slot and, behind them in the same allocation and upload, the tables of the gated
+// linear recurrence: callers of the LSTM layers alone do not pay a copy of their own for them.
+static cudaError_t upload_lengths(Plan& p, ScanTables* t)
 {
-    std::vector<int4> pieces;       // of each level, the first pieces of all slots before their second ones
+    const size_t front = (p.B + 3) / 4;     // of the lengths, in int4
+    std::vector<int4> pieces(front);        // then, of each level, the first pieces of all slots before their second ones
+    std::copy(p.h_len, p.h_len + p.B, (int32_t*)pieces.data());
     std::vector<int32_t> first(p.B);
     for (int32_t l = 0; ; ++l) {
         const int64_t len = (int64_t)kScanPiece << l;
@@ -210,7 +213,7 @@ static cudaError_t upload_scan_tables(const Plan& p, ScanTables* t)
             sum += n;
             most = std::max(most, n);
         }
-        t->level_first[l] = (int32_t)pieces.size();
+        t->level_first[l] = (int32_t)(pieces.size() - front);
         t->level_count[l] = sum;
         for (int32_t k = 0; k < most; ++k)
             for (int32_t j = 0; j < p.B; ++j) {
@@ -231,8 +234,9 @@ static cudaError_t upload_scan_tables(const Plan& p, ScanTables* t)
         t->chunks += (p.h_len[j] + kScanChunk - 1) / kScanChunk;
     }
     chunk[p.B] = (int32_t)t->chunks;
-    const cudaError_t e = upload(&t->d_pieces, pieces.data(), pieces.size());
-    t->d_chunk = (int32_t*)(t->d_pieces + count);
+    const cudaError_t e = upload(&p.d_len, (const int32_t*)pieces.data(), pieces.size() * 4);
+    t->d_pieces = (const int4*)p.d_len + front;
+    t->d_chunk = p.d_len + count * 4;
     return e;
 }
 
@@ -280,12 +284,11 @@ static lstm_status create_plan(const int32_t* lengths, int32_t B, bool padded, l
     if (e == cudaSuccess) e = upload(&p.d_bs, p.h_bs, (size_t)T);
     if (e == cudaSuccess) e = upload(&p.d_off, p.h_off, (size_t)T + 1);
     if (e == cudaSuccess) e = upload(&p.d_perm, p.h_perm, (size_t)B);
-    if (e == cudaSuccess) e = upload(&p.d_len, p.h_len, (size_t)B);
+    if (e == cudaSuccess) e = upload_lengths(p, &hp->scan);
     if (e == cudaSuccess) e = upload(&p.d_row_src, row_src.data(), (size_t)rows);
     if (e == cudaSuccess && fm) e = upload(&p.d_row_dst, row_dst.data(), (size_t)rows);
     if (e == cudaSuccess) e = upload(&p.d_prev_fwd, prev_fwd.data(), (size_t)rows);
     if (e == cudaSuccess) e = upload(&p.d_prev_rev, prev_rev.data(), (size_t)rows);
-    if (e == cudaSuccess) e = upload_scan_tables(p, &hp->scan);
     {   // sorted slot of each packed row (row off[t] + j holds slot j)
         std::vector<int32_t> row_slot(rows);
         for (int t = 0; t < T; ++t)
@@ -298,7 +301,6 @@ static lstm_status create_plan(const int32_t* lengths, int32_t B, bool padded, l
     if (e == cudaSuccess) e = cudaMemset(p.d_status, 0, sizeof(DeviceStatus));
     if (e != cudaSuccess) {
         free_plan(p);
-        cudaFree(hp->scan.d_pieces);
         delete hp;
         return LSTM_ERR_CUDA;
     }
@@ -446,7 +448,6 @@ lstm_status lstm_plan_destroy(lstm_plan* plan)
     if (!plan) return LSTM_OK;
     lstm::ScanPlan* full = static_cast<lstm::ScanPlan*>(plan);
     lstm::free_plan(full->p);
-    cudaFree(full->scan.d_pieces);
     delete full;
     return LSTM_OK;
 }

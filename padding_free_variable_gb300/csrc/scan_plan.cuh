@@ -14,8 +14,8 @@ struct ScanTables {
     int32_t levels = 0;
     int32_t level_first[24] = {};       // first entry of the level in d_pieces
     int32_t level_count[25] = {};
-    int4* d_pieces = nullptr;           // (slot, piece, length of the sequence, entry of the slot's first piece in its level by slot)
-    int32_t* d_chunk = nullptr;         // [B+1] first chunk of each slot; behind the pieces, in their allocation
+    const int4* d_pieces = nullptr;     // (slot, piece, length of the sequence, entry of the slot's first piece in its level by slot)
+    const int32_t* d_chunk = nullptr;   // [B+1] first chunk of each slot (both in the allocation of the plan's d_len)
 };
 
 // What every plan handle points to.
