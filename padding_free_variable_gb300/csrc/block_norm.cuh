@@ -281,14 +281,7 @@ struct RowSum {
     }
 };
 
-// act(q) and act'(q)
-__device__ __forceinline__ void activation(int kind, float q, float& act, float& slope)
-{
-    float s, c;
-    sigmoid_pair(q, s, c);
-    act = kind == LSTM_GATE_SIGMOID ? s : q * s;
-    slope = kind == LSTM_GATE_SIGMOID ? s * c : s * fmaf(q, c, 1.f);
-}
+// act(q)
 __device__ __forceinline__ float activation(int kind, float q)
 {
     const float s = rcp_approx(1.f + ex2_approx(q * kNegLog2e));

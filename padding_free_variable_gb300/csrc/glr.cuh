@@ -175,10 +175,6 @@ template <typename T, int V, typename X> __device__ __forceinline__ void store_v
     }
 }
 
-__device__ __forceinline__ void cp_async4(void* to, const char* from)
-{
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"((unsigned)__cvta_generic_to_shared(to)), "l"(from) : "memory");
-}
 __device__ __forceinline__ void cp_async16(void* to, const char* from)
 {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((unsigned)__cvta_generic_to_shared(to)), "l"(from) : "memory");
