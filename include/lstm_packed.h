@@ -706,7 +706,9 @@ lstm_status lstm_md_bwd(const lstm_md_plan* plan, const lstm_md_shape* shape, co
  * gradients are set to zero).
  *
  * Arithmetic: the state, the gates and every product are fp32 whatever the
- * dtype; outputs are rounded once.  The order of every sum is fixed by the
+ * dtype; outputs are rounded once.  sig uses the hardware's approximations of
+ * the exponential and the reciprocal: the smaller of sig(x) and 1 - sig(x) is
+ * off by at most (8 + |x|) 2^-24 of its value, the larger by less.  The order of every sum is fixed by the
  * plan and the shape: repeated calls agree bitwise.  sig(f) and products of
  * such gates are at least 2^-126: an infinite state stays infinite.
  *
@@ -823,8 +825,8 @@ lstm_status lstm_glr_step(const lstm_glr_shape* shape, const lstm_glr_gates* gat
  *     LSTM_NORM_RMS    norm(v) = v / sqrt(mean(v^2) + eps)
  *     LSTM_NORM_LAYER  norm(v) = (v - mean v) / sqrt(mean((v - mean v)^2) + eps)
  *     LSTM_NORM_NONE   norm(v) = v
- * All arithmetic is fp32; x' and n are each rounded once (n is the norm of the
- * unrounded x').  Column sums of the backward pass are added in a fixed order.
+ * All arithmetic is fp32, sig as in the gated linear recurrence; x' and n are
+ * each rounded once (n is the norm of the unrounded x').  Column sums of the backward pass are added in a fixed order.
  * ====================================================================== */
 
 typedef enum { LSTM_NORM_NONE = 0, LSTM_NORM_RMS = 1, LSTM_NORM_LAYER = 2 } lstm_norm_kind;

@@ -80,3 +80,18 @@ def test_long_memories():
     # 20 000 frames of gates near 1: roundings do not drift beyond their bounds
     for bias in (6.0, 9.0, 12.0):
         Case([20000, 257], 1, 8, "f32", "tied", bias=bias, seed=7).check()
+
+
+@pytest.mark.parametrize("cell", ["tied", "gated"])
+def test_gates_errors_average_out(cell):
+    # h = a h0 with h0 = 1: the gate itself.  A product of n gates drifts by n times their mean error; held to half a rounding
+    # (2^-25 of the value) over every range of gates above 1/2, a million of each
+    o, H, B = ops(), 65536, 16
+    plan, shape = o.Plan([1] * B), o.glr_shape(H, 1, False, cell)
+    h0, zero = torch.ones(1, B, H, device="cuda"), torch.zeros(B, 1, H, device="cuda")
+    y = torch.empty_like(zero)
+    for lo, hi in ((0, 1), (1, 2), (2, 4), (4, 8), (8, 12), (12, 16)):
+        f = torch.rand(B, 1, H, generator=torch.Generator(device="cuda").manual_seed(lo), device="cuda") * (hi - lo) + lo
+        o.glr_forward(plan, shape, f, zero, zero if cell == "gated" else None, h0, y, None, None)
+        off = y.double() / torch.sigmoid(f.double()) - 1
+        assert abs(float(off.mean())) < 2.0 ** -25 and float(off.abs().max()) < 16 * ref.U
