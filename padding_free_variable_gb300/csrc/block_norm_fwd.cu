@@ -193,7 +193,12 @@ template <typename TB, typename TS, int VEC, int PER, int KIND, int GATE, bool S
 
 template <typename TB, typename TS, int KIND, int GATE> lstm_status go(const NormArgs& a, cudaStream_t cs)
 {
-    // values of a thread: 32 where rows are many, 8 where a call's few rows leave SMs idle
+    // Values of a thread: 8, 16 or 32.  8 where a call's few rows leave SMs idle: RMS, bf16, in a graph, 8 rows
+    // of 1024 2.7 / 3.3 / 4.1 us, 304 rows 3.2 / 3.8 / 4.6, 304 of 4096 4.5 / 4.6 / 5.5, 608 of 4096 7.5 / 5.6 / 6.2.
+    // Where rows are many (4e7 values, cold L2), 16 up to 512 columns and 32 beyond, which keeps a row
+    // within a warp: centred bf16 512 119 / 80 / 91 us, 520 171 / 146 / 136, 768 126 / 105 / 101, 1024 122 / 91 / 93;
+    // centred fp32 512 148 / 130 / 154, 520 185 / 199 / 156, 4096 181 / 187 / 160.  Up to 256 columns 8: fp32 128
+    // 122 / 124 / 128, bf16 78 / 68 / 72.  Value by value 255 columns (1e7 values, fp32) 48 / 56 / 95, 1003 52 / 64 / 107.
     auto threads = [&](int each) { return row_threads(ceil_div(a.D, each)); };
     const bool few = a.rows <= 304;
     if (norm_whole(a)) {

@@ -198,6 +198,9 @@ bool glr_short(const ScanPlan& p, int V, int ctas, GlrArgs* a)
     // A warp takes 8 steps at a time, all warps that the GPU holds at once: the longest sequence's
     // tiles against an even share.  A CTA's 64 steps cost it as much for a sequence of 8.  512
     // directions of 70 frames of 1024 bf16 units forward / backward: 42 / 87 us, a CTA each 76 / 136 us.
+    // Sequences of two tiles at most need no such share: 64 of 16 frames of 512 bf16 units 3.6 / 5.0 us in a graph, a
+    // CTA each 6.2 / 8.6; few of them come out alike (8: 3.5 / 4.7 and 3.3 / 4.3), three tiles no more (8 of 24 frames:
+    // 4.0 / 5.8 and 3.6 / 4.0).
     const int64_t items = (int64_t)ceil_div(a->H, 32 * V) * a->ndir * p.p.B, warps = (int64_t)p.p.num_sms * ctas * kGlrWarps;
     const int64_t longest = ceil_div(p.p.T, kGlrSteps), share = p.p.rows / kGlrSteps * (items / p.p.B) / warps;
     if (longest > 2 && (items * 2 < warps || longest > 2 * share + 8)) return false;
