@@ -713,7 +713,7 @@ lstm_status lstm_md_bwd(const lstm_md_plan* plan, const lstm_md_shape* shape, co
  * such gates are at least 2^-126: an infinite state stays infinite.
  *
  * Device pointers of this section need the alignment of their element type
- * only, workspaces 16 bytes; rows whose pointers, strides and widths allow
+ * only, workspaces and scratch 16 bytes; rows whose pointers, strides and widths allow
  * 8- or 16-byte accesses are read and written that way.
  * Every device pointer of this section and the next belongs to the current
  * device, where the kernels run.
@@ -886,8 +886,9 @@ typedef struct {
  * Forward pass over `rows` rows.
  *   x_out   [rows][D] stream dtype: x'; may be x itself; NULL with y NULL
  *   n       [rows][D] norm dtype; NULL with pre_kind NONE
- *   stats   [rows][4] fp32 (mean and 1/deviation of both norms), kept for
- *           lstm_block_norm_bwd; NULL when no backward pass follows
+ *   stats   [rows][4] fp32 (mean and 1/deviation of both norms), 16-byte
+ *           aligned, kept for lstm_block_norm_bwd; NULL when no backward pass
+ *           follows
  */
 lstm_status lstm_block_norm_fwd(const lstm_block_norm_shape* shape, const lstm_block_norm_params* params,
                                 const lstm_block_norm_inputs* in, int64_t rows, void* x_out, void* n,
