@@ -681,12 +681,16 @@ def _glr_sizes(plan: Plan, shape):
 
 
 def _glr_scratch(plan: Plan, key, need: int, stream: int, dev: int):
-    """A scratch that no call of this plan on another stream shares.  Calls that a graph captures, whose replays may run on
-    any stream, get one each, from the graph's own memory; the others of a stream and shape, which run one after another,
-    share one that the plan keeps."""
-    if stream != torch._C._cuda_getCurrentRawStream(dev):       # memory that the allocator ties to the stream that uses it
-        with torch.cuda.stream(torch.cuda.ExternalStream(stream, dev)):
-            return _glr_scratch(plan, key, need, stream, dev)
+    """A scratch that no call of this plan on another stream shares."""
+    if stream == torch._C._cuda_getCurrentRawStream(dev):
+        return _current_scratch(plan, key, need, stream, dev)
+    with torch.cuda.stream(torch.cuda.ExternalStream(stream, dev)):     # memory that the allocator ties to the stream that uses it
+        return _current_scratch(plan, key, need, stream, dev)
+
+
+def _current_scratch(plan: Plan, key, need: int, stream: int, dev: int):
+    """The same for the current stream.  Calls that a graph captures, whose replays may run on any stream, get one each, from
+    the graph's own memory; the others of a stream and shape, which run one after another, share one that the plan keeps."""
     if torch._C._cuda_isCurrentStreamCapturing():
         return torch.empty(need, dtype=torch.uint8, device=dev)
     buf = plan.scratch.get((key, stream))
