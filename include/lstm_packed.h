@@ -713,8 +713,8 @@ lstm_status lstm_md_bwd(const lstm_md_plan* plan, const lstm_md_shape* shape, co
  * such gates are at least 2^-126: an infinite state stays infinite.
  *
  * Device pointers of this section need the alignment of their element type
- * only, workspaces and scratch 16 bytes; rows whose pointers, strides and widths allow
- * 8- or 16-byte accesses are read and written that way.
+ * only, workspaces and scratch 16 bytes; rows whose pointers, strides and
+ * widths allow 8- or 16-byte accesses are read and written that way.
  * Every device pointer of this section and the next belongs to the current
  * device, where the kernels run.
  * ====================================================================== */

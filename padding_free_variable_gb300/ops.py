@@ -769,7 +769,7 @@ def block_norm_shape(width, kind: str = "rms", gate: str = "silu", branch_bf16: 
                             int(bool(norm_bf16)), float(eps))
     s.types = tuple(torch.bfloat16 if b else torch.float32 for b in (branch_bf16, stream_bf16, norm_bf16))
     s.row, s.ref = (s.width,), ctypes.byref(s)
-    s.scratch = (0, 0)      # rows and bytes of the last backward call's scratch
+    s.scratch = (-1, 0)     # rows and bytes of the last backward call's scratch
     return s
 
 
