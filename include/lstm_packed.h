@@ -913,6 +913,232 @@ lstm_status lstm_block_norm_bwd(const lstm_block_norm_shape* shape, const lstm_b
                                 const void* dx_out, const void* dn, const lstm_block_norm_input_grads* din,
                                 const lstm_block_norm_grads* grads, void* scratch, void* stream);
 
+/* ======================================================================
+ * Linear attention with a decay for each head, over the packed rows
+ *
+ * The recurrence with a matrix for a state.  Per direction, head and sequence,
+ * with lambda = exp(log_decay[direction][head]) in [0, 1]:
+ *     S_t = lambda S_{t-1} + k_t v_t^T        [key_size x value_size]
+ *     o_t = scale * S_t^T q_t                 (the frame itself included)
+ * S_0 = 0 unless given.  The reverse direction runs from the last frame to the
+ * first.  Works on every plan, as the gated linear recurrence does: packed,
+ * segments, windows, and the padded comparator (whose masked rows read
+ * nothing; their outputs and gradients are set to zero).
+ *
+ * Arithmetic: sums and states are fp32 whatever the dtype, outputs and
+ * gradients are rounded once.  With LSTM_BF16 the products between two frames
+ * of one chunk (q k^T with their decay) are rounded to bf16 before they weigh
+ * the values, as operands of a product; states are carried in fp32 and enter
+ * products as two or three bf16 pieces.  Every order of summation is fixed by
+ * the plan and the shape: repeated calls agree bitwise.  A log_decay above 0
+ * counts as 0, one below -138 as -138 (lambda^n = 0 for n > 0 in fp32).  An
+ * infinity or NaN in a frame may reach every frame of its head and sequence,
+ * earlier ones too, but no other head, direction or sequence.
+ *
+ * Pointers need the alignment of their element type only, scratch 16 bytes.
+ * Every device pointer belongs to the current device.  bf16 rows whose
+ * pointers and strides are multiples of 16 bytes and whose sizes are multiples
+ * of 8 run on the tensor cores, the rest on CUDA cores.
+ * ====================================================================== */
+
+typedef struct {
+    int32_t num_heads;       /* per direction, 1..4096 */
+    int32_t key_size;        /* 1..128 (else LSTM_ERR_UNSUPPORTED) */
+    int32_t value_size;      /* 1..128 */
+    int32_t num_directions;  /* 1 (forward only) or 2 (forward and reverse) */
+    int32_t dtype;           /* lstm_dtype of q, k, v, y and their gradients */
+    float scale;             /* finite */
+} lstm_la_shape;
+
+/* Rows of one operand, device: value c of head h of direction d in row r at
+ * ptr[r * row_stride + d * dir_stride + h * head_stride + c] (elements), so
+ * that q, k and v may be blocks of one projection's output in any order.
+ * Strides are 0 (read by all alike) or more. */
+typedef struct {
+    const void* ptr;
+    int64_t row_stride;
+    int64_t dir_stride;
+    int64_t head_stride;
+} lstm_la_rows;
+
+typedef struct {
+    lstm_la_rows q;
+    lstm_la_rows k;
+    lstm_la_rows v;
+} lstm_la_inputs;
+
+/* Gradients in the same form (blocks of one buffer, with strides of their
+ * own); overwritten.  No two values may share a place (LSTM_ERR_INVALID_ARG):
+ * an input that heads or directions share has a gradient for each of them. */
+typedef struct {
+    void* ptr;
+    int64_t row_stride;
+    int64_t dir_stride;
+    int64_t head_stride;
+} lstm_la_grad_rows;
+
+typedef struct {
+    lstm_la_grad_rows dq;
+    lstm_la_grad_rows dk;
+    lstm_la_grad_rows dv;
+} lstm_la_grads;
+
+/* Bytes of the transient scratch of lstm_la_fwd and lstm_la_bwd (the states at
+ * the starts of the pieces that few long sequences are cut into); 0 where none
+ * is needed, and on a bad argument. */
+size_t lstm_la_scratch_bytes(const lstm_plan* plan, const lstm_la_shape* shape);
+
+/*
+ * Forward pass.
+ *   log_decay  [ndir][num_heads] fp32, device: ln lambda
+ *   s0         [ndir][B][num_heads][key_size][value_size] fp32, caller order;
+ *              NULL = zero
+ *   y          [rows][ndir][num_heads][value_size] dtype: o of every row
+ *   s_n        as s0: the states after each sequence's last step (s0 for a
+ *              sequence of length 0); NULL to skip.  May be s0 itself, but not
+ *              overlap it otherwise (LSTM_ERR_INVALID_ARG)
+ *   scratch    lstm_la_scratch_bytes, one for each call that may run at the
+ *              same time; NULL: no sequence is cut (slower for few long ones)
+ * The plan's device must be the current one (else LSTM_ERR_INVALID_ARG).
+ */
+lstm_status lstm_la_fwd(const lstm_plan* plan, const lstm_la_shape* shape, const lstm_la_inputs* in,
+                        const float* log_decay, const float* s0, void* y, float* s_n, void* scratch,
+                        void* stream);
+
+/*
+ * Backward pass of the loss L = sum <y, dy> + <s_n, ds_n>.  Nothing is kept by
+ * the forward pass: the states are run again.  The decays are constants.
+ *   in, log_decay, s0  as given to lstm_la_fwd
+ *   dy         [rows][ndir][num_heads][value_size] dtype
+ *   ds_n       as s_n, caller order; NULL = zero
+ *   grads      dL/dq, dL/dk, dL/dv
+ *   ds0        as s0: dL/ds0 (ds_n for a sequence of length 0); NULL to skip.
+ *              May be ds_n itself, but not overlap it otherwise
+ *   scratch    as for lstm_la_fwd
+ */
+lstm_status lstm_la_bwd(const lstm_plan* plan, const lstm_la_shape* shape, const lstm_la_inputs* in,
+                        const float* log_decay, const float* s0, const void* dy, const float* ds_n,
+                        const lstm_la_grads* grads, float* ds0, void* scratch, void* stream);
+
+/*
+ * One new frame of each of `rows` streams (num_directions must be 1), without a
+ * plan: the recurrence as it is written.
+ *   in         `rows` rows
+ *   slots      [rows] int32, device: the state of each stream in a cache of
+ *              num_slots states; NULL = stream r has state r.  A row whose slot
+ *              is outside 0..num_slots-1 is idle: its y is zero and no state is
+ *              read or written.  Two live rows must not name the same slot.
+ *   state_in, state_out  [num_slots][num_heads][key_size][value_size] fp32; may
+ *              be the same array, but not overlap otherwise.  Slots that no row
+ *              names are not written.
+ *   y          [rows][num_heads][value_size] dtype
+ */
+lstm_status lstm_la_step(const lstm_la_shape* shape, const lstm_la_inputs* in, const float* log_decay,
+                         int32_t rows, const int32_t* slots, int32_t num_slots, const float* state_in,
+                         float* state_out, void* y, void* stream);
+
+/* ======================================================================
+ * Norms of queries and keys for each head, with the position rotation
+ *
+ * What stands between a projection and its attention, in one pass over the
+ * heads: each head's query (and key) of head_size values is normalised, weighted
+ * and its first rotary_size values are rotated in pairs by an angle that grows
+ * with the frame's position:
+ *     u = norm(x) * w                     lstm_norm_kind; w NULL: 1
+ *     a' = (a cos p - b sin p) * rotary_scale,  b' = (a sin p + b cos p) * rotary_scale
+ * for every pair (a, b) of u, p = position * frequency of the pair.  Pairs are
+ * (i, i + rotary_size / 2) with LSTM_ROTARY_HALF, (2i, 2i + 1) with
+ * LSTM_ROTARY_INTERLEAVED; values from rotary_size on are not rotated.
+ *
+ * Angles are exact for far positions: frequencies are given in units of 2^-64
+ * turn a position, and position * frequency is taken modulo one turn in
+ * integers before the sine and cosine of what remains (fp32).  All other
+ * arithmetic is fp32; outputs are rounded once; sums over rows have a fixed
+ * order.
+ * ====================================================================== */
+
+typedef enum { LSTM_ROTARY_HALF = 0, LSTM_ROTARY_INTERLEAVED = 1 } lstm_rotary_layout;
+
+typedef struct {
+    int32_t q_heads;       /* 1..4096 */
+    int32_t k_heads;       /* 0 (no keys) .. 4096 */
+    int32_t head_size;     /* 1..256 (else LSTM_ERR_UNSUPPORTED) */
+    int32_t kind;          /* lstm_norm_kind; no biases */
+    int32_t rotary_size;   /* even, 0..head_size */
+    int32_t layout;        /* lstm_rotary_layout */
+    int32_t dtype;         /* lstm_dtype of q, k, what they become, and their gradients */
+    float eps;             /* > 0 */
+    float rotary_scale;    /* finite; 1 but for scalings that ask for another */
+} lstm_qk_norm_shape;
+
+/* Device: weights fp32 [head_size], shared by the heads (with kind NONE they
+ * must be NULL); turns int64 [rotary_size / 2], frequencies in 2^-64 turn a
+ * position (NULL with rotary_size 0); positions int32 [rows], or NULL: row r of
+ * the plan is at first_position + its step. */
+typedef struct {
+    const float* w_q;
+    const float* w_k;
+    const int64_t* turns;
+    const int32_t* positions;
+    int64_t first_position;
+} lstm_qk_norm_params;
+
+/* Rows of queries and keys, device: value c of head h in row r at
+ * q[r * q_row_stride + h * q_head_stride + c]; k NULL with k_heads 0. */
+typedef struct {
+    const void* q;
+    const void* k;
+    int64_t q_row_stride;
+    int64_t q_head_stride;
+    int64_t k_row_stride;
+    int64_t k_head_stride;
+} lstm_qk_rows;
+
+/* The same, written.  No two values may share a place (LSTM_ERR_INVALID_ARG). */
+typedef struct {
+    void* q;
+    void* k;
+    int64_t q_row_stride;
+    int64_t q_head_stride;
+    int64_t k_row_stride;
+    int64_t k_head_stride;
+} lstm_qk_out_rows;
+
+/* Gradients of the weights, fp32 [head_size], overwritten; NULL: not wanted. */
+typedef struct {
+    float* w_q;
+    float* w_k;
+} lstm_qk_norm_grads;
+
+/*
+ * Forward pass over `rows` rows.
+ *   plan    where positions come from when params->positions is NULL (then
+ *           rows must be its rows); NULL otherwise.  Masked rows of the padded
+ *           comparator give zeros (and no gradient).
+ *   out     may be `in` itself, with the same strides, but not overlap it
+ *           otherwise
+ */
+lstm_status lstm_qk_norm_fwd(const lstm_plan* plan, const lstm_qk_norm_shape* shape,
+                             const lstm_qk_norm_params* params, const lstm_qk_rows* in, int64_t rows,
+                             const lstm_qk_out_rows* out, void* stream);
+
+/* Bytes of lstm_qk_norm_bwd's scratch (partial sums of the weights' gradients).
+ * 0 on a bad argument. */
+size_t lstm_qk_norm_scratch_bytes(const lstm_qk_norm_shape* shape, int64_t rows);
+
+/*
+ * Backward pass: nothing but the inputs is kept from the forward pass.
+ *   in      as given to lstm_qk_norm_fwd
+ *   dout    dL/d(what the queries and keys became)
+ *   din     dL/dq and dL/dk; may be `dout` itself, with the same strides
+ *   grads   dL/dw_q and dL/dw_k
+ *   scratch 16-byte aligned; NULL when no weight's gradient is wanted
+ */
+lstm_status lstm_qk_norm_bwd(const lstm_plan* plan, const lstm_qk_norm_shape* shape,
+                             const lstm_qk_norm_params* params, const lstm_qk_rows* in, int64_t rows,
+                             const lstm_qk_rows* dout, const lstm_qk_out_rows* din,
+                             const lstm_qk_norm_grads* grads, void* scratch, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -40,12 +40,15 @@ EXPORTED = (
     "lstm_md_plan_enable_timing", "lstm_md_plan_read_timing", "lstm_md_debug_skip_arrival",
     "lstm_glr_workspace_bytes", "lstm_glr_scratch_bytes", "lstm_glr_fwd", "lstm_glr_bwd", "lstm_glr_step",
     "lstm_block_norm_fwd", "lstm_block_norm_scratch_bytes", "lstm_block_norm_bwd",
+    "lstm_la_scratch_bytes", "lstm_la_fwd", "lstm_la_bwd", "lstm_la_step",
+    "lstm_qk_norm_fwd", "lstm_qk_norm_scratch_bytes", "lstm_qk_norm_bwd",
 )
 
 KERNEL_KINDS = ("pack", "unpack", "input_gemm", "rec_fwd", "rec_bwd", "gemm_dx", "gemm_dw", "gemm_dr", "convert")
 GLR_CELLS = ("tied", "gated")
 NORM_KINDS = ("none", "rms", "layer")
 GATE_KINDS = ("none", "sigmoid", "silu")
+ROTARY_LAYOUTS = ("half", "interleaved")
 MD_KINDS = ("md_input", "md_fwd", "md_bwd", "md_grads")
 
 
@@ -115,9 +118,48 @@ class BlockNormInputs(ctypes.Structure):
                 ("y_stride", ctypes.c_int64), ("gate_stride", ctypes.c_int64)]
 
 
+class LaShape(ctypes.Structure):
+    _fields_ = [(k, ctypes.c_int32) for k in ("num_heads", "key_size", "value_size", "num_directions", "dtype")] + \
+        [("scale", ctypes.c_float)]
+
+
+class LaRows(ctypes.Structure):
+    """lstm_la_rows and lstm_la_grad_rows."""
+    _fields_ = [("ptr", ctypes.c_void_p), ("row_stride", ctypes.c_int64), ("dir_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64)]
+
+
+class LaInputs(ctypes.Structure):
+    """lstm_la_inputs and lstm_la_grads."""
+    _fields_ = [("q", LaRows), ("k", LaRows), ("v", LaRows)]
+
+
+class QkNormShape(ctypes.Structure):
+    _fields_ = [(k, ctypes.c_int32) for k in ("q_heads", "k_heads", "head_size", "kind", "rotary_size", "layout", "dtype")] + \
+        [("eps", ctypes.c_float), ("rotary_scale", ctypes.c_float)]
+
+
+class QkNormParams(ctypes.Structure):
+    _fields_ = [(k, ctypes.c_void_p) for k in ("w_q", "w_k", "turns", "positions")] + [("first_position", ctypes.c_int64)]
+
+
+class QkRows(ctypes.Structure):
+    """lstm_qk_rows and lstm_qk_out_rows."""
+    _fields_ = [("q", ctypes.c_void_p), ("k", ctypes.c_void_p)] + \
+        [(k, ctypes.c_int64) for k in ("q_row_stride", "q_head_stride", "k_row_stride", "k_head_stride")]
+
+
+class QkNormGrads(ctypes.Structure):
+    _fields_ = [("w_q", ctypes.c_void_p), ("w_k", ctypes.c_void_p)]
+
+
 # The bytes of a GlrGates or BlockNormInputs, and of a BlockNormParams: for a call, a quarter of the time of making the structure.
 pack_rows = struct.Struct("@PPPqq").pack
 pack_params = struct.Struct("@PPPPP").pack
+pack_la = struct.Struct("@PqqqPqqqPqqq").pack          # a LaInputs
+pack_qk = struct.Struct("@PPqqqq").pack                # a QkRows
+pack_qk_params = struct.Struct("@PPPPq").pack
+pack_qk_grads = struct.Struct("@PP").pack
 
 
 class LSTMError(RuntimeError):
@@ -210,6 +252,13 @@ def _declare(lib):
         "lstm_block_norm_fwd": (c, [ctypes.POINTER(BlockNormShape), vp, vp, i64, vp, vp, vp, vp]),
         "lstm_block_norm_scratch_bytes": (sz, [ctypes.POINTER(BlockNormShape), i64]),
         "lstm_block_norm_bwd": (c, [ctypes.POINTER(BlockNormShape), vp, vp, i64, vp, vp, vp, vp, vp, vp, vp]),
+        "lstm_la_scratch_bytes": (sz, [vp, ctypes.POINTER(LaShape)]),
+        "lstm_la_fwd": (c, [vp, ctypes.POINTER(LaShape), vp, vp, vp, vp, vp, vp, vp]),
+        "lstm_la_bwd": (c, [vp, ctypes.POINTER(LaShape), vp, vp, vp, vp, vp, vp, vp, vp, vp]),
+        "lstm_la_step": (c, [ctypes.POINTER(LaShape), vp, vp, i32, vp, i32, vp, vp, vp, vp]),
+        "lstm_qk_norm_fwd": (c, [vp, ctypes.POINTER(QkNormShape), vp, vp, i64, vp, vp]),
+        "lstm_qk_norm_scratch_bytes": (sz, [ctypes.POINTER(QkNormShape), i64]),
+        "lstm_qk_norm_bwd": (c, [vp, ctypes.POINTER(QkNormShape), vp, vp, i64, vp, vp, vp, vp, vp]),
         "lstm_plan_dims": (c, [pi32, i32, i32, pi32, ctypes.POINTER(i64)]),
         "lstm_plan_compute_host": (c, [pi32, i32, i32, pi32, pi32, pi32, pi32, pi32, pi32, pi32]),
     }

@@ -1,0 +1,81 @@
+// la.cuh -- linear attention with a decay for each head: arguments shared by its kernels.
+//
+// One operator serves the forward pass and all three gradients.  In the order of its own time u = 0, 1, ...
+//     out_u = sum_{w <= u} sP lambda^(u-w) (q_u . k_w) v_w + sI lambda^u q_u^T Y
+// where Y [a x b] is what came before; behind c steps Y becomes lambda^c Y + sK sum_w lambda^(c-w) k_w v_w^T.
+//     forward  q, k, v as they are      Y = lambda S_0     sP = sI = scale, sK = 1
+//     dq       dy, v, k                 Y = lambda S_0^T   the same
+//     dk       v, dy, q, time reversed  Y = dS_n^T         sP = sK = scale, sI = 1
+//     dv       k, q, dy, time reversed  Y = dS_n           the same
+// Y holds one factor lambda more than S behind the same steps, and as many as dS in front of them: the final state
+// of the forward pass takes one factor less at its last step (`early`), dS_0 is Y itself.
+#pragma once
+
+#include "scan_plan.cuh"
+
+namespace lstm {
+
+constexpr int kLaMax = 128;             // largest key or value size
+
+struct LaRows {
+    const void* p = nullptr;
+    int64_t row = 0, dir = 0, head = 0;
+};
+
+struct LaJob {
+    LaRows q, k, v, out;                // out is written
+    int a = 0, b = 0;                   // widths of q and k, of v and out
+    const float* init = nullptr;        // [ndir][B][heads][a][b], or [b][a] with `flip`
+    float* fin = nullptr;               // [ndir][B][heads][a][b]
+    float* starts = nullptr;            // cut sequences: Y in front of each piece, [entry][ndir * heads][a][b]
+    float sP = 1.f, sI = 1.f, sK = 1.f;
+    int flip = 0, back = 0, early = 0;
+};
+
+struct LaArgs {
+    int heads = 0, ndir = 0, B = 0, T = 0, padded = 0;
+    const int32_t* off = nullptr;
+    const int32_t* perm = nullptr;
+    const float* log_decay = nullptr;
+    const int4* pieces = nullptr;       // (slot, piece, length of the sequence, entry of the slot's first piece)
+    int count = 0, piece = 0;           // pieces and their steps
+    int jobs = 0;
+    LaJob job[3];
+    DeviceStatus* status = nullptr;
+    unsigned long long limit_ns = 0;
+};
+
+// What a block works on: a piece of a sequence, a direction and head, and one of the jobs (the jobs of one piece
+// next to each other, as they read the same rows).
+struct LaPart {
+    int job, d, h, slot, piece, entry, begin, end, len;
+    bool last;
+};
+
+__device__ __forceinline__ LaPart la_part(const LaArgs& p, unsigned id)
+{
+    LaPart c;
+    c.job = id % p.jobs;
+    id /= p.jobs;
+    const int dh = id % (p.ndir * p.heads);
+    const int4 e = __ldg(p.pieces + id / (p.ndir * p.heads));
+    c.d = dh / p.heads;
+    c.h = dh - c.d * p.heads;
+    c.slot = e.x; c.piece = e.y; c.len = e.z; c.entry = e.w + e.y;
+    c.begin = (int)min((int64_t)e.y * p.piece, (int64_t)e.z);
+    c.end = (int)min((int64_t)c.begin + p.piece, (int64_t)e.z);
+    c.last = c.end == e.z;
+    return c;
+}
+
+// log2 of a head's decay: at most 0, and low enough that any power but the 0th is 0 in fp32.
+__device__ __forceinline__ float la_log2_decay(const LaArgs& p, int d, int h)
+{
+    return fminf(fmaxf(__ldg(p.log_decay + d * p.heads + h), -138.f), 0.f) * 1.4426950408889634f;
+}
+
+lstm_status launch_la_general(const LaArgs& a, bool bf16, bool states, cudaStream_t cs);
+lstm_status launch_la_tensor(const LaArgs& a, bool states, cudaStream_t cs);
+bool la_tensor_fits(const LaArgs& a, int dtype);
+
+}  // namespace lstm

@@ -51,7 +51,7 @@ class Plan:
         lens = np.ascontiguousarray(np.asarray(lengths, dtype=np.int32))
         self.lengths = lens
         self.padded = padded
-        self.scratch = {}       # of the gated linear recurrence: sizes by shape, device buffers by shape and stream
+        self.scratch = {}       # of the recurrences without a recurrent product: sizes by shape, device buffers by shape and stream
         h = ctypes.c_void_p()
         lp = lens.ctypes.data_as(ctypes.POINTER(ctypes.c_int32))
         if segments is not None:
@@ -837,3 +837,203 @@ def block_norm_backward(shape, x, y, gate, params: dict, stats, dx_out, dn, dx, 
         shape.ref, p, rin, rows, _dense(stats, torch.float32, (rows, 4), "stats", dev),
         _dense(dx_out, types[1], rd, "dx_out", dev), _dense(dn, types[2], rd, "dn", dev), din, g,
         _bytes(scratch, need, "scratch", dev), _stream_of(stream, dev)), "lstm_block_norm_bwd")
+
+
+# --------------------------------------------------------------------------- linear attention, norms of queries and keys
+
+def la_shape(num_heads, key_size, value_size, num_directions: int = 1, bf16: bool = False, scale: float | None = None) -> _lib.LaShape:
+    """Linear attention's shape: heads of a direction, widths of a key and of a value, directions, and the factor of the
+    outputs (key_size ** -0.5 unless given)."""
+    s = _lib.LaShape(int(num_heads), int(key_size), int(value_size), int(num_directions),
+                     _lib.LSTM_BF16 if bf16 else _lib.LSTM_F32, float(key_size ** -0.5 if scale is None else scale))
+    s.key = ("la", s.num_directions, s.num_heads, s.key_size, s.value_size, torch.bfloat16 if bf16 else torch.float32)
+    s.ref = ctypes.byref(s)
+    return s
+
+
+def _la_rows(t, dt, want, name, dev):
+    """(address, row, direction and head stride) of a [rows, ndir, heads, width] view whose values lie next to each other."""
+    if t.dtype is not dt or t.shape != want or t.get_device() != dev:
+        raise ValueError(f"{name}: expected a {dt} tensor of shape {tuple(want)} on cuda:{dev}, got {t.dtype} {tuple(t.shape)} on "
+                         f"{t.device}")
+    r, d, h, one = t.stride()
+    if one != 1 and want[3] > 1:
+        raise ValueError(f"{name}: a head's values have to lie next to each other")
+    # the stride of a single row, direction or head is never stepped over
+    return t.data_ptr(), r if want[0] > 1 else 0, d if want[1] > 1 else 0, h if want[2] > 1 else 0
+
+
+def _la_three(key, q, k, v, rows, names, dev):
+    _, nd, heads, dk, dv, dt = key
+    return _lib.pack_la(*_la_rows(q, dt, (rows, nd, heads, dk), names[0], dev), *_la_rows(k, dt, (rows, nd, heads, dk), names[1], dev),
+                        *_la_rows(v, dt, (rows, nd, heads, dv), names[2], dev))
+
+
+_LA_IN, _LA_GRADS = ("q", "k", "v"), ("dq", "dk", "dv")
+
+
+def la_scratch_bytes(plan: Plan, shape) -> int:
+    """Bytes of the scratch that la_forward and la_backward take (0: none is used)."""
+    got = plan.scratch.get(shape.key)
+    if got is None:
+        got = plan.scratch[shape.key] = int(_lib.load().lstm_la_scratch_bytes(plan.handle, shape.ref))
+    return got
+
+
+def la_forward(plan: Plan, shape, q, k, v, log_decay, s0, y, s_n, stream=None, scratch=None):
+    """lstm_la_fwd: q, k [rows, ndir, heads, key_size] and v [rows, ndir, heads, value_size] views of any strides, log_decay
+    fp32 [ndir, heads], s0 / s_n fp32 [ndir, B, heads, key_size, value_size] in caller order or None (they may be one tensor),
+    y [rows, ndir, heads, value_size]; scratch: a buffer of la_scratch_bytes for this call alone while it runs, or None for one
+    of the plan's."""
+    key, rows = shape.key, plan.rows
+    _, nd, heads, dk, dv, dt = key
+    dev = _device_of(q, "q")
+    three = _la_three(key, q, k, v, rows, _LA_IN, dev)
+    st = (nd, plan.batch, heads, dk, dv)
+    most = la_scratch_bytes(plan, shape)
+    stream = _stream_of(stream, dev)
+    if scratch is None and most > 0:
+        scratch = _glr_scratch(plan, key, most, stream, dev)
+    check(_lib.load().lstm_la_fwd(
+        plan.handle, shape.ref, three, _dense(log_decay, torch.float32, (nd, heads), "log_decay", dev),
+        _dense(s0, torch.float32, st, "s0", dev), _dense(y, dt, (rows, nd, heads, dv), "y", dev),
+        _dense(s_n, torch.float32, st, "s_n", dev), _bytes(scratch, most, "scratch", dev), stream), "lstm_la_fwd")
+
+
+def la_backward(plan: Plan, shape, q, k, v, log_decay, s0, dy, ds_n, dq, dk, dv, ds0, stream=None, scratch=None):
+    """lstm_la_bwd: q, k, v, log_decay, s0 of the forward call; dy [rows, ndir, heads, value_size], ds_n / ds0 as s_n or None
+    (they may be one tensor); dq, dk, dv views like q, k, v in which no two values share a place; scratch as for la_forward."""
+    key, rows = shape.key, plan.rows
+    _, nd, heads, wk, wv, dt = key
+    dev = _device_of(q, "q")
+    three = _la_three(key, q, k, v, rows, _LA_IN, dev)
+    grads = _la_three(key, dq, dk, dv, rows, _LA_GRADS, dev)
+    st = (nd, plan.batch, heads, wk, wv)
+    most = la_scratch_bytes(plan, shape)
+    stream = _stream_of(stream, dev)
+    if scratch is None and most > 0:
+        scratch = _glr_scratch(plan, key, most, stream, dev)
+    check(_lib.load().lstm_la_bwd(
+        plan.handle, shape.ref, three, _dense(log_decay, torch.float32, (nd, heads), "log_decay", dev),
+        _dense(s0, torch.float32, st, "s0", dev), _dense(dy, dt, (rows, nd, heads, wv), "dy", dev),
+        _dense(ds_n, torch.float32, st, "ds_n", dev), grads, _dense(ds0, torch.float32, st, "ds0", dev),
+        _bytes(scratch, most, "scratch", dev), stream), "lstm_la_bwd")
+
+
+def la_step(shape, q, k, v, log_decay, state_in, state_out, y, slots=None, stream=None):
+    """lstm_la_step: one frame of each of q.shape[0] streams; q, k [rows, 1, heads, key_size], v and y [rows, 1, heads,
+    value_size]; state_in / state_out fp32 [slots, heads, key_size, value_size] (may be the same); slots: int32 [rows] state of
+    each stream (outside the cache: idle), None for stream r in state r."""
+    key, rows, n = shape.key, q.shape[0], state_in.shape[0]
+    _, nd, heads, dk, dv, dt = key
+    dev = _device_of(q, "q")
+    three = _la_three(key, q, k, v, rows, _LA_IN, dev)
+    st = (n, heads, dk, dv)
+    check(_lib.load().lstm_la_step(
+        shape.ref, three, _dense(log_decay, torch.float32, (nd, heads), "log_decay", dev), rows,
+        _dense(slots, torch.int32, (rows,), "slots", dev), n, _dense(state_in, torch.float32, st, "state_in", dev),
+        _dense(state_out, torch.float32, st, "state_out", dev), _dense(y, dt, (rows, nd, heads, dv), "y", dev),
+        _stream_of(stream, dev)), "lstm_la_step")
+
+
+def rotary_frequencies(rotary_size, base: float = 10000.0, stretch: float = 1.0, trained: float | None = None,
+                       ramp: tuple = (1.0, 32.0)) -> np.ndarray:
+    """Radians a position of each pair, float64 [rotary_size / 2]: base^(-2i / rotary_size), for contexts `stretch` times as
+    long.  Without `trained` every pair turns `stretch` times slower (positions interpolated); with it only those that turn
+    fewer than ramp[0] times within `trained` positions, those that turn more than ramp[1] times keep their speed, and the
+    ones between are mixed in proportion."""
+    r = int(rotary_size)
+    _need(r > 0 and r % 2 == 0 and base > 0 and stretch > 0 and ramp[1] > ramp[0], "rotary_frequencies: sizes out of range")
+    f = float(base) ** (-np.arange(0, r, 2, dtype=np.float64) / r)
+    if trained is None:
+        return f / stretch
+    keep = np.clip((f * trained / (2 * np.pi) - ramp[0]) / (ramp[1] - ramp[0]), 0.0, 1.0)
+    return f * keep + f / stretch * (1.0 - keep)
+
+
+def rotary_table(frequencies, device="cuda") -> torch.Tensor:
+    """int64 [pairs]: frequencies (radians a position, float64) in units of 2^-64 turn, as qk_norm_forward takes them."""
+    f = np.asarray(frequencies, dtype=np.float64)
+    _need(f.ndim == 1 and np.isfinite(f).all(), "rotary_table: finite frequencies of each pair are needed")
+    turns = f.astype(np.longdouble) / (2 * np.arccos(np.longdouble(-1)))
+    turns -= np.floor(turns)
+    high = np.floor(turns * 2 ** 32)                    # 2^64 is more than a double holds exactly: two halves
+    low = np.floor((turns * 2 ** 32 - high) * 2 ** 32)
+    t = (high.astype(np.uint64) << np.uint64(32)) + low.astype(np.uint64)
+    return torch.from_numpy(t.view(np.int64).copy()).to(device)
+
+
+def qk_norm_shape(q_heads, k_heads, head_size, kind: str = "rms", rotary_size: int = 0, layout: str = "half", bf16: bool = False,
+                  eps: float = 1e-6, rotary_scale: float = 1.0) -> _lib.QkNormShape:
+    """Norms of queries and keys: heads of each (k_heads 0: queries alone), the norm over a head, how many of its first values
+    are rotated, in pairs (i, i + rotary_size / 2) ("half") or (2i, 2i + 1) ("interleaved")."""
+    _need(kind in _lib.NORM_KINDS, f"unknown norm {kind!r}")
+    _need(layout in _lib.ROTARY_LAYOUTS, f"unknown layout {layout!r}")
+    s = _lib.QkNormShape(int(q_heads), int(k_heads), int(head_size), _lib.NORM_KINDS.index(kind), int(rotary_size),
+                         _lib.ROTARY_LAYOUTS.index(layout), _lib.LSTM_BF16 if bf16 else _lib.LSTM_F32, float(eps),
+                         float(rotary_scale))
+    s.key = (s.q_heads, s.k_heads, s.head_size, torch.bfloat16 if bf16 else torch.float32)
+    s.ref = ctypes.byref(s)
+    s.scratch = (-1, 0)     # rows and bytes of the last backward call's scratch
+    return s
+
+
+def _qk_rows(key, rows, q, k, names, dev):
+    """lstm_qk_rows of [rows, heads, head_size] views whose values lie next to each other (k None without keys)."""
+    out = []
+    for t, heads, name in ((q, key[0], names[0]), (k, key[1], names[1])):
+        if heads == 0:
+            _need(t is None, f"{name}: the shape has no keys")
+            out.append((0, 0, 0))
+            continue
+        if t is None or t.dtype is not key[3] or t.shape != (rows, heads, key[2]) or t.get_device() != dev:
+            raise ValueError(f"{name}: expected a {key[3]} tensor of shape {(rows, heads, key[2])} on cuda:{dev}, got "
+                             f"{None if t is None else (t.dtype, tuple(t.shape), str(t.device))}")
+        r, h, one = t.stride()
+        if one != 1 and key[2] > 1:
+            raise ValueError(f"{name}: a head's values have to lie next to each other")
+        out.append((t.data_ptr(), r if rows > 1 else 0, h if heads > 1 else 0))
+    (a, ar, ah), (b, br, bh) = out
+    return _lib.pack_qk(a, b, ar, ah, br, bh)
+
+
+def _qk_params(shape, wq, wk, table, positions, rows, first_position, dev):
+    d = (shape.head_size,)
+    return _lib.pack_qk_params(
+        _dense(wq, torch.float32, d, "wq", dev) or 0, _dense(wk, torch.float32, d, "wk", dev) or 0,
+        _dense(table, torch.int64, (shape.rotary_size // 2,), "table", dev) or 0,
+        _dense(positions, torch.int32, (rows,), "positions", dev) or 0, int(first_position))
+
+
+def qk_norm_forward(shape, q, k, wq, wk, table, positions, q_out, k_out, plan: Plan | None = None, first_position: int = 0,
+                    stream=None):
+    """lstm_qk_norm_fwd: q [rows, q_heads, head_size] and k [rows, k_heads, head_size] views (k None without keys), weights fp32
+    [head_size] or None, table of rotary_table (None without a rotation), positions int32 [rows] or None: first_position + the
+    step of the plan's row; writes q_out and k_out (views, may be q and k themselves)."""
+    rows, dev = q.shape[0], _device_of(q, "q")
+    check(_lib.load().lstm_qk_norm_fwd(
+        plan.handle if plan is not None else None, shape.ref, _qk_params(shape, wq, wk, table, positions, rows, first_position, dev),
+        _qk_rows(shape.key, rows, q, k, ("q", "k"), dev), rows, _qk_rows(shape.key, rows, q_out, k_out, ("q_out", "k_out"), dev),
+        _stream_of(stream, dev)), "lstm_qk_norm_fwd")
+
+
+def qk_norm_scratch_bytes(shape, rows: int) -> int:
+    return int(_lib.load().lstm_qk_norm_scratch_bytes(shape.ref, int(rows)))
+
+
+def qk_norm_backward(shape, q, k, wq, wk, table, positions, dq_out, dk_out, dq, dk, dwq, dwk, scratch, plan: Plan | None = None,
+                     first_position: int = 0, stream=None):
+    """lstm_qk_norm_bwd: the forward call's inputs, dq_out and dk_out; writes dq and dk (views, may be dq_out and dk_out
+    themselves) and, where given, dwq and dwk (fp32 [head_size]; scratch: qk_norm_scratch_bytes, None without them)."""
+    rows, dev = q.shape[0], _device_of(q, "q")
+    known, need = shape.scratch
+    if known != rows:
+        need = qk_norm_scratch_bytes(shape, rows)
+        shape.scratch = (rows, need)
+    d = (shape.head_size,)
+    check(_lib.load().lstm_qk_norm_bwd(
+        plan.handle if plan is not None else None, shape.ref, _qk_params(shape, wq, wk, table, positions, rows, first_position, dev),
+        _qk_rows(shape.key, rows, q, k, ("q", "k"), dev), rows, _qk_rows(shape.key, rows, dq_out, dk_out, ("dq_out", "dk_out"), dev),
+        _qk_rows(shape.key, rows, dq, dk, ("dq", "dk"), dev),
+        _lib.pack_qk_grads(_dense(dwq, torch.float32, d, "dwq", dev) or 0, _dense(dwk, torch.float32, d, "dwk", dev) or 0),
+        _bytes(scratch, need, "scratch", dev), _stream_of(stream, dev)), "lstm_qk_norm_bwd")
