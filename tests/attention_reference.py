@@ -82,7 +82,10 @@ def qk_norm(kind, layout, rotary, x, w, freq, pos, eps=1e-6, turn_scale=1.0, dou
     w = np.ones(d) if w is None else w.astype(np.float64)
     left = np.arange(rotary // 2) * (1 if layout == "half" else 2)
     right = left + (rotary // 2 if layout == "half" else 1)
-    ang = pos.astype(np.float64)[:, None] * (np.asarray(freq) if rotary else np.zeros(0))
+    # position 10^12 times a frequency is off by 10^12 2^-53 = 10^-4 in 64 bits: the angle, modulo a turn, in long doubles (2^-64)
+    turn_ = 2 * np.arccos(np.longdouble(-1))
+    ang = pos.astype(np.longdouble)[:, None] * (np.asarray(freq, dtype=np.longdouble) if rotary else np.zeros(0))
+    ang = (ang - turn_ * np.floor(ang / turn_)).astype(np.float64)
     co, si = turn_scale * np.cos(ang)[:, None], turn_scale * np.sin(ang)[:, None]
     ec = abs(turn_scale) * 10 * U
 

@@ -174,7 +174,7 @@ def test_in_place_head_major_and_streams():
         c.check()
         want = [t.clone() for t in c.out]
         x = [t.clone(memory_format=torch.preserve_format) for t in c.x]
-        c.x = [t.transpose(0, 1).contiguous().transpose(0, 1) for t in x]
+        c.x = [t.clone(memory_format=torch.preserve_format) for t in x]
         side = torch.cuda.Stream()
         torch.cuda.synchronize()
         c.forward(out=c.x, stream=side)
