@@ -252,14 +252,16 @@ LaArgs plan_args(const ScanPlan& sp, const lstm_la_shape& s, const float* log_de
 lstm_status run_jobs(const LaArgs& a, const lstm_la_shape& s, cudaStream_t cs)
 {
     if ((int64_t)a.count * a.ndir * a.heads * a.jobs > INT32_MAX) return LSTM_ERR_UNSUPPORTED;
+    const bool bf16 = s.dtype == LSTM_BF16, tensor = bf16 && la_tensor_fits(a);
+    auto launch = [&](bool states) { return tensor ? launch_la_tensor(a, states, cs) : launch_la_general(a, bf16, states, cs); };
     if (a.job[0].starts) {
-        const lstm_status st = launch_la_general(a, s.dtype == LSTM_BF16, true, cs);
+        const lstm_status st = launch(true);
         if (st != LSTM_OK) return st;
         const dim3 grid((unsigned)(a.B * a.ndir * a.heads), ceil_div(s.key_size * s.value_size, 256), a.jobs);
         la_starts_kernel<<<grid, 256, 0, cs>>>(a);
         if (cudaGetLastError() != cudaSuccess) return LSTM_ERR_CUDA;
     }
-    return launch_la_general(a, s.dtype == LSTM_BF16, false, cs);
+    return launch(false);
 }
 
 lstm_status pass_through(const float* in, float* out, size_t bytes, cudaStream_t cs)

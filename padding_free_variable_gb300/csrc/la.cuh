@@ -74,8 +74,36 @@ __device__ __forceinline__ float la_log2_decay(const LaArgs& p, int d, int h)
     return fminf(fmaxf(__ldg(p.log_decay + d * p.heads + h), -138.f), 0.f) * 1.4426950408889634f;
 }
 
+// The padded comparator's rows past a sequence's end: zeros, written by the block of its first piece.
+template <typename T>
+__device__ __forceinline__ void la_past_end(const LaArgs& p, const LaJob& j, const LaPart& c)
+{
+    if (!p.padded || c.piece != 0) return;
+    T* const out = (T*)j.out.p + c.d * j.out.dir + c.h * j.out.head;
+    for (int64_t i = threadIdx.x; i < (int64_t)(p.T - c.len) * j.b; i += blockDim.x)
+        out[(int64_t)(__ldg(p.off + c.len + (int)(i / j.b)) + c.slot) * j.out.row + (int)(i % j.b)] = (T)0.f;
+}
+
+// Where a sequence's state lies, and Y's start for a piece.
+__device__ __forceinline__ int64_t la_state(const LaArgs& p, const LaJob& j, const LaPart& c)
+{
+    return (((int64_t)c.d * p.B + __ldg(p.perm + c.slot)) * p.heads + c.h) * j.a * j.b;
+}
+
+__device__ __forceinline__ float* la_start(const LaArgs& p, const LaJob& j, const LaPart& c)
+{
+    return j.starts + ((int64_t)c.entry * p.ndir * p.heads + c.d * p.heads + c.h) * j.a * j.b;
+}
+
+// No step: the state that came in goes out.
+__device__ __forceinline__ void la_pass(const LaJob& j, int64_t state)
+{
+    if (!j.fin || j.fin == j.init) return;
+    for (int i = threadIdx.x; i < j.a * j.b; i += blockDim.x) j.fin[state + i] = j.init ? j.init[state + i] : 0.f;
+}
+
 lstm_status launch_la_general(const LaArgs& a, bool bf16, bool states, cudaStream_t cs);
 lstm_status launch_la_tensor(const LaArgs& a, bool states, cudaStream_t cs);
-bool la_tensor_fits(const LaArgs& a, int dtype);
+bool la_tensor_fits(const LaArgs& a);     // bf16 rows that its 16-byte loads can take
 
 }  // namespace lstm

@@ -78,25 +78,17 @@ __global__ void __launch_bounds__(kThreads) la_general_kernel(const LaArgs p)
     float* const P = Y + a4 * 4 * ldb;
     const bool rev = (c.d == 1) != (j.back != 0);
     const float l2 = la_log2_decay(p, c.d, c.h);
-    const int seq = __ldg(p.perm + c.slot);
-    const int64_t state = (((int64_t)c.d * p.B + seq) * p.heads + c.h) * a * b;
+    const int64_t state = la_state(p, j, c);
 
-    if (!STATES && p.padded && c.piece == 0) {          // the padded comparator's rows past the end
-        T* out = (T*)j.out.p + c.d * j.out.dir + c.h * j.out.head;
-        for (int64_t i = tid; i < (int64_t)(p.T - c.len) * b; i += kThreads)
-            out[(int64_t)(__ldg(p.off + c.len + (int)(i / b)) + c.slot) * j.out.row + (int)(i % b)] = narrow<T>(0.f);
-    }
-    if (!STATES && c.len == 0) {                         // no step: what came in goes out
-        if (j.fin && j.fin != j.init)
-            for (int i = tid; i < a * b; i += kThreads) j.fin[state + i] = j.init ? j.init[state + i] : 0.f;
-        return;
+    if (!STATES) {
+        la_past_end<T>(p, j, c);
+        if (c.len == 0) return la_pass(j, state);
     }
     if (tid <= kSteps) W[tid] = exp2f(tid * l2);
     __syncthreads();
     {
         const float first = j.early ? W[1] : 1.f;
-        const float* from = STATES ? nullptr : j.starts ? j.starts + ((int64_t)c.entry * p.ndir * p.heads + c.d * p.heads + c.h) * a * b
-                                             : j.init ? j.init + state : nullptr;
+        const float* from = STATES ? nullptr : j.starts ? la_start(p, j, c) : j.init ? j.init + state : nullptr;
         for (int i = tid; i < a4 * 4 * ldb; i += kThreads) {
             const int x = i / ldb, y = i - x * ldb;
             float v = 0.f;
@@ -211,8 +203,7 @@ __global__ void __launch_bounds__(kThreads) la_general_kernel(const LaArgs p)
         }
         __syncthreads();
     }
-    float* const to = STATES ? j.starts + ((int64_t)c.entry * p.ndir * p.heads + c.d * p.heads + c.h) * a * b
-                             : c.last && j.fin ? j.fin + state : nullptr;
+    float* const to = STATES ? la_start(p, j, c) : c.last && j.fin ? j.fin + state : nullptr;
     if (to)
         for (int i = tid; i < a * b; i += kThreads) to[i] = Y[i / b * ldb + i % b];
 }
