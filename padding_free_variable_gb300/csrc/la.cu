@@ -245,7 +245,7 @@ LaArgs plan_args(const ScanPlan& sp, const lstm_la_shape& s, const float* log_de
     a.pieces = sp.scan.d_pieces + sp.scan.level_first[level];
     a.count = sp.scan.level_count[level];
     a.piece = level < sp.scan.levels - 1 ? kScanPiece << level : INT32_MAX;
-    a.status = p.d_status; a.limit_ns = p.wait_limit_ns;
+    a.status = p.d_status; a.limit_ns = p.wait_limit_ns; a.sms = p.num_sms; a.rows = p.rows;
     return a;
 }
 
@@ -341,9 +341,9 @@ lstm_status lstm_la_bwd(const lstm_plan* plan, const lstm_la_shape* shape, const
     for (int n = 0; n < 3; ++n) a.job[n].starts = starts ? (float*)((char*)scratch + n * starts) : nullptr;
     LaJob &jv = a.job[0], &jk = a.job[1], &jq = a.job[2];
     jq.q = g; jq.k = v; jq.v = k; jq.out = rows_of(grads->dq);
-    jq.a = s.value_size; jq.b = s.key_size; jq.init = s0; jq.flip = 1; jq.early = 1; jq.sP = jq.sI = s.scale;
+    jq.a = s.value_size; jq.b = s.key_size; jq.init = s0; jq.flip = 1; jq.early = 1; jq.sP = jq.sI = s.scale; jq.pieces = 2;
     jk.q = v; jk.k = g; jk.v = q; jk.out = rows_of(grads->dk);
-    jk.a = s.value_size; jk.b = s.key_size; jk.init = ds_n; jk.flip = 1; jk.back = 1; jk.sP = jk.sK = s.scale;
+    jk.a = s.value_size; jk.b = s.key_size; jk.init = ds_n; jk.flip = 1; jk.back = 1; jk.sP = jk.sK = s.scale; jk.pieces = 2;
     jv.q = k; jv.k = q; jv.v = g; jv.out = rows_of(grads->dv);
     jv.a = s.key_size; jv.b = s.value_size; jv.init = ds_n; jv.back = 1; jv.sP = jv.sK = s.scale; jv.fin = ds0;
     if (!starts && ds0 && ds0 == ds_n) {

@@ -30,6 +30,7 @@ struct LaJob {
     float* starts = nullptr;            // cut sequences: Y in front of each piece, [entry][ndir * heads][a][b]
     float sP = 1.f, sI = 1.f, sK = 1.f;
     int flip = 0, back = 0, early = 0;
+    int pieces = 3;                     // bf16 pieces of a weighted value in Y's products (tensor cores)
 };
 
 struct LaArgs {
@@ -39,7 +40,8 @@ struct LaArgs {
     const float* log_decay = nullptr;
     const int4* pieces = nullptr;       // (slot, piece, length of the sequence, entry of the slot's first piece)
     int count = 0, piece = 0;           // pieces and their steps
-    int jobs = 0;
+    int jobs = 0, sms = 0;
+    int64_t rows = 0;
     LaJob job[3];
     DeviceStatus* status = nullptr;
     unsigned long long limit_ns = 0;

@@ -1,0 +1,494 @@
+// la_tensor.cuh -- linear attention of bf16 rows on the tensor cores (tcgen05, accumulators in tensor memory).
+//
+// A CTA walks one head of one sequence (or a piece of it) 128 steps at a time.  Per chunk, with M = 128 rows of a product:
+//     S = Q K^T                  128 x 128     O = Q Y           128 x B    (Y in two bf16 pieces)
+//     P = S lambda^(i-j), i >= j, rounded to bf16, back into tensor memory as the next product's left operand
+//     O' = P V                   128 x B       out = sP O' + sI lambda^i O
+//     Y = lambda^n Y + K^T (sK lambda^(n-j) V) A x B            (the weighted values in bf16 pieces)
+// The weighted values enter in three pieces (24 bits) where Y may be asked for in the end, in two (16 bits) where it
+// only serves outputs that are rounded to bf16.  Rows come by cp.async into the 128-byte swizzled layout, one image of 64 columns a panel: read along a row it is the
+// K-major operand of S, read along a column the MN-major operand of the other products, so nothing is transposed.  Y stays in
+// tensor memory; once a chunk it is read, cut into pieces for the next chunk and decayed.
+//
+// CTAs stay on the GPU and take every so-many-th walk; the next chunk's rows, of the same walk or the next, are on their way
+// as soon as the products that read the last ones are done.
+#pragma once
+
+#include <type_traits>
+
+#include "la.cuh"
+#include "tc_ptx.cuh"
+
+namespace lstm {
+
+namespace {
+
+constexpr int kC = 128, kPanel = kC * 128;      // steps of a chunk, bytes of 64 columns of all of them
+
+// A: width of queries and keys, B: of values, padded to 64 or 128.
+template <int A, int B> struct Layout {
+    // two CTAs an SM where their shared and tensor memory allow it, else one of twice the threads
+    static constexpr int T = A == 64 && B == 64 ? 256 : 512, CTAS = A == 64 && B == 64 ? 2 : 1, PARTS = T / 128;
+    static constexpr int Q = 0, K = Q + kC * A * 2, V = K + kC * A * 2, V1 = V + kC * B * 2, V2 = V1 + kC * B * 2;
+    static constexpr bool in_q = A == 128 && B == 128;          // no room: the third piece takes the queries' place
+    static constexpr int V3 = in_q ? Q : V2 + kC * B * 2;
+    static constexpr int Y1 = (in_q ? V2 : V3) + kC * B * 2, Y2 = Y1 + A * B * 2;
+    static constexpr int POWERS = Y2 + A * B * 2;               // [2][64]: lambda^n and lambda^(31-n), of two walks
+    static constexpr int BARS = POWERS + 512, BYTES = BARS + 64;
+    // tensor memory, columns
+    static constexpr uint32_t S = 0, O = 128, Y = O + B, COLUMNS = B == 64 ? 256 : 512;
+    static constexpr int OC = B / PARTS, YC = A == 128 ? B / PARTS : B / (2 * PARTS);       // columns of a thread
+};
+
+__device__ __forceinline__ uint32_t swizzled(int row, int chunk) { return row * 128 + ((chunk ^ (row & 7)) << 4); }
+
+// Where 8 columns from 8 * chunk on of a row lie, panels of `rows` rows.
+__device__ __forceinline__ uint32_t tile_at(int row, int chunk, int panel) { return (chunk >> 3) * panel + swizzled(row, chunk & 7); }
+
+// Descriptor of an MN-major operand in the 128-byte swizzled layout: 64 values of the M or N dimension a 128-byte row, a row
+// a step of K, groups of 8 rows 1024 bytes apart, the next 64 values `panel` bytes on.
+__device__ __forceinline__ uint64_t sdesc_mn(uint32_t saddr, uint32_t panel)
+{
+    return (uint64_t)((saddr >> 4) & 0x3FFFu) | (uint64_t)(panel >> 4) << 16 | (uint64_t)(1024u >> 4) << 32 | (uint64_t)1 << 46 |
+           (uint64_t)2 << 61;
+}
+
+constexpr uint32_t kAmn = 1u << 15, kBmn = 1u << 16;            // instruction descriptor: A, B are MN-major
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool on)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
+}
+
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+__device__ __forceinline__ uint32_t pack2(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+__device__ __forceinline__ float low(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float high(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+// Two values less what their first piece holds.
+__device__ __forceinline__ uint32_t cut(float& x, float& y)
+{
+    const uint32_t w = pack2(x, y);
+    x -= low(w);
+    y -= high(w);
+    return w;
+}
+
+// A walk's place: its part, and the chunk's first step.
+struct LaSpot {
+    LaPart c;
+    int u;
+};
+
+// STATES: only what a piece adds to Y, into `starts`.
+template <int A, int B, bool STATES>
+__global__ void __launch_bounds__(Layout<A, B>::T, Layout<A, B>::CTAS) la_tensor_kernel(const __grid_constant__ LaArgs p, int total)
+{
+    typedef Layout<A, B> L;
+    extern __shared__ __align__(1024) unsigned char sm[];
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, quad = warp % 4, part = warp / 4;
+    const uint32_t base = tc::smem_u32(sm);
+    float* const powers = (float*)(sm + L::POWERS);
+    // S and O, O', Y are done
+    uint64_t* const bar = (uint64_t*)(sm + L::BARS);
+    enum { DONE_S = 0, DONE_O, DONE_Y, BARRIERS };
+    uint32_t* const slot_of_tmem = (uint32_t*)(bar + BARRIERS);
+    int* const stop = (int*)(slot_of_tmem + 1);
+    if (tid == 0) {
+        for (int i = 0; i < BARRIERS; ++i) tc::mbar_init(bar + i, 1);
+        *stop = 0;
+        tc::fence_mbar_init();
+    }
+    if (warp == 0) {
+        tc::tmem_alloc(slot_of_tmem, L::COLUMNS);
+        tc::tmem_relinquish();
+    }
+
+    // the next walk of this CTA that has a step: there and back along the CTAs, as walks get shorter
+    int round = -1;
+    auto next_walk = [&](LaSpot& s) {
+        for (;;) {
+            ++round;
+            const int64_t id = (int64_t)round * gridDim.x + (round & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+            if (id >= total) return false;
+            s.c = la_part(p, (unsigned)id);
+            s.u = s.c.begin;
+            if (STATES) {
+                if (s.c.last) continue;
+            } else {
+                const LaJob& j = p.job[s.c.job];
+                la_past_end<__nv_bfloat16>(p, j, s.c);
+                if (s.c.len == 0) {
+                    la_pass(j, la_state(p, j, s.c));
+                    continue;
+                }
+            }
+            return true;
+        }
+    };
+    // first row of a step (the walk's own lies `slot` behind it); steps past the chunk's end count as its last
+    auto row_of = [&](const LaSpot& s, int back, int step, int n) {
+        const int u = s.u + min(step, n - 1), t = (s.c.d == 1) != (back != 0) ? s.c.len - 1 - u : u;
+        return __ldg(p.off + t);
+    };
+    auto steps_of = [&](const LaSpot& s) { return min(kC, s.c.end - s.u); };
+    // steps that a chunk's state decays by: one less behind the last step of a walk whose final state holds one lambda less
+    auto decay_of = [&](const LaSpot& s) { return steps_of(s) - (s.c.last && s.u + kC >= s.c.end ? p.job[s.c.job].early : 0); };
+    auto set_powers = [&](int which, float l2) {
+        if (tid < 64) powers[which * 64 + tid] = exp2f((tid < 32 ? tid : 63 - tid) * l2);
+    };
+
+    // a chunk's rows: 16 bytes a thread and copy, zeros past the end.  Where they lie is looked up a chunk ahead.
+    constexpr int CHA = A / 8, EACHA = L::T / CHA, ITA = kC / EACHA, CHB = B / 8, EACHB = L::T / CHB, ITB = kC / EACHB;
+    int rows_a[ITA], rows_b[A == B ? 1 : ITB];
+    auto find_rows = [&](const LaSpot& s) {
+        const int n = steps_of(s), back = p.job[s.c.job].back;
+#pragma unroll
+        for (int i = 0; i < ITA; ++i) rows_a[i] = row_of(s, back, i * EACHA + tid / CHA, n);
+        if (A != B) {
+#pragma unroll
+            for (int i = 0; i < ITB; ++i) rows_b[A == B ? 0 : i] = row_of(s, back, i * EACHB + tid / CHB, n);
+        }
+    };
+    auto copy = [&](const LaRows& r, const LaSpot& s, int to, int w, const auto& rows, auto width) {
+        constexpr int CH = decltype(width)::value / 8, EACH = L::T / CH;
+        const int ch = tid % CH, n = ch * 8 < w ? steps_of(s) : 0;
+        const __nv_bfloat16* const from = (const __nv_bfloat16*)r.p + s.c.d * r.dir + s.c.h * r.head + s.c.slot * r.row + (n > 0 ? ch * 8 : 0);
+        const uint32_t at0 = base + to + tile_at(tid / CH, ch, kPanel);     // EACH rows on: the same swizzle, EACH a multiple of 8
+#pragma unroll
+        for (int i = 0; i < kC / EACH; ++i) cp_async16(at0 + i * EACH * 128, from + rows[i] * r.row, i * EACH + tid / CH < n);
+    };
+    auto load_q = [&](const LaSpot& s) {
+        const LaJob& j = p.job[s.c.job];
+        if (!STATES) copy(j.q, s, L::Q, j.a, rows_a, std::integral_constant<int, A>());
+    };
+    auto load_kv = [&](const LaSpot& s) {
+        const LaJob& j = p.job[s.c.job];
+        copy(j.k, s, L::K, j.a, rows_a, std::integral_constant<int, A>());
+        if constexpr (A == B) copy(j.v, s, L::V, j.b, rows_a, std::integral_constant<int, B>());
+        else copy(j.v, s, L::V, j.b, rows_b, std::integral_constant<int, B>());
+    };
+
+    LaSpot at;
+    bool more = next_walk(at);
+    tc::tc_fence_before_sync();
+    __syncthreads();
+    tc::tc_fence_after_sync();
+    const uint32_t tmem = *slot_of_tmem, mine = tmem + ((uint32_t)(quad * 32) << 16);
+    const int row = quad * 32 + lane;                   // of S and O
+    // of Y: with A = 64 the second 64 lanes hold the rows once more, for other columns
+    const int x = row % A, y0 = (A == 128 ? part : (quad >> 1) * L::PARTS + part) * L::YC, o0 = part * L::OC;
+    auto waited = [&](int which, uint32_t phase) {
+        if (!tc::mbar_wait(bar + which, phase, p.limit_ns)) {
+            *(volatile int*)stop = 1;
+            record_failure(p.status, LSTM_ERR_TIMEOUT, 0x90000u | which);
+        }
+        __syncwarp();
+    };
+    // Y in front of a chunk: its pieces for the outputs, decayed by the chunk's steps for the sum of its products.
+    auto put_state = [&](float (&y)[L::YC], float keep) {
+#pragma unroll
+        for (int k = 0; k < L::YC; k += 16) {
+            uint32_t r[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(y[k + e] * keep);
+            tc::tmem_st_32x32b_x16(mine + L::Y + y0 + k, r);
+        }
+        if (!STATES) {
+#pragma unroll
+            for (int k = 0; k < L::YC; k += 8) {
+                uint4 hi, lo;
+                hi.x = cut(y[k], y[k + 1]); hi.y = cut(y[k + 2], y[k + 3]); hi.z = cut(y[k + 4], y[k + 5]); hi.w = cut(y[k + 6], y[k + 7]);
+                lo = make_uint4(pack2(y[k], y[k + 1]), pack2(y[k + 2], y[k + 3]), pack2(y[k + 4], y[k + 5]), pack2(y[k + 6], y[k + 7]));
+                const uint32_t to = tile_at(x, (y0 + k) / 8, A * 128);
+                *(uint4*)(sm + L::Y1 + to) = hi;
+                *(uint4*)(sm + L::Y2 + to) = lo;
+            }
+        }
+        tc::tmem_wait_st();
+    };
+    auto load_columns = [&](uint32_t column, auto& v) {
+        constexpr int N = sizeof(v) / sizeof(v[0]);
+        uint32_t r[N / 16][16];
+#pragma unroll
+        for (int k = 0; k < N / 16; ++k) tc::tmem_ld_32x32b_x16(mine + column + 16 * k, r[k]);
+        tc::tmem_wait_ld();
+#pragma unroll
+        for (int k = 0; k < N; ++k) v[k] = __uint_as_float(r[k / 16][k % 16]);
+    };
+    // Y in front of a walk; false: nothing
+    auto first_state = [&](const LaSpot& s, float l2) {
+        const LaJob& j = p.job[s.c.job];
+        const float* from = STATES ? nullptr : j.starts ? la_start(p, j, s.c) : j.init ? j.init + la_state(p, j, s.c) : nullptr;
+        if (!from) return false;
+        const bool flip = j.flip && !j.starts;
+        const float first = j.early && !j.starts ? exp2f(l2) : 1.f;
+        float y[L::YC];
+        if (!flip && ((uintptr_t)from & 15) == 0) {
+#pragma unroll
+            for (int k = 0; k < L::YC; k += 4) {
+                const float4 q = x < j.a && y0 + k < j.b ? *(const float4*)(from + x * j.b + y0 + k) : make_float4(0.f, 0.f, 0.f, 0.f);
+                y[k] = first * q.x; y[k + 1] = first * q.y; y[k + 2] = first * q.z; y[k + 3] = first * q.w;
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < L::YC; ++k) {
+                const int col = y0 + k;
+                y[k] = x < j.a && col < j.b ? first * from[flip ? col * j.a + x : x * j.b + col] : 0.f;
+            }
+        }
+        put_state(y, exp2f(decay_of(s) * l2));
+        return true;
+    };
+
+    float l2 = 0.f;
+    bool carry = false;                                 // is there anything in Y?
+    int table = 0;
+    if (more) {
+        find_rows(at);
+        load_q(at);
+        load_kv(at);
+        l2 = la_log2_decay(p, at.c.d, at.c.h);
+        set_powers(0, l2);
+        carry = first_state(at, l2);
+    }
+    for (uint32_t phase = 0; more; phase ^= 1) {
+        const LaJob& j = p.job[at.c.job];
+        const int n = steps_of(at), steps = (n + 15) / 16;
+        const bool final = at.u + kC >= at.c.end, sum = STATES || !final || (at.c.last && j.fin);
+        const int pieces = j.pieces;
+        LaSpot to = at;
+        bool next = true;
+        float next_l2 = l2;
+        if (!final) {
+            to.u = at.u + kC;
+        } else {
+            next = next_walk(to);
+            if (next) {
+                next_l2 = la_log2_decay(p, to.c.d, to.c.h);
+                set_powers(table ^ 1, next_l2);
+            }
+        }
+        if (next) find_rows(to);
+        cp_async_wait();
+        tc::fence_async_smem();
+        tc::tc_fence_before_sync();
+        __syncthreads();
+        if (*(volatile int*)stop) break;
+        if (!STATES && tid == 0) {
+            tc::tc_fence_after_sync();
+            for (int k = 0; k < A / 16; ++k) {
+                const uint32_t k0 = (k / 4) * kPanel + (k % 4) * 32;
+                tc::mma_bf16_ss(tmem + L::S, tc::sdesc_sw128(base + L::Q + k0), tc::sdesc_sw128(base + L::K + k0),
+                                tc::idesc_bf16_f32(128, 128), k > 0);
+            }
+            if (carry)
+                for (int k = 0; k < 2 * (A / 16); ++k) {
+                    const int s = k % (A / 16);
+                    tc::mma_bf16_ss(tmem + L::O, tc::sdesc_sw128(base + L::Q + (s / 4) * kPanel + (s % 4) * 32),
+                                    sdesc_mn(base + (k < A / 16 ? L::Y1 : L::Y2) + s * 2048, A * 128), tc::idesc_bf16_f32(128, B) | kBmn,
+                                    k > 0);
+                }
+            tc::mma_commit(bar + DONE_S);
+        }
+        __syncwarp();
+        // the weighted values in pieces
+        constexpr int CH = B / 8, EACH = L::T / CH, IT = kC / EACH;
+        uint4 third[IT];
+        if (sum) {
+            const int behind = decay_of(at);
+#pragma unroll
+            for (int i = 0; i < IT; ++i) {
+                const int s = i * EACH + tid / CH;
+                const uint32_t v0 = tile_at(s, tid % CH, kPanel);
+                uint4 v = *(const uint4*)(sm + L::V + v0);
+                if (s >= n) v = make_uint4(0, 0, 0, 0);
+                const float w = j.sK * exp2f(max(behind - s, 0) * l2);
+                float f[8] = {low(v.x) * w, high(v.x) * w, low(v.y) * w, high(v.y) * w, low(v.z) * w, high(v.z) * w, low(v.w) * w, high(v.w) * w};
+                uint4 a, b;
+                a.x = cut(f[0], f[1]); a.y = cut(f[2], f[3]); a.z = cut(f[4], f[5]); a.w = cut(f[6], f[7]);
+                *(uint4*)(sm + L::V1 + v0) = a;
+                b.x = cut(f[0], f[1]); b.y = cut(f[2], f[3]); b.z = cut(f[4], f[5]); b.w = cut(f[6], f[7]);
+                *(uint4*)(sm + L::V2 + v0) = b;
+                third[i] = make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
+                if (!L::in_q && pieces > 2) *(uint4*)(sm + L::V3 + v0) = third[i];
+            }
+        }
+        float o[L::OC];
+        constexpr int CPR = L::OC / 8, RPT = 32 / CPR;
+        int rows_out[CPR];
+        if (!STATES) {
+#pragma unroll
+            for (int k = 0; k < CPR; ++k) rows_out[k] = row_of(at, j.back, quad * 32 + k * RPT + lane / CPR, n);
+            waited(DONE_S, phase);
+            tc::tc_fence_after_sync();
+            if (!L::in_q && next) load_q(to);
+        }
+        if (L::in_q && sum && pieces > 2) {
+#pragma unroll
+            for (int i = 0; i < IT; ++i) *(uint4*)(sm + L::V3 + tile_at(i * EACH + tid / CH, tid % CH, kPanel)) = third[i];
+        }
+        if (!STATES) {
+            const float* const power = powers + table * 64;
+            // S to P, 32 columns at a time; each piece of P lies where its columns of S lay
+#pragma unroll
+            for (int b = part; b < 4; b += L::PARTS) {
+                uint32_t w[16];
+                if (b > quad) {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) w[e] = 0;
+                } else {
+                    float s[32];
+                    load_columns(L::S + 32 * b, s);
+                    if (b == quad) {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            const float s0 = lane >= 2 * e ? s[2 * e] * power[max(lane - 2 * e, 0)] : 0.f;
+                            const float s1 = lane >= 2 * e + 1 ? s[2 * e + 1] * power[max(lane - 2 * e - 1, 0)] : 0.f;
+                            w[e] = pack2(s0, s1);
+                        }
+                    } else {
+                        // lambda^(i-j) in two factors that are at most 1: from the block's last column on, and up to it
+                        const float f = exp2f((row - 32 * b - 31) * l2);
+#pragma unroll
+                        for (int e = 0; e < 16; e += 2) {
+                            const float4 g = *(const float4*)(power + 32 + 2 * e);
+                            w[e] = pack2(s[2 * e] * (f * g.x), s[2 * e + 1] * (f * g.y));
+                            w[e + 1] = pack2(s[2 * e + 2] * (f * g.z), s[2 * e + 3] * (f * g.w));
+                        }
+                    }
+                }
+                tc::tmem_st_32x32b_x16(mine + L::S + 32 * b, w);
+            }
+            if (carry) {
+                const float f = j.sI * exp2f(row * l2);
+                load_columns(L::O + o0, o);
+#pragma unroll
+                for (int k = 0; k < L::OC; ++k) o[k] *= f;
+            } else {
+#pragma unroll
+                for (int k = 0; k < L::OC; ++k) o[k] = 0.f;
+            }
+            tc::tmem_wait_st();
+        }
+        tc::fence_async_smem();
+        tc::tc_fence_before_sync();
+        __syncthreads();
+        if (*(volatile int*)stop) break;
+        if (tid == 0) {
+            tc::tc_fence_after_sync();
+            if (!STATES) {
+                for (int k = 0; k < steps; ++k)
+                    tc::mma_bf16_ts(tmem + L::O, tmem + L::S + 32 * (k / 2) + 8 * (k % 2), sdesc_mn(base + L::V + k * 2048, kPanel),
+                                    tc::idesc_bf16_f32(128, B) | kBmn, k > 0);
+                tc::mma_commit(bar + DONE_O);
+            }
+            if (sum)
+                for (int e = 0; e < pieces; ++e)
+                    for (int k = 0; k < steps; ++k)
+                        // keys of 64 columns: the same panel again for the second 64 rows of the product
+                        tc::mma_bf16_ss(tmem + L::Y, sdesc_mn(base + L::K + k * 2048, A == 128 ? kPanel : 0),
+                                        sdesc_mn(base + (e == 0 ? L::V1 : e == 1 ? L::V2 : L::V3) + k * 2048, kPanel),
+                                        tc::idesc_bf16_f32(128, B) | kAmn | kBmn, carry || e > 0 || k > 0);
+            tc::mma_commit(bar + DONE_Y);
+        }
+        __syncwarp();
+        if (!STATES) {
+            // rows out: 16 bytes a thread and CPR threads a row, by way of the warp's part of the pieces of Y, which S and O have read
+            unsigned char* const stage = sm + L::Y1 + warp * 64 * L::OC;
+            __nv_bfloat16* const out = (__nv_bfloat16*)j.out.p + at.c.d * j.out.dir + at.c.h * j.out.head + at.c.slot * j.out.row + o0;
+            waited(DONE_O, phase);
+            tc::tc_fence_after_sync();
+            float v[L::OC];
+            load_columns(L::O + o0, v);
+#pragma unroll
+            for (int k = 0; k < L::OC; ++k) v[k] = fmaf(j.sP, v[k], o[k]);
+#pragma unroll
+            for (int k = 0; k < CPR; ++k)
+                *(uint4*)(stage + lane * 2 * L::OC + ((k ^ ((lane >> 1) & (CPR - 1))) << 4)) =
+                    make_uint4(pack2(v[8 * k], v[8 * k + 1]), pack2(v[8 * k + 2], v[8 * k + 3]), pack2(v[8 * k + 4], v[8 * k + 5]),
+                               pack2(v[8 * k + 6], v[8 * k + 7]));
+            __syncwarp();
+#pragma unroll
+            for (int k = 0; k < CPR; ++k) {
+                const int r = k * RPT + lane / CPR, ch = lane % CPR;
+                const uint4 w = *(const uint4*)(stage + r * 2 * L::OC + ((ch ^ ((r >> 1) & (CPR - 1))) << 4));
+                if (quad * 32 + r < n && o0 + ch * 8 < j.b) *(uint4*)(out + rows_out[k] * j.out.row + ch * 8) = w;
+            }
+        }
+        waited(DONE_Y, phase);
+        tc::tc_fence_after_sync();
+        if (next) {
+            if (L::in_q) load_q(to);
+            load_kv(to);
+        }
+        if (!STATES) __syncthreads();                   // the rows have left the pieces' place
+        if (sum) {
+            float y[L::YC];
+            load_columns(L::Y + y0, y);
+            if (!final) {
+                put_state(y, exp2f(decay_of(to) * l2));
+                carry = true;
+            } else {
+                float* const fin = STATES ? la_start(p, j, at.c) : j.fin + la_state(p, j, at.c);
+                if (((uintptr_t)fin & 15) == 0) {       // widths are multiples of 8
+#pragma unroll
+                    for (int k = 0; k < L::YC; k += 4)
+                        if (x < j.a && y0 + k < j.b) *(float4*)(fin + x * j.b + y0 + k) = make_float4(y[k], y[k + 1], y[k + 2], y[k + 3]);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < L::YC; ++k)
+                        if (x < j.a && y0 + k < j.b) fin[x * j.b + y0 + k] = y[k];
+                }
+            }
+        }
+        if (final) {
+            carry = next ? first_state(to, next_l2) : false;
+            table ^= 1;
+            l2 = next_l2;
+        }
+        at = to;
+        more = next;
+    }
+    cp_async_wait();
+    tc::tc_fence_before_sync();
+    __syncthreads();
+    if (warp == 0) {
+        tc::tc_fence_after_sync();
+        tc::tmem_dealloc(tmem, L::COLUMNS);
+    }
+}
+
+template <int A, int B, bool STATES>
+lstm_status launch(const LaArgs& a, cudaStream_t cs)
+{
+    typedef Layout<A, B> L;
+    auto kernel = la_tensor_kernel<A, B, STATES>;
+    LSTM_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::BYTES));
+    const int total = a.count * a.ndir * a.heads * a.jobs, ctas = a.sms * L::CTAS;
+    kernel<<<total < ctas ? total : ctas, L::T, L::BYTES, cs>>>(a, total);
+    return cudaGetLastError() == cudaSuccess ? LSTM_OK : LSTM_ERR_CUDA;
+}
+
+template <int A, int B>
+lstm_status launch_padded(const LaArgs& a, bool states, cudaStream_t cs)
+{
+    return states ? launch<A, B, true>(a, cs) : launch<A, B, false>(a, cs);
+}
+
+}  // namespace
+
+// One translation unit each (la_tensor_*.cu).
+lstm_status launch_la_64_64(const LaArgs& a, bool states, cudaStream_t cs);
+lstm_status launch_la_64_128(const LaArgs& a, bool states, cudaStream_t cs);
+lstm_status launch_la_128_64(const LaArgs& a, bool states, cudaStream_t cs);
+lstm_status launch_la_128_128(const LaArgs& a, bool states, cudaStream_t cs);
+
+}  // namespace lstm
