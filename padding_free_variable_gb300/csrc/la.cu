@@ -126,16 +126,19 @@ __global__ void __launch_bounds__(256) la_starts_kernel(const LaArgs p)
     }
     float* at = j.starts + ((int64_t)e.w * dhs + dh) * size + i;
     const int64_t step = (int64_t)dhs * size;
-    for (int n = 0; n < pieces; n += 8) {
-        float add[8];
+    // 16 pieces at a time, the next 16 read before these are written
+    float add[16], next[16];
 #pragma unroll
-        for (int o = 0; o < 8; ++o) add[o] = n + o < pieces - 1 ? at[(n + o) * step] : 0.f;
+    for (int o = 0; o < 16; ++o) add[o] = o < pieces - 1 ? at[o * step] : 0.f;
+    for (int n = 0; n < pieces; n += 16) {
 #pragma unroll
-        for (int o = 0; o < 8; ++o)
-            if (n + o < pieces) {
-                at[(n + o) * step] = y;
-                y = fmaf(keep, y, add[o]);
-            }
+        for (int o = 0; o < 16; ++o) next[o] = n + 16 + o < pieces - 1 ? at[(n + 16 + o) * step] : 0.f;
+#pragma unroll
+        for (int o = 0; o < 16; ++o) {
+            if (n + o < pieces) at[(n + o) * step] = y;
+            y = fmaf(keep, y, add[o]);
+            add[o] = next[o];
+        }
     }
 }
 
@@ -221,12 +224,13 @@ LaRows dense_rows(const void* p, const lstm_la_shape& s)
 // The level of the plan's pieces that `jobs` walks of every sequence run over (the last one: uncut).
 int cut_level(const ScanPlan& sp, const lstm_la_shape& s, int jobs)
 {
-    const int64_t slots = (int64_t)sp.p.num_sms, each = (int64_t)s.num_directions * s.num_heads * jobs;
+    const bool bf16 = s.dtype == LSTM_BF16, wide = s.key_size > 64 || s.value_size > 64;
+    const int64_t slots = (int64_t)sp.p.num_sms * (bf16 ? wide ? 1 : 2 : wide ? 1 : 3), each = (int64_t)s.num_directions * s.num_heads * jobs;
     const int64_t share = (sp.p.padded ? sp.p.frames : sp.p.rows) * each / slots;
     const int whole = sp.scan.levels - 1;
-    if (sp.p.T <= share * 3 / 2 + 512) return whole;
+    if (sp.p.T <= share * 3 / 2 + kScanPiece) return whole;
     for (int l = 0; l < whole; ++l)
-        if (((int64_t)kScanPiece << l) * 4 >= share) return l;
+        if (((int64_t)kScanPiece << l) * 8 >= share) return l;
     return whole;
 }
 

@@ -20,35 +20,45 @@ __host__ __device__ constexpr int ld_of(int w) { return ((w + 3) / 4 | 1) * 4; }
 size_t shared_bytes(int a, int b, bool states)
 {
     const int a4 = (a + 3) / 4 * 4;
-    return sizeof(float) * ((size_t)kSteps * (2 * ld_of(a) + ld_of(b)) + (states ? 0 : kSteps * kLdP) + (size_t)a4 * ld_of(b) + kSteps + 4);
+    return sizeof(float) * ((size_t)kSteps * (2 * ld_of(a) + ld_of(b)) + (states ? 0 : kSteps * kLdP) + (size_t)a4 * ld_of(b) + 3 * kSteps + 4);
 }
 
-// `n` rows of `w` values into shared memory, zeros behind them and behind the width's last value.
+// `n` rows of `w` values into shared memory, zeros behind them and behind the width's last value.  rows: of the chunk's
+// steps; log: of the threads of a row.
 template <typename T, int V>
-__device__ __forceinline__ void load_rows(float* dst, int ld, const LaRows& r, const LaArgs& p, const LaPart& c, int w, int u, int n, bool rev)
+__device__ __forceinline__ void load_rows(float* dst, int ld, int log, const LaRows& r, const LaPart& c, const int* rows, int w, int n)
 {
-    const T* base = (const T*)r.p + c.d * r.dir + c.h * r.head;
-    const int groups = (w + 3) / 4;
-    for (int i = threadIdx.x; i < kSteps * groups; i += kThreads) {
-        const int s = i / groups, g = (i - s * groups) * 4;
-        float4 q = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (s < n) {
-            const int t = rev ? c.len - 1 - (u + s) : u + s;
-            const T* at = base + (int64_t)(__ldg(p.off + t) + c.slot) * r.row + g;
-            if constexpr (V == 4 && sizeof(T) == 4) {
-                q = __ldg((const float4*)at);
-            } else if constexpr (V == 4) {
+    const T* const base = (const T*)r.p + c.d * r.dir + c.h * r.head;
+    const int g = (threadIdx.x & ((1 << log) - 1)) * 4;
+    if (g >= w) return;
+#pragma unroll 4
+    for (int s = threadIdx.x >> log; s < kSteps; s += kThreads >> log) {
+        const bool on = s < n;
+        const T* const at = on ? base + rows[s] * r.row + g : base;
+        float* const to = dst + s * ld + g;
+        if constexpr (sizeof(T) == 4) {
+            // asynchronous copies: the rows of all three operands are on their way together
+#pragma unroll
+            for (int e = 0; e < 4; e += V) {
+                const int bytes = on && g + e < w ? 4 * V : 0;
+                const uint32_t d = (uint32_t)__cvta_generic_to_shared(to + e);
+                if constexpr (V == 4) asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(at), "r"(bytes) : "memory");
+                else asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(d), "l"(bytes ? at + e : at), "r"(bytes) : "memory");
+            }
+        } else {
+            float4 q = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (on && V == 4) {
                 const uint2 x = __ldg((const uint2*)at);
                 q = make_float4(__uint_as_float(x.x << 16), __uint_as_float(x.x & 0xffff0000u), __uint_as_float(x.y << 16),
                                 __uint_as_float(x.y & 0xffff0000u));
-            } else {
+            } else if (on) {
                 q.x = to_f32(at[0]);
                 if (g + 1 < w) q.y = to_f32(at[1]);
                 if (g + 2 < w) q.z = to_f32(at[2]);
                 if (g + 3 < w) q.w = to_f32(at[3]);
             }
+            *(float4*)to = q;
         }
-        *(float4*)(dst + s * ld + g) = q;
     }
 }
 
@@ -69,11 +79,12 @@ __global__ void __launch_bounds__(kThreads) la_general_kernel(const LaArgs p)
     const LaPart c = la_part(p, blockIdx.x);
     const LaJob& j = p.job[c.job];
     if (STATES && c.last) return;
-    const int tid = threadIdx.x, a = j.a, b = j.b, a4 = (a + 3) / 4, b4 = (b + 3) / 4, lda = ld_of(a), ldb = ld_of(b);
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, a = j.a, b = j.b, a4 = (a + 3) / 4, b4 = (b + 3) / 4, lda = ld_of(a), ldb = ld_of(b);
     float* const Q = sm;
     float* const K = Q + kSteps * lda;
     float* const W = K + kSteps * lda;
-    float* const Vs = W + kSteps + 4;
+    int* rows = (int*)(W + kSteps + 4);         // [2][kSteps]: of this chunk's steps and the next one's
+    float* const Vs = W + 3 * kSteps + 4;
     float* const Y = Vs + kSteps * ldb;
     float* const P = Y + a4 * 4 * ldb;
     const bool rev = (c.d == 1) != (j.back != 0);
@@ -85,28 +96,50 @@ __global__ void __launch_bounds__(kThreads) la_general_kernel(const LaArgs p)
         if (c.len == 0) return la_pass(j, state);
     }
     if (tid <= kSteps) W[tid] = exp2f(tid * l2);
+    // the row of a chunk's step (the last one's where there is none)
+    auto row_of = [&](int u) {
+        const int s = min(u + tid, c.end - 1), t = rev ? c.len - 1 - s : s;
+        return __ldg(p.off + t) + c.slot;
+    };
+    int ahead = 0, loga = 0, logb = 0;
+    while (1 << loga < a4) ++loga;
+    while (1 << logb < b4) ++logb;
+    if (tid < kSteps) rows[tid] = row_of(c.begin);
     __syncthreads();
     {
         const float first = j.early ? W[1] : 1.f;
         const float* from = STATES ? nullptr : j.starts ? la_start(p, j, c) : j.init ? j.init + state : nullptr;
-        for (int i = tid; i < a4 * 4 * ldb; i += kThreads) {
-            const int x = i / ldb, y = i - x * ldb;
-            float v = 0.f;
-            if (from && x < a && y < b) v = j.starts ? from[x * b + y] : first * from[j.flip ? y * a + x : x * b + y];
-            Y[i] = v;
-        }
+        for (int x = warp; x < 4 * a4; x += kThreads / 32)
+            for (int y = lane; y < 4 * b4; y += 32) {
+                float v = 0.f;
+                if (from && x < a && y < b) v = j.starts ? from[x * b + y] : first * from[j.flip ? y * a + x : x * b + y];
+                Y[x * ldb + y] = v;
+            }
+    }
+    // a warp's places of Y, 4 x 4 values each: nx of a column, ng of a row, `share` threads each
+    int share = 1, nx = 8, ng = 4;
+    while (share < 8) {
+        const int x = nx > ng ? nx / 2 : nx, y = nx > ng ? ng : ng / 2;
+        if ((a4 + x - 1) / x * ((b4 + y - 1) / y) > kThreads / 32) break;
+        share *= 2;
+        nx = x;
+        ng = y;
     }
     for (int u = c.begin; u < c.end; u += kSteps) {
         const int n = min(kSteps, c.end - u);
         const bool final = c.last && u + kSteps >= c.end;
-        if (!STATES) load_rows<T, V>(Q, lda, j.q, p, c, a, u, n, rev);
-        load_rows<T, V>(K, lda, j.k, p, c, a, u, n, rev);
-        load_rows<T, V>(Vs, ldb, j.v, p, c, b, u, n, rev);
+        load_rows<T, V>(K, lda, loga, j.k, c, rows, a, n);
+        if (!STATES) load_rows<T, V>(Q, lda, loga, j.q, c, rows, a, n);
+        load_rows<T, V>(Vs, ldb, logb, j.v, c, rows, b, n);
+        if (tid < kSteps && u + kSteps < c.end) ahead = row_of(u + kSteps);
+        asm volatile("cp.async.wait_all;" ::: "memory");
         __syncthreads();
         if (!STATES) {
-            // steps against steps: rows ti + 16 m, columns tj + 16 n of a thread
-            const int ti = tid / 16, tj = tid % 16;
+            // steps against steps: rows ti + 16 m, columns tj + 16 n of a thread; a warp's lanes 8 x 4, so that either side's
+            // rows come in one piece of 128 bytes or less
+            const int ti = warp % 2 * 8 + lane / 4, tj = warp / 2 * 4 + lane % 4;
             float s[4][4] = {};
+#pragma unroll 2
             for (int x = 0; x < a4; ++x) {
                 float4 q[4], k[4];
 #pragma unroll
@@ -117,21 +150,22 @@ __global__ void __launch_bounds__(kThreads) la_general_kernel(const LaArgs p)
 #pragma unroll
                 for (int m = 0; m < 4; ++m)
 #pragma unroll
-                    for (int o = 0; o < 4; ++o)
+                    for (int o = 0; o <= m; ++o)        // what is later than all of its rows stays 0
                         s[m][o] = fmaf(q[m].w, k[o].w, fmaf(q[m].z, k[o].z, fmaf(q[m].y, k[o].y, fmaf(q[m].x, k[o].x, s[m][o]))));
             }
 #pragma unroll
             for (int m = 0; m < 4; ++m)
 #pragma unroll
-                for (int o = 0; o < 4; ++o) {
+                for (int o = 0; o <= m; ++o) {
                     const int near = ti + 16 * m - (tj + 16 * o);
                     P[(ti + 16 * m) * kLdP + tj + 16 * o] = near >= 0 ? s[m][o] * (j.sP * W[near]) : 0.f;
                 }
             __syncthreads();
             T* out = (T*)j.out.p + c.d * j.out.dir + c.h * j.out.head;
-            for (int i = tid; i < 16 * b4; i += kThreads) {
-                const int r = i / b4, g = (i - r * b4) * 4;
+            const int r = ti;
+            for (int g = 4 * tj; g < b; g += 64) {
                 float4 o[4] = {};
+#pragma unroll 2
                 for (int x = 0; x < a4; ++x) {
                     float4 y[4];
 #pragma unroll
@@ -147,22 +181,24 @@ __global__ void __launch_bounds__(kThreads) la_general_kernel(const LaArgs p)
                     const float f = j.sI * W[r + 16 * m];
                     o[m] = make_float4(o[m].x * f, o[m].y * f, o[m].z * f, o[m].w * f);
                 }
-                for (int x = 0; x < kSteps / 4; ++x) {
-                    float4 v[4];
 #pragma unroll
-                    for (int m = 0; m < 4; ++m) v[m] = *(const float4*)(Vs + (4 * x + m) * ldb + g);
+                for (int first = 0; first < 4; ++first)     // rows of block m weigh the steps of blocks up to m
+#pragma unroll 2
+                    for (int x = 4 * first; x < 4 * first + 4; ++x) {
+                        float4 v[4];
 #pragma unroll
-                    for (int m = 0; m < 4; ++m) {
-                        const float4 q = *(const float4*)(P + (r + 16 * m) * kLdP + 4 * x);
-                        fma4(o[m], q.x, v[0]); fma4(o[m], q.y, v[1]); fma4(o[m], q.z, v[2]); fma4(o[m], q.w, v[3]);
+                        for (int m = 0; m < 4; ++m) v[m] = *(const float4*)(Vs + (4 * x + m) * ldb + g);
+#pragma unroll
+                        for (int m = first; m < 4; ++m) {
+                            const float4 q = *(const float4*)(P + (r + 16 * m) * kLdP + 4 * x);
+                            fma4(o[m], q.x, v[0]); fma4(o[m], q.y, v[1]); fma4(o[m], q.z, v[2]); fma4(o[m], q.w, v[3]);
+                        }
                     }
-                }
 #pragma unroll
                 for (int m = 0; m < 4; ++m) {
                     const int s1 = r + 16 * m;
                     if (s1 >= n) continue;
-                    const int t = rev ? c.len - 1 - (u + s1) : u + s1;
-                    T* at = out + (int64_t)(__ldg(p.off + t) + c.slot) * j.out.row + g;
+                    T* at = out + rows[s1] * j.out.row + g;
                     if constexpr (V == 4 && sizeof(T) == 4) {
                         *(float4*)at = o[m];
                     } else {
@@ -175,6 +211,8 @@ __global__ void __launch_bounds__(kThreads) la_general_kernel(const LaArgs p)
             }
             if (final && !j.fin) return;
         }
+        rows = (int*)(W + kSteps + 4) + ((u - c.begin) / kSteps % 2 ? 0 : kSteps);
+        if (tid < kSteps) rows[tid] = ahead;
         // the state: keys weighted by what is left of the chunk behind them
         const int less = final ? j.early : 0;
         for (int i = tid; i < n * a4; i += kThreads) {
@@ -186,20 +224,34 @@ __global__ void __launch_bounds__(kThreads) la_general_kernel(const LaArgs p)
         }
         __syncthreads();
         const float keep = W[n - less];
-        for (int i = tid; i < a4 * b4; i += kThreads) {
-            const int x = i / b4, g = (i - x * b4) * 4;
-            float4 y[4];
-#pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                y[m] = *(const float4*)(Y + (4 * x + m) * ldb + g);
-                y[m] = make_float4(y[m].x * keep, y[m].y * keep, y[m].z * keep, y[m].w * keep);
-            }
-            for (int s = 0; s < n; ++s) {
+        // few places: 2 to 8 threads next to each other share one, each a part of the steps
+        const int each = (n + share - 1) / share, s0 = min(n, lane % share * each), s1 = min(n, s0 + each);
+        const int wide = (b4 + ng - 1) / ng, blocks = (a4 + nx - 1) / nx * wide, at = lane / share;
+        for (int i = warp; i < blocks; i += kThreads / 32) {
+            const int x = i / wide * nx + at / ng, g = (i % wide * ng + at % ng) * 4;
+            if (x >= a4 || g >= b) continue;
+            float4 y[4] = {};
+#pragma unroll 4
+            for (int s = s0; s < s1; ++s) {
                 const float4 k = *(const float4*)(K + s * lda + 4 * x), v = *(const float4*)(Vs + s * ldb + g);
                 fma4(y[0], k.x, v); fma4(y[1], k.y, v); fma4(y[2], k.z, v); fma4(y[3], k.w, v);
             }
+            for (int m = share / 2; m > 0; m /= 2) {
+                const unsigned group = ((1u << share) - 1) << (lane & ~(share - 1));
 #pragma unroll
-            for (int m = 0; m < 4; ++m) *(float4*)(Y + (4 * x + m) * ldb + g) = y[m];
+                for (int e = 0; e < 4; ++e) {
+                    y[e].x += __shfl_xor_sync(group, y[e].x, m); y[e].y += __shfl_xor_sync(group, y[e].y, m);
+                    y[e].z += __shfl_xor_sync(group, y[e].z, m); y[e].w += __shfl_xor_sync(group, y[e].w, m);
+                }
+            }
+            if (lane % share == 0) {
+#pragma unroll
+                for (int m = 0; m < 4; ++m) {
+                    float4* const at = (float4*)(Y + (4 * x + m) * ldb + g);
+                    const float4 q = *at;
+                    *at = make_float4(fmaf(q.x, keep, y[m].x), fmaf(q.y, keep, y[m].y), fmaf(q.z, keep, y[m].z), fmaf(q.w, keep, y[m].w));
+                }
+            }
         }
         __syncthreads();
     }

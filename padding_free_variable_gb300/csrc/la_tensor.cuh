@@ -5,10 +5,11 @@
 //     P = S lambda^(i-j), i >= j, rounded to bf16, back into tensor memory as the next product's left operand
 //     O' = P V                   128 x B       out = sP O' + sI lambda^i O
 //     Y = lambda^n Y + K^T (sK lambda^(n-j) V) A x B            (the weighted values in bf16 pieces)
+// Tensor cores cut off what does not fit behind a sum, so a chunk's products are added up from zero, the smallest pieces
+// first, and Y, in registers, takes their sum with a rounding: a long memory does not shrink chunk by chunk.
 // The weighted values enter in three pieces (24 bits) where Y may be asked for in the end, in two (16 bits) where it
 // only serves outputs that are rounded to bf16.  Rows come by cp.async into the 128-byte swizzled layout, one image of 64 columns a panel: read along a row it is the
-// K-major operand of S, read along a column the MN-major operand of the other products, so nothing is transposed.  Y stays in
-// tensor memory; once a chunk it is read, cut into pieces for the next chunk and decayed.
+// K-major operand of S, read along a column the MN-major operand of the other products, so nothing is transposed.
 //
 // CTAs stay on the GPU and take every so-many-th walk; the next chunk's rows, of the same walk or the next, are on their way
 // as soon as the products that read the last ones are done.
@@ -96,13 +97,13 @@ __global__ void __launch_bounds__(Layout<A, B>::T, Layout<A, B>::CTAS) la_tensor
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, quad = warp % 4, part = warp / 4;
     const uint32_t base = tc::smem_u32(sm);
     float* const powers = (float*)(sm + L::POWERS);
-    // S and O, O', Y are done
+    // S and O, O', the sum for Y are done; the weighted values are there
     uint64_t* const bar = (uint64_t*)(sm + L::BARS);
-    enum { DONE_S = 0, DONE_O, DONE_Y, BARRIERS };
+    enum { DONE_S = 0, DONE_O, DONE_Y, PIECES, BARRIERS };
     uint32_t* const slot_of_tmem = (uint32_t*)(bar + BARRIERS);
     int* const stop = (int*)(slot_of_tmem + 1);
     if (tid == 0) {
-        for (int i = 0; i < BARRIERS; ++i) tc::mbar_init(bar + i, 1);
+        for (int i = 0; i < BARRIERS; ++i) tc::mbar_init(bar + i, i == PIECES ? L::T / 32 : 1);
         *stop = 0;
         tc::fence_mbar_init();
     }
@@ -192,27 +193,19 @@ __global__ void __launch_bounds__(Layout<A, B>::T, Layout<A, B>::CTAS) la_tensor
         }
         __syncwarp();
     };
-    // Y in front of a chunk: its pieces for the outputs, decayed by the chunk's steps for the sum of its products.
-    auto put_state = [&](float (&y)[L::YC], float keep) {
+    float y[L::YC];                                     // Y, this thread's columns of row x
+    auto put_pieces = [&] {
 #pragma unroll
-        for (int k = 0; k < L::YC; k += 16) {
-            uint32_t r[16];
+        for (int k = 0; k < L::YC; k += 8) {
+            float f[8];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(y[k + e] * keep);
-            tc::tmem_st_32x32b_x16(mine + L::Y + y0 + k, r);
+            for (int e = 0; e < 8; ++e) f[e] = y[k + e];
+            const uint32_t to = tile_at(x, (y0 + k) / 8, A * 128);
+            uint4 w;
+            w.x = cut(f[0], f[1]); w.y = cut(f[2], f[3]); w.z = cut(f[4], f[5]); w.w = cut(f[6], f[7]);
+            *(uint4*)(sm + L::Y1 + to) = w;
+            *(uint4*)(sm + L::Y2 + to) = make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
         }
-        if (!STATES) {
-#pragma unroll
-            for (int k = 0; k < L::YC; k += 8) {
-                uint4 hi, lo;
-                hi.x = cut(y[k], y[k + 1]); hi.y = cut(y[k + 2], y[k + 3]); hi.z = cut(y[k + 4], y[k + 5]); hi.w = cut(y[k + 6], y[k + 7]);
-                lo = make_uint4(pack2(y[k], y[k + 1]), pack2(y[k + 2], y[k + 3]), pack2(y[k + 4], y[k + 5]), pack2(y[k + 6], y[k + 7]));
-                const uint32_t to = tile_at(x, (y0 + k) / 8, A * 128);
-                *(uint4*)(sm + L::Y1 + to) = hi;
-                *(uint4*)(sm + L::Y2 + to) = lo;
-            }
-        }
-        tc::tmem_wait_st();
     };
     auto load_columns = [&](uint32_t column, auto& v) {
         constexpr int N = sizeof(v) / sizeof(v[0]);
@@ -227,10 +220,13 @@ __global__ void __launch_bounds__(Layout<A, B>::T, Layout<A, B>::CTAS) la_tensor
     auto first_state = [&](const LaSpot& s, float l2) {
         const LaJob& j = p.job[s.c.job];
         const float* from = STATES ? nullptr : j.starts ? la_start(p, j, s.c) : j.init ? j.init + la_state(p, j, s.c) : nullptr;
-        if (!from) return false;
+        if (!from) {
+#pragma unroll
+            for (int k = 0; k < L::YC; ++k) y[k] = 0.f;
+            return false;
+        }
         const bool flip = j.flip && !j.starts;
         const float first = j.early && !j.starts ? exp2f(l2) : 1.f;
-        float y[L::YC];
         if (!flip && ((uintptr_t)from & 15) == 0) {
 #pragma unroll
             for (int k = 0; k < L::YC; k += 4) {
@@ -244,13 +240,13 @@ __global__ void __launch_bounds__(Layout<A, B>::T, Layout<A, B>::CTAS) la_tensor
                 y[k] = x < j.a && col < j.b ? first * from[flip ? col * j.a + x : x * j.b + col] : 0.f;
             }
         }
-        put_state(y, exp2f(decay_of(s) * l2));
+        if (!STATES) put_pieces();
         return true;
     };
 
     float l2 = 0.f;
     bool carry = false;                                 // is there anything in Y?
-    int table = 0;
+    int table = 0, sums = 0;                            // the walk's powers; sums for Y so far
     if (more) {
         find_rows(at);
         load_q(at);
@@ -301,7 +297,7 @@ __global__ void __launch_bounds__(Layout<A, B>::T, Layout<A, B>::CTAS) la_tensor
         __syncwarp();
         // the weighted values in pieces
         constexpr int CH = B / 8, EACH = L::T / CH, IT = kC / EACH;
-        uint4 third[IT];
+        uint4 third[L::in_q ? IT : 1];
         if (sum) {
             const int behind = decay_of(at);
 #pragma unroll
@@ -317,23 +313,52 @@ __global__ void __launch_bounds__(Layout<A, B>::T, Layout<A, B>::CTAS) la_tensor
                 *(uint4*)(sm + L::V1 + v0) = a;
                 b.x = cut(f[0], f[1]); b.y = cut(f[2], f[3]); b.z = cut(f[4], f[5]); b.w = cut(f[6], f[7]);
                 *(uint4*)(sm + L::V2 + v0) = b;
-                third[i] = make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
-                if (!L::in_q && pieces > 2) *(uint4*)(sm + L::V3 + v0) = third[i];
+                if (pieces > 2) {
+                    const uint4 last = make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
+                    if (L::in_q) third[L::in_q ? i : 0] = last;
+                    else *(uint4*)(sm + L::V3 + v0) = last;
+                }
             }
         }
         float o[L::OC];
         constexpr int CPR = L::OC / 8, RPT = 32 / CPR;
         int rows_out[CPR];
-        if (!STATES) {
-#pragma unroll
-            for (int k = 0; k < CPR; ++k) rows_out[k] = row_of(at, j.back, quad * 32 + k * RPT + lane / CPR, n);
+        if (!STATES && L::in_q) {
             waited(DONE_S, phase);
             tc::tc_fence_after_sync();
-            if (!L::in_q && next) load_q(to);
         }
         if (L::in_q && sum && pieces > 2) {
 #pragma unroll
-            for (int i = 0; i < IT; ++i) *(uint4*)(sm + L::V3 + tile_at(i * EACH + tid / CH, tid % CH, kPanel)) = third[i];
+            for (int i = 0; i < IT; ++i) *(uint4*)(sm + L::V3 + tile_at(i * EACH + tid / CH, tid % CH, kPanel)) = third[L::in_q ? i : 0];
+        }
+        if (sum) {
+            // what a chunk adds to Y, while the rest goes on
+            tc::fence_async_smem();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(bar + PIECES);
+            if (warp == 0) {
+                waited(PIECES, sums & 1);
+                if (lane == 0) {
+                    tc::tc_fence_after_sync();
+                    for (int e = pieces - 1; e >= 0; --e)
+                        for (int k = 0; k < steps; ++k)
+                            // keys of 64 columns: the same panel again for the second 64 rows of the product
+                            tc::mma_bf16_ss(tmem + L::Y, sdesc_mn(base + L::K + k * 2048, A == 128 ? kPanel : 0),
+                                            sdesc_mn(base + (e == 0 ? L::V1 : e == 1 ? L::V2 : L::V3) + k * 2048, kPanel),
+                                            tc::idesc_bf16_f32(128, B) | kAmn | kBmn, e < pieces - 1 || k > 0);
+                    tc::mma_commit(bar + DONE_Y);
+                }
+                __syncwarp();
+            }
+        }
+        if (!STATES) {
+#pragma unroll
+            for (int k = 0; k < CPR; ++k) rows_out[k] = row_of(at, j.back, quad * 32 + k * RPT + lane / CPR, n);
+            if (!L::in_q) {
+                waited(DONE_S, phase);
+                tc::tc_fence_after_sync();
+                if (next) load_q(to);
+            }
         }
         if (!STATES) {
             const float* const power = powers + table * 64;
@@ -378,26 +403,17 @@ __global__ void __launch_bounds__(Layout<A, B>::T, Layout<A, B>::CTAS) la_tensor
             }
             tc::tmem_wait_st();
         }
-        tc::fence_async_smem();
-        tc::tc_fence_before_sync();
-        __syncthreads();
-        if (*(volatile int*)stop) break;
-        if (tid == 0) {
-            tc::tc_fence_after_sync();
-            if (!STATES) {
+        if (!STATES) {
+            tc::tc_fence_before_sync();
+            __syncthreads();
+            if (*(volatile int*)stop) break;
+            if (tid == 0) {
+                tc::tc_fence_after_sync();
                 for (int k = 0; k < steps; ++k)
                     tc::mma_bf16_ts(tmem + L::O, tmem + L::S + 32 * (k / 2) + 8 * (k % 2), sdesc_mn(base + L::V + k * 2048, kPanel),
                                     tc::idesc_bf16_f32(128, B) | kBmn, k > 0);
                 tc::mma_commit(bar + DONE_O);
             }
-            if (sum)
-                for (int e = 0; e < pieces; ++e)
-                    for (int k = 0; k < steps; ++k)
-                        // keys of 64 columns: the same panel again for the second 64 rows of the product
-                        tc::mma_bf16_ss(tmem + L::Y, sdesc_mn(base + L::K + k * 2048, A == 128 ? kPanel : 0),
-                                        sdesc_mn(base + (e == 0 ? L::V1 : e == 1 ? L::V2 : L::V3) + k * 2048, kPanel),
-                                        tc::idesc_bf16_f32(128, B) | kAmn | kBmn, carry || e > 0 || k > 0);
-            tc::mma_commit(bar + DONE_Y);
         }
         __syncwarp();
         if (!STATES) {
@@ -423,20 +439,28 @@ __global__ void __launch_bounds__(Layout<A, B>::T, Layout<A, B>::CTAS) la_tensor
                 if (quad * 32 + r < n && o0 + ch * 8 < j.b) *(uint4*)(out + rows_out[k] * j.out.row + ch * 8) = w;
             }
         }
-        waited(DONE_Y, phase);
-        tc::tc_fence_after_sync();
+        if (sum) {
+            waited(DONE_Y, sums & 1);
+            tc::tc_fence_after_sync();
+            ++sums;
+        }
         if (next) {
             if (L::in_q) load_q(to);
             load_kv(to);
         }
-        if (!STATES) __syncthreads();                   // the rows have left the pieces' place
         if (sum) {
-            float y[L::YC];
-            load_columns(L::Y + y0, y);
-            if (!final) {
-                put_state(y, exp2f(decay_of(to) * l2));
-                carry = true;
-            } else {
+            float v[L::YC];
+            const float keep = exp2f(decay_of(at) * l2);
+            load_columns(L::Y + y0, v);
+#pragma unroll
+            for (int k = 0; k < L::YC; ++k) y[k] = fmaf(keep, y[k], v[k]);
+        }
+        if (!STATES) __syncthreads();                   // the rows have left the pieces' place
+        if (!final) {
+            if (!STATES) put_pieces();
+            carry = true;
+        } else {
+            if (sum) {
                 float* const fin = STATES ? la_start(p, j, at.c) : j.fin + la_state(p, j, at.c);
                 if (((uintptr_t)fin & 15) == 0) {       // widths are multiples of 8
 #pragma unroll
@@ -448,8 +472,6 @@ __global__ void __launch_bounds__(Layout<A, B>::T, Layout<A, B>::CTAS) la_tensor
                         if (x < j.a && y0 + k < j.b) fin[x * j.b + y0 + k] = y[k];
                 }
             }
-        }
-        if (final) {
             carry = next ? first_state(to, next_l2) : false;
             table ^= 1;
             l2 = next_l2;
