@@ -35,7 +35,7 @@ template <int A, int B> struct Layout {
     static constexpr int V3 = in_q ? Q : V2 + kC * B * 2;
     static constexpr int Y1 = (in_q ? V2 : V3) + kC * B * 2, Y2 = Y1 + A * B * 2;
     static constexpr int POWERS = Y2 + A * B * 2;               // [2][64]: lambda^n and lambda^(31-n), of two walks
-    static constexpr int BARS = POWERS + 512, BYTES = BARS + 64;
+    static constexpr int BARS = POWERS + 512, WALKS = BARS + 64, BYTES = WALKS + 128;       // WALKS: of this walk, the next and the last one
     // tensor memory, columns
     static constexpr uint32_t S = 0, O = 128, Y = O + B, COLUMNS = B == 64 ? 256 : 512;
     static constexpr int OC = B / PARTS, YC = A == 128 ? B / PARTS : B / (2 * PARTS);       // columns of a thread
@@ -82,12 +82,6 @@ __device__ __forceinline__ uint32_t cut(float& x, float& y)
     return w;
 }
 
-// A walk's place: its part, and the chunk's first step.
-struct LaSpot {
-    LaPart c;
-    int u;
-};
-
 // STATES: only what a piece adds to Y, into `starts`.
 template <int A, int B, bool STATES>
 __global__ void __launch_bounds__(Layout<A, B>::T, Layout<A, B>::CTAS) la_tensor_kernel(const __grid_constant__ LaArgs p, int total)
@@ -97,13 +91,13 @@ __global__ void __launch_bounds__(Layout<A, B>::T, Layout<A, B>::CTAS) la_tensor
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, quad = warp % 4, part = warp / 4;
     const uint32_t base = tc::smem_u32(sm);
     float* const powers = (float*)(sm + L::POWERS);
-    // S and O, O', the sum for Y are done; the weighted values are there
+    // S and O, O', the sum for Y are done
     uint64_t* const bar = (uint64_t*)(sm + L::BARS);
-    enum { DONE_S = 0, DONE_O, DONE_Y, PIECES, BARRIERS };
+    enum { DONE_S = 0, DONE_O, DONE_Y, BARRIERS };
     uint32_t* const slot_of_tmem = (uint32_t*)(bar + BARRIERS);
     int* const stop = (int*)(slot_of_tmem + 1);
     if (tid == 0) {
-        for (int i = 0; i < BARRIERS; ++i) tc::mbar_init(bar + i, i == PIECES ? L::T / 32 : 1);
+        for (int i = 0; i < BARRIERS; ++i) tc::mbar_init(bar + i, 1);
         *stop = 0;
         tc::fence_mbar_init();
     }
@@ -114,34 +108,34 @@ __global__ void __launch_bounds__(Layout<A, B>::T, Layout<A, B>::CTAS) la_tensor
 
     // the next walk of this CTA that has a step: there and back along the CTAs, as walks get shorter
     int round = -1;
-    auto next_walk = [&](LaSpot& s) {
+    auto next_walk = [&](LaPart* to) {
         for (;;) {
             ++round;
             const int64_t id = (int64_t)round * gridDim.x + (round & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
             if (id >= total) return false;
-            s.c = la_part(p, (unsigned)id);
-            s.u = s.c.begin;
+            const LaPart c = la_part(p, (unsigned)id);
             if (STATES) {
-                if (s.c.last) continue;
+                if (c.last) continue;
             } else {
-                const LaJob& j = p.job[s.c.job];
-                la_past_end<__nv_bfloat16>(p, j, s.c);
-                if (s.c.len == 0) {
-                    la_pass(j, la_state(p, j, s.c));
+                const LaJob& j = p.job[c.job];
+                la_past_end<__nv_bfloat16>(p, j, c);
+                if (c.len == 0) {
+                    la_pass(j, la_state(p, j, c));
                     continue;
                 }
             }
+            if (tid == 0) *to = c;
             return true;
         }
     };
     // first row of a step (the walk's own lies `slot` behind it); steps past the chunk's end count as its last
-    auto row_of = [&](const LaSpot& s, int back, int step, int n) {
-        const int u = s.u + min(step, n - 1), t = (s.c.d == 1) != (back != 0) ? s.c.len - 1 - u : u;
+    auto row_of = [&](const LaPart& c, int u, int back, int step, int n) {
+        const int v = u + min(step, n - 1), t = (c.d == 1) != (back != 0) ? c.len - 1 - v : v;
         return __ldg(p.off + t);
     };
-    auto steps_of = [&](const LaSpot& s) { return min(kC, s.c.end - s.u); };
+    auto steps_of = [&](const LaPart& c, int u) { return min(kC, c.end - u); };
     // steps that a chunk's state decays by: one less behind the last step of a walk whose final state holds one lambda less
-    auto decay_of = [&](const LaSpot& s) { return steps_of(s) - (s.c.last && s.u + kC >= s.c.end ? p.job[s.c.job].early : 0); };
+    auto decay_of = [&](const LaPart& c, int u) { return steps_of(c, u) - (c.last && u + kC >= c.end ? p.job[c.job].early : 0); };
     auto set_powers = [&](int which, float l2) {
         if (tid < 64) powers[which * 64 + tid] = exp2f((tid < 32 ? tid : 63 - tid) * l2);
     };
@@ -149,36 +143,37 @@ __global__ void __launch_bounds__(Layout<A, B>::T, Layout<A, B>::CTAS) la_tensor
     // a chunk's rows: 16 bytes a thread and copy, zeros past the end.  Where they lie is looked up a chunk ahead.
     constexpr int CHA = A / 8, EACHA = L::T / CHA, ITA = kC / EACHA, CHB = B / 8, EACHB = L::T / CHB, ITB = kC / EACHB;
     int rows_a[ITA], rows_b[A == B ? 1 : ITB];
-    auto find_rows = [&](const LaSpot& s) {
-        const int n = steps_of(s), back = p.job[s.c.job].back;
+    auto find_rows = [&](const LaPart& c, int u) {
+        const int n = steps_of(c, u), back = p.job[c.job].back;
 #pragma unroll
-        for (int i = 0; i < ITA; ++i) rows_a[i] = row_of(s, back, i * EACHA + tid / CHA, n);
+        for (int i = 0; i < ITA; ++i) rows_a[i] = row_of(c, u, back, i * EACHA + tid / CHA, n);
         if (A != B) {
 #pragma unroll
-            for (int i = 0; i < ITB; ++i) rows_b[A == B ? 0 : i] = row_of(s, back, i * EACHB + tid / CHB, n);
+            for (int i = 0; i < ITB; ++i) rows_b[A == B ? 0 : i] = row_of(c, u, back, i * EACHB + tid / CHB, n);
         }
     };
-    auto copy = [&](const LaRows& r, const LaSpot& s, int to, int w, const auto& rows, auto width) {
+    auto copy = [&](const LaRows& r, const LaPart& c, int u, int to, int w, const auto& rows, auto width) {
         constexpr int CH = decltype(width)::value / 8, EACH = L::T / CH;
-        const int ch = tid % CH, n = ch * 8 < w ? steps_of(s) : 0;
-        const __nv_bfloat16* const from = (const __nv_bfloat16*)r.p + s.c.d * r.dir + s.c.h * r.head + s.c.slot * r.row + (n > 0 ? ch * 8 : 0);
+        const int ch = tid % CH, n = ch * 8 < w ? steps_of(c, u) : 0;
+        const __nv_bfloat16* const from = (const __nv_bfloat16*)r.p + c.d * r.dir + c.h * r.head + c.slot * r.row + (n > 0 ? ch * 8 : 0);
         const uint32_t at0 = base + to + tile_at(tid / CH, ch, kPanel);     // EACH rows on: the same swizzle, EACH a multiple of 8
 #pragma unroll
         for (int i = 0; i < kC / EACH; ++i) cp_async16(at0 + i * EACH * 128, from + rows[i] * r.row, i * EACH + tid / CH < n);
     };
-    auto load_q = [&](const LaSpot& s) {
-        const LaJob& j = p.job[s.c.job];
-        if (!STATES) copy(j.q, s, L::Q, j.a, rows_a, std::integral_constant<int, A>());
+    auto load_q = [&](const LaPart& c, int u) {
+        const LaJob& j = p.job[c.job];
+        if (!STATES) copy(j.q, c, u, L::Q, j.a, rows_a, std::integral_constant<int, A>());
     };
-    auto load_kv = [&](const LaSpot& s) {
-        const LaJob& j = p.job[s.c.job];
-        copy(j.k, s, L::K, j.a, rows_a, std::integral_constant<int, A>());
-        if constexpr (A == B) copy(j.v, s, L::V, j.b, rows_a, std::integral_constant<int, B>());
-        else copy(j.v, s, L::V, j.b, rows_b, std::integral_constant<int, B>());
+    auto load_kv = [&](const LaPart& c, int u) {
+        const LaJob& j = p.job[c.job];
+        copy(j.k, c, u, L::K, j.a, rows_a, std::integral_constant<int, A>());
+        if constexpr (A == B) copy(j.v, c, u, L::V, j.b, rows_a, std::integral_constant<int, B>());
+        else copy(j.v, c, u, L::V, j.b, rows_b, std::integral_constant<int, B>());
     };
 
-    LaSpot at;
-    bool more = next_walk(at);
+    LaPart* const walks = (LaPart*)(sm + L::WALKS);
+    int now = 0, u = 0;                                 // this walk's place, and the chunk's first step
+    bool more = next_walk(walks);
     tc::tc_fence_before_sync();
     __syncthreads();
     tc::tc_fence_after_sync();
@@ -217,9 +212,9 @@ __global__ void __launch_bounds__(Layout<A, B>::T, Layout<A, B>::CTAS) la_tensor
         for (int k = 0; k < N; ++k) v[k] = __uint_as_float(r[k / 16][k % 16]);
     };
     // Y in front of a walk; false: nothing
-    auto first_state = [&](const LaSpot& s, float l2) {
-        const LaJob& j = p.job[s.c.job];
-        const float* from = STATES ? nullptr : j.starts ? la_start(p, j, s.c) : j.init ? j.init + la_state(p, j, s.c) : nullptr;
+    auto first_state = [&](const LaPart& c, float l2) {
+        const LaJob& j = p.job[c.job];
+        const float* from = STATES ? nullptr : j.starts ? la_start(p, j, c) : j.init ? j.init + la_state(p, j, c) : nullptr;
         if (!from) {
 #pragma unroll
             for (int k = 0; k < L::YC; ++k) y[k] = 0.f;
@@ -248,36 +243,34 @@ __global__ void __launch_bounds__(Layout<A, B>::T, Layout<A, B>::CTAS) la_tensor
     bool carry = false;                                 // is there anything in Y?
     int table = 0, sums = 0;                            // the walk's powers; sums for Y so far
     if (more) {
-        find_rows(at);
-        load_q(at);
-        load_kv(at);
-        l2 = la_log2_decay(p, at.c.d, at.c.h);
+        u = walks[0].begin;
+        find_rows(walks[0], u);
+        load_q(walks[0], u);
+        load_kv(walks[0], u);
+        l2 = la_log2_decay(p, walks[0].d, walks[0].h);
         set_powers(0, l2);
-        carry = first_state(at, l2);
+        carry = first_state(walks[0], l2);
     }
     for (uint32_t phase = 0; more; phase ^= 1) {
-        const LaJob& j = p.job[at.c.job];
-        const int n = steps_of(at), steps = (n + 15) / 16;
-        const bool final = at.u + kC >= at.c.end, sum = STATES || !final || (at.c.last && j.fin);
-        const int pieces = j.pieces;
-        LaSpot to = at;
-        bool next = true;
-        float next_l2 = l2;
-        if (!final) {
-            to.u = at.u + kC;
-        } else {
-            next = next_walk(to);
-            if (next) {
-                next_l2 = la_log2_decay(p, to.c.d, to.c.h);
-                set_powers(table ^ 1, next_l2);
-            }
-        }
-        if (next) find_rows(to);
+        const LaPart& at = walks[now];
+        const LaJob& j = p.job[at.job];
+        const int n = steps_of(at, u), steps = (n + 15) / 16, pieces = j.pieces;
+        const bool final = u + kC >= at.end, sum = STATES || !final || (at.last && j.fin);
+        const int then = final ? (now + 1) % 3 : now;
+        const LaPart& to = walks[then];
+        const bool next = !final || next_walk(walks + then);
         cp_async_wait();
         tc::fence_async_smem();
         tc::tc_fence_before_sync();
         __syncthreads();
         if (*(volatile int*)stop) break;
+        const int then_u = final ? to.begin : u + kC;
+        float next_l2 = l2;
+        if (final && next) {
+            next_l2 = la_log2_decay(p, to.d, to.h);
+            set_powers(table ^ 1, next_l2);
+        }
+        if (next) find_rows(to, then_u);
         if (!STATES && tid == 0) {
             tc::tc_fence_after_sync();
             for (int k = 0; k < A / 16; ++k) {
@@ -299,7 +292,7 @@ __global__ void __launch_bounds__(Layout<A, B>::T, Layout<A, B>::CTAS) la_tensor
         constexpr int CH = B / 8, EACH = L::T / CH, IT = kC / EACH;
         uint4 third[L::in_q ? IT : 1];
         if (sum) {
-            const int behind = decay_of(at);
+            const int behind = decay_of(at, u);
 #pragma unroll
             for (int i = 0; i < IT; ++i) {
                 const int s = i * EACH + tid / CH;
@@ -331,33 +324,13 @@ __global__ void __launch_bounds__(Layout<A, B>::T, Layout<A, B>::CTAS) la_tensor
 #pragma unroll
             for (int i = 0; i < IT; ++i) *(uint4*)(sm + L::V3 + tile_at(i * EACH + tid / CH, tid % CH, kPanel)) = third[L::in_q ? i : 0];
         }
-        if (sum) {
-            // what a chunk adds to Y, while the rest goes on
-            tc::fence_async_smem();
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive(bar + PIECES);
-            if (warp == 0) {
-                waited(PIECES, sums & 1);
-                if (lane == 0) {
-                    tc::tc_fence_after_sync();
-                    for (int e = pieces - 1; e >= 0; --e)
-                        for (int k = 0; k < steps; ++k)
-                            // keys of 64 columns: the same panel again for the second 64 rows of the product
-                            tc::mma_bf16_ss(tmem + L::Y, sdesc_mn(base + L::K + k * 2048, A == 128 ? kPanel : 0),
-                                            sdesc_mn(base + (e == 0 ? L::V1 : e == 1 ? L::V2 : L::V3) + k * 2048, kPanel),
-                                            tc::idesc_bf16_f32(128, B) | kAmn | kBmn, e < pieces - 1 || k > 0);
-                    tc::mma_commit(bar + DONE_Y);
-                }
-                __syncwarp();
-            }
-        }
         if (!STATES) {
 #pragma unroll
-            for (int k = 0; k < CPR; ++k) rows_out[k] = row_of(at, j.back, quad * 32 + k * RPT + lane / CPR, n);
+            for (int k = 0; k < CPR; ++k) rows_out[k] = row_of(at, u, j.back, quad * 32 + k * RPT + lane / CPR, n);
             if (!L::in_q) {
                 waited(DONE_S, phase);
                 tc::tc_fence_after_sync();
-                if (next) load_q(to);
+                if (next) load_q(to, then_u);
             }
         }
         if (!STATES) {
@@ -403,23 +376,33 @@ __global__ void __launch_bounds__(Layout<A, B>::T, Layout<A, B>::CTAS) la_tensor
             }
             tc::tmem_wait_st();
         }
-        if (!STATES) {
-            tc::tc_fence_before_sync();
-            __syncthreads();
-            if (*(volatile int*)stop) break;
-            if (tid == 0) {
-                tc::tc_fence_after_sync();
+        tc::fence_async_smem();
+        tc::tc_fence_before_sync();
+        __syncthreads();
+        if (*(volatile int*)stop) break;
+        if (tid == 0) {
+            tc::tc_fence_after_sync();
+            if (!STATES) {
                 for (int k = 0; k < steps; ++k)
                     tc::mma_bf16_ts(tmem + L::O, tmem + L::S + 32 * (k / 2) + 8 * (k % 2), sdesc_mn(base + L::V + k * 2048, kPanel),
                                     tc::idesc_bf16_f32(128, B) | kBmn, k > 0);
                 tc::mma_commit(bar + DONE_O);
+            }
+            if (sum) {
+                for (int e = pieces - 1; e >= 0; --e)
+                    for (int k = 0; k < steps; ++k)
+                        // keys of 64 columns: the same panel again for the second 64 rows of the product
+                        tc::mma_bf16_ss(tmem + L::Y, sdesc_mn(base + L::K + k * 2048, A == 128 ? kPanel : 0),
+                                        sdesc_mn(base + (e == 0 ? L::V1 : e == 1 ? L::V2 : L::V3) + k * 2048, kPanel),
+                                        tc::idesc_bf16_f32(128, B) | kAmn | kBmn, e < pieces - 1 || k > 0);
+                tc::mma_commit(bar + DONE_Y);
             }
         }
         __syncwarp();
         if (!STATES) {
             // rows out: 16 bytes a thread and CPR threads a row, by way of the warp's part of the pieces of Y, which S and O have read
             unsigned char* const stage = sm + L::Y1 + warp * 64 * L::OC;
-            __nv_bfloat16* const out = (__nv_bfloat16*)j.out.p + at.c.d * j.out.dir + at.c.h * j.out.head + at.c.slot * j.out.row + o0;
+            __nv_bfloat16* const out = (__nv_bfloat16*)j.out.p + at.d * j.out.dir + at.h * j.out.head + at.slot * j.out.row + o0;
             waited(DONE_O, phase);
             tc::tc_fence_after_sync();
             float v[L::OC];
@@ -445,12 +428,12 @@ __global__ void __launch_bounds__(Layout<A, B>::T, Layout<A, B>::CTAS) la_tensor
             ++sums;
         }
         if (next) {
-            if (L::in_q) load_q(to);
-            load_kv(to);
+            if (L::in_q) load_q(to, then_u);
+            load_kv(to, then_u);
         }
         if (sum) {
             float v[L::YC];
-            const float keep = exp2f(decay_of(at) * l2);
+            const float keep = exp2f(decay_of(at, u) * l2);
             load_columns(L::Y + y0, v);
 #pragma unroll
             for (int k = 0; k < L::YC; ++k) y[k] = fmaf(keep, y[k], v[k]);
@@ -461,7 +444,7 @@ __global__ void __launch_bounds__(Layout<A, B>::T, Layout<A, B>::CTAS) la_tensor
             carry = true;
         } else {
             if (sum) {
-                float* const fin = STATES ? la_start(p, j, at.c) : j.fin + la_state(p, j, at.c);
+                float* const fin = STATES ? la_start(p, j, at) : j.fin + la_state(p, j, at);
                 if (((uintptr_t)fin & 15) == 0) {       // widths are multiples of 8
 #pragma unroll
                     for (int k = 0; k < L::YC; k += 4)
@@ -476,7 +459,8 @@ __global__ void __launch_bounds__(Layout<A, B>::T, Layout<A, B>::CTAS) la_tensor
             table ^= 1;
             l2 = next_l2;
         }
-        at = to;
+        now = then;
+        u = then_u;
         more = next;
     }
     cp_async_wait();
