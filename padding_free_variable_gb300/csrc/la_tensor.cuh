@@ -211,6 +211,8 @@ __global__ void __launch_bounds__(Layout<A, B>::T, Layout<A, B>::CTAS) la_tensor
 #pragma unroll
         for (int k = 0; k < N; ++k) v[k] = __uint_as_float(r[k / 16][k % 16]);
     };
+    // a state on its way in or out, in the place of Y's pieces: 16 bytes next to each other for threads next to each other
+    auto whole_at = [&](int r, int f) { return L::Y1 + r * B * 4 + ((f ^ (r & 7)) << 4); };
     // Y in front of a walk; false: nothing
     auto first_state = [&](const LaPart& c, float l2) {
         const LaJob& j = p.job[c.job];
@@ -223,11 +225,18 @@ __global__ void __launch_bounds__(Layout<A, B>::T, Layout<A, B>::CTAS) la_tensor
         const bool flip = j.flip && !j.starts;
         const float first = j.early && !j.starts ? exp2f(l2) : 1.f;
         if (!flip && ((uintptr_t)from & 15) == 0) {
+            for (int i = tid; i < A * B / 4; i += L::T) {
+                const int r = i / (B / 4), f = i % (B / 4);
+                const bool in = r < j.a && 4 * f < j.b;
+                *(float4*)(sm + whole_at(r, f)) = in ? *(const float4*)(from + r * j.b + 4 * f) : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+            __syncthreads();
 #pragma unroll
             for (int k = 0; k < L::YC; k += 4) {
-                const float4 q = x < j.a && y0 + k < j.b ? *(const float4*)(from + x * j.b + y0 + k) : make_float4(0.f, 0.f, 0.f, 0.f);
+                const float4 q = *(const float4*)(sm + whole_at(x, (y0 + k) / 4));
                 y[k] = first * q.x; y[k + 1] = first * q.y; y[k + 2] = first * q.z; y[k + 3] = first * q.w;
             }
+            __syncthreads();
         } else {
 #pragma unroll
             for (int k = 0; k < L::YC; ++k) {
@@ -448,7 +457,13 @@ __global__ void __launch_bounds__(Layout<A, B>::T, Layout<A, B>::CTAS) la_tensor
                 if (((uintptr_t)fin & 15) == 0) {       // widths are multiples of 8
 #pragma unroll
                     for (int k = 0; k < L::YC; k += 4)
-                        if (x < j.a && y0 + k < j.b) *(float4*)(fin + x * j.b + y0 + k) = make_float4(y[k], y[k + 1], y[k + 2], y[k + 3]);
+                        *(float4*)(sm + whole_at(x, (y0 + k) / 4)) = make_float4(y[k], y[k + 1], y[k + 2], y[k + 3]);
+                    __syncthreads();
+                    for (int i = tid; i < A * B / 4; i += L::T) {
+                        const int r = i / (B / 4), f = i % (B / 4);
+                        if (r < j.a && 4 * f < j.b) *(float4*)(fin + r * j.b + 4 * f) = *(const float4*)(sm + whole_at(r, f));
+                    }
+                    __syncthreads();
                 } else {
 #pragma unroll
                     for (int k = 0; k < L::YC; ++k)
