@@ -270,7 +270,7 @@ lstm_status launch(const LaArgs& a, bool states, cudaStream_t cs)
     }
     const unsigned grid = (unsigned)((int64_t)a.count * a.ndir * a.heads * a.jobs);
     auto kernel = states ? la_general_kernel<T, V, true> : la_general_kernel<T, V, false>;
-    LSTM_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)need));
+    if (need > 48 * 1024) LSTM_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)need));
     kernel<<<grid, kThreads, need, cs>>>(a);
     return cudaGetLastError() == cudaSuccess ? LSTM_OK : LSTM_ERR_CUDA;
 }

@@ -225,8 +225,9 @@ __global__ void __launch_bounds__(Layout<A, B>::T, Layout<A, B>::CTAS) la_tensor
         const bool flip = j.flip && !j.starts;
         const float first = j.early && !j.starts ? exp2f(l2) : 1.f;
         if (!flip && ((uintptr_t)from & 15) == 0) {
-            for (int i = tid; i < A * B / 4; i += L::T) {
-                const int r = i / (B / 4), f = i % (B / 4);
+#pragma unroll
+            for (int k = 0; k < A * B / 4 / L::T; ++k) {        // all reads on their way together
+                const int i = k * L::T + tid, r = i / (B / 4), f = i % (B / 4);
                 const bool in = r < j.a && 4 * f < j.b;
                 *(float4*)(sm + whole_at(r, f)) = in ? *(const float4*)(from + r * j.b + 4 * f) : make_float4(0.f, 0.f, 0.f, 0.f);
             }
@@ -459,8 +460,9 @@ __global__ void __launch_bounds__(Layout<A, B>::T, Layout<A, B>::CTAS) la_tensor
                     for (int k = 0; k < L::YC; k += 4)
                         *(float4*)(sm + whole_at(x, (y0 + k) / 4)) = make_float4(y[k], y[k + 1], y[k + 2], y[k + 3]);
                     __syncthreads();
-                    for (int i = tid; i < A * B / 4; i += L::T) {
-                        const int r = i / (B / 4), f = i % (B / 4);
+#pragma unroll
+                    for (int k = 0; k < A * B / 4 / L::T; ++k) {
+                        const int i = k * L::T + tid, r = i / (B / 4), f = i % (B / 4);
                         if (r < j.a && 4 * f < j.b) *(float4*)(fin + r * j.b + 4 * f) = *(const float4*)(sm + whole_at(r, f));
                     }
                     __syncthreads();

@@ -6,6 +6,7 @@
 // value is read once and written once.
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "scan_plan.cuh"
 
@@ -79,26 +80,26 @@ template <typename T> __device__ __forceinline__ T narrow(float v);
 template <> __device__ __forceinline__ float narrow<float>(float v) { return v; }
 template <> __device__ __forceinline__ __nv_bfloat16 narrow<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
-// Where a lane's four pairs (from 4 l on) lie.  VEC: in two groups of four neighbours, the pairs' first and second values
-// (rotated halves) or two pairs each; otherwise every value has a column of its own.
-template <bool VEC> struct Lane {
+// Where a lane's four pairs (from 4 l on) lie.  VEC: in two groups of four neighbours: with HALF the pairs' first and second
+// values (what is not rotated has no pairs), else two pairs each.  Otherwise every value has a column of its own.
+template <bool VEC, bool HALF> struct Lane {
     int pair, d, turned;                // turned: pairs of halves, `turned` apart
     bool on;
     __device__ __forceinline__ void set(const QkArgs& p, int l)
     {
         pair = 4 * l;
         d = p.d;
-        turned = p.half ? p.rotary / 2 : 0;
+        turned = HALF ? p.rotary / 2 : 0;
         on = 2 * pair < d;
     }
-    __device__ __forceinline__ bool halves() const { return pair < turned; }
     __device__ __forceinline__ int col(int e, int which) const
     {
         const int k = pair + e;
-        return (VEC ? halves() : k < turned) ? k + which * turned : 2 * k + which;
+        if (VEC && HALF) return group(which) + e;
+        return HALF && k < turned ? k + which * turned : 2 * k + which;
     }
     __device__ __forceinline__ bool has(int e, int which) const { return VEC ? on : col(e, which) < d; }
-    __device__ __forceinline__ int group(int which) const { return halves() ? pair + which * turned : 2 * pair + 4 * which; }
+    __device__ __forceinline__ int group(int which) const { return HALF && pair < turned ? pair + which * turned : 2 * pair + 4 * which; }
 };
 
 // A lane's values of one head as they were read: first[4] and second[4] of its pairs.
@@ -106,26 +107,31 @@ template <typename T, bool VEC> struct Pairs;
 template <typename T> struct Pairs<T, true> {
     Four<T> a, b;
     __device__ __forceinline__ void zero() { const float z[4] = {}; a.set(z); b.set(z); }
-    __device__ __forceinline__ void load(const T* p, const Lane<true>& w) { a.load(p + w.group(0)); b.load(p + w.group(1)); }
-    __device__ __forceinline__ void get(float (&f)[4], float (&s)[4], const Lane<true>& w) const
+    template <bool HALF> __device__ __forceinline__ void load(const T* p, const Lane<true, HALF>& w) { a.load(p + w.group(0)); b.load(p + w.group(1)); }
+    template <bool HALF> __device__ __forceinline__ void get(float (&f)[4], float (&s)[4], const Lane<true, HALF>&) const
     {
         float x[4], y[4];
         a.get(x);
         b.get(y);
-        const bool h = w.halves();
-        f[0] = x[0];             s[0] = h ? y[0] : x[1];
-        f[1] = h ? x[1] : x[2];  s[1] = h ? y[1] : x[3];
-        f[2] = h ? x[2] : y[0];  s[2] = h ? y[2] : y[1];
-        f[3] = h ? x[3] : y[2];  s[3] = y[3];
+        if (HALF) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) { f[e] = x[e]; s[e] = y[e]; }
+        } else {
+            f[0] = x[0]; s[0] = x[1]; f[1] = x[2]; s[1] = x[3];
+            f[2] = y[0]; s[2] = y[1]; f[3] = y[2]; s[3] = y[3];
+        }
     }
-    __device__ __forceinline__ static void put(T* p, const float (&f)[4], const float (&s)[4], const Lane<true>& w)
+    template <bool HALF> __device__ __forceinline__ static void put(T* p, const float (&f)[4], const float (&s)[4], const Lane<true, HALF>& w)
     {
-        const bool h = w.halves();
-        const float x[4] = {f[0], h ? f[1] : s[0], h ? f[2] : f[1], h ? f[3] : s[1]};
-        const float y[4] = {h ? s[0] : f[2], h ? s[1] : s[2], h ? s[2] : f[3], s[3]};
         Four<T> a, b;
-        a.set(x);
-        b.set(y);
+        if (HALF) {
+            a.set(f);
+            b.set(s);
+        } else {
+            const float x[4] = {f[0], s[0], f[1], s[1]}, y[4] = {f[2], s[2], f[3], s[3]};
+            a.set(x);
+            b.set(y);
+        }
         a.store(p + w.group(0));
         b.store(p + w.group(1));
     }
@@ -137,7 +143,7 @@ template <typename T> struct Pairs<T, false> {
 #pragma unroll
         for (int e = 0; e < 4; ++e) f[e] = s[e] = 0.f;
     }
-    __device__ __forceinline__ void load(const T* p, const Lane<false>& w)
+    template <typename L> __device__ __forceinline__ void load(const T* p, const L& w)
     {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -145,12 +151,12 @@ template <typename T> struct Pairs<T, false> {
             s[e] = w.has(e, 1) ? to_f32(p[w.col(e, 1)]) : 0.f;
         }
     }
-    __device__ __forceinline__ void get(float (&a)[4], float (&b)[4], const Lane<false>&) const
+    template <typename L> __device__ __forceinline__ void get(float (&a)[4], float (&b)[4], const L&) const
     {
 #pragma unroll
         for (int e = 0; e < 4; ++e) { a[e] = f[e]; b[e] = s[e]; }
     }
-    __device__ __forceinline__ static void put(T* p, const float (&f)[4], const float (&s)[4], const Lane<false>& w)
+    template <typename L> __device__ __forceinline__ static void put(T* p, const float (&f)[4], const float (&s)[4], const L& w)
     {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -172,11 +178,13 @@ __device__ __forceinline__ float sum8(const float (&f)[4], const float (&s)[4])
     return ((f[0] + s[0]) + (f[1] + s[1])) + ((f[2] + s[2]) + (f[3] + s[3]));
 }
 
-template <typename T, bool VEC, bool BACK, int AHEAD>
-__global__ void __launch_bounds__(kWarps * 32) qk_norm_kernel(const QkArgs p)
+template <typename T, bool VEC, bool BACK, bool HALF>
+__global__ void __launch_bounds__(kWarps * 32, BACK ? 4 : 4) qk_norm_kernel(const QkArgs p)
 {
+    constexpr int AHEAD = BACK ? 2 : 4;                 // heads of a lane on their way at a time
+    __shared__ float turns[kWarps][2][kMaxHead / 2];    // cosines and sines of the warp's row
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, l = lane % p.lanes, sub = lane / p.lanes, at_once = 32 / p.lanes;
-    Lane<VEC> w;
+    Lane<VEC, HALF> w;
     w.set(p, l);
     float wf[2][4], ws[2][4], gf[2][4] = {}, gs[2][4] = {};
 #pragma unroll
@@ -186,7 +194,7 @@ __global__ void __launch_bounds__(kWarps * 32) qk_norm_kernel(const QkArgs p)
             wf[k][e] = w.has(e, 0) ? p.w[k] ? __ldg(p.w[k] + w.col(e, 0)) : 1.f : 0.f;
             ws[k][e] = w.has(e, 1) ? p.w[k] ? __ldg(p.w[k] + w.col(e, 1)) : 1.f : 0.f;
         }
-    const int passes0 = (p.heads[0] + at_once - 1) / at_once, passes = passes0 + (p.heads[1] + at_once - 1) / at_once;
+    const int passes0 = (p.heads[0] + at_once - 1) / at_once;
     const float per = 1.f / p.d;
     const int64_t units = p.rows * p.split;
     for (int64_t unit = blockIdx.x * (int64_t)kWarps + warp; unit < units; unit += (int64_t)gridDim.x * kWarps) {
@@ -202,93 +210,109 @@ __global__ void __launch_bounds__(kWarps * 32) qk_norm_kernel(const QkArgs p)
                 step = step_of(p, row, lane);
             }
         }
-        float co[4], si[4];
-        {
+        float co[4] = {1.f, 1.f, 1.f, 1.f}, si[4] = {};
+        if (p.rotary) {
+            // a lane each pair, then every lane its own four; position * frequency modulo a turn, in half turns from -1 to 1
             const int64_t at = p.positions ? (int64_t)__ldg(p.positions + row) : p.first + step;
+            __syncwarp();
+            for (int i = lane; i < p.rotary / 2; i += 32) {
+                const unsigned long long a = (unsigned long long)at * (unsigned long long)__ldg((const long long*)p.turns + i);
+                float s, c;
+                sincospif((float)(int)(a >> 32) * 4.656612873077393e-10f, &s, &c);
+                turns[warp][0][i] = c * p.turn_scale;
+                turns[warp][1][i] = s * p.turn_scale;
+            }
+            __syncwarp();
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                co[e] = 1.f;
-                si[e] = 0.f;
+            for (int e = 0; e < 4; ++e)
                 if (4 * l + e < p.rotary / 2) {
-                    // position * frequency modulo a turn, in half turns from -1 to 1
-                    const unsigned long long a = (unsigned long long)at * (unsigned long long)__ldg((const long long*)p.turns + 4 * l + e);
-                    sincospif((float)(int)(a >> 32) * 4.656612873077393e-10f, &si[e], &co[e]);
-                    co[e] *= p.turn_scale;
-                    si[e] *= p.turn_scale;
+                    co[e] = turns[warp][0][4 * l + e];
+                    si[e] = turns[warp][1][4 * l + e];
                 }
-            }
         }
-        for (int q0 = begin; q0 < passes; q0 += AHEAD * p.split) {
-            Pairs<T, VEC> x[AHEAD], y[BACK ? AHEAD : 1];
+        // the heads of one operand, `at_once` a pass; of a row's passes this warp takes every split-th
+        auto heads = [&](auto which) {
+            constexpr int k = decltype(which)::value;
+            const int count = p.heads[k];
+            int h = (k == 0 ? begin : (begin + passes0 * (p.split - 1)) % p.split) * at_once + sub;
+            const int by = at_once * p.split;
+            const T* x0 = (const T*)p.x[k] + row * p.xr[k] + h * p.xh[k];
+            const T* y0 = BACK ? (const T*)p.dy[k] + row * p.yr[k] + h * p.yh[k] : nullptr;
+            T* o0 = (T*)p.out[k] + row * p.our[k] + h * p.oh[k];
+            const int64_t xs = by * p.xh[k], ys = by * p.yh[k], os = by * p.oh[k];
+            for (; h - sub < count; h += AHEAD * by) {
+                Pairs<T, VEC> x[AHEAD], y[BACK ? AHEAD : 1];
 #pragma unroll
-            for (int n = 0; n < AHEAD; ++n) {
-                const int pass = q0 + n * p.split, k = pass >= passes0, h = (pass - (k ? passes0 : 0)) * at_once + sub;
-                x[n].zero();
-                if (BACK) y[BACK ? n : 0].zero();
-                if (pass < passes && h < p.heads[k] && w.on && live) {
-                    x[n].load((const T*)p.x[k] + row * p.xr[k] + h * p.xh[k], w);
-                    if (BACK) y[BACK ? n : 0].load((const T*)p.dy[k] + row * p.yr[k] + h * p.yh[k], w);
-                }
-            }
-#pragma unroll
-            for (int n = 0; n < AHEAD; ++n) {
-                const int pass = q0 + n * p.split;
-                if (pass >= passes) break;
-                const bool k = pass >= passes0;
-                const int h = (pass - (k ? passes0 : 0)) * at_once + sub;
-                float f[4], s[4], r = 1.f;
-                x[n].get(f, s, w);
-                if (p.kind == LSTM_NORM_LAYER) {
-                    const float mean = head_sum(sum8(f, s), p.lanes) * per;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        f[e] = w.has(e, 0) ? f[e] - mean : 0.f;
-                        s[e] = w.has(e, 1) ? s[e] - mean : 0.f;
+                for (int n = 0; n < AHEAD; ++n) {
+                    x[n].zero();
+                    if (BACK) y[BACK ? n : 0].zero();
+                    if (h + n * by < count && w.on && live) {
+                        x[n].load(x0, w);
+                        if (BACK) y[BACK ? n : 0].load(y0, w);
                     }
+                    x0 += xs;
+                    if (BACK) y0 += ys;
                 }
-                if (p.kind != LSTM_NORM_NONE) {
-                    float sf[4], ss[4];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) { sf[e] = f[e] * f[e]; ss[e] = s[e] * s[e]; }
-                    r = rsqrtf(head_sum(sum8(sf, ss), p.lanes) * per + p.eps);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) { f[e] *= r; s[e] *= r; }
-                }
-                if (!BACK) {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float a = f[e] * (k ? wf[1][e] : wf[0][e]), b = s[e] * (k ? ws[1][e] : ws[0][e]);
-                        f[e] = a * co[e] - b * si[e];
-                        s[e] = fmaf(a, si[e], b * co[e]);
-                    }
-                } else {
-                    float df[4], ds[4], uf[4], us[4];
-                    y[BACK ? n : 0].get(df, ds, w);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float a = fmaf(df[e], co[e], ds[e] * si[e]), b = ds[e] * co[e] - df[e] * si[e];
-                        if (k) { gf[1][e] = fmaf(a, f[e], gf[1][e]); gs[1][e] = fmaf(b, s[e], gs[1][e]); }
-                        else { gf[0][e] = fmaf(a, f[e], gf[0][e]); gs[0][e] = fmaf(b, s[e], gs[0][e]); }
-                        df[e] = a * (k ? wf[1][e] : wf[0][e]);
-                        ds[e] = b * (k ? ws[1][e] : ws[0][e]);
-                        uf[e] = df[e] * f[e];
-                        us[e] = ds[e] * s[e];
-                    }
-                    if (p.kind != LSTM_NORM_NONE) {
-                        const float along = head_sum(sum8(uf, us), p.lanes) * per;
-                        const float mean = p.kind == LSTM_NORM_LAYER ? head_sum(sum8(df, ds), p.lanes) * per : 0.f;
+                for (int n = 0; n < AHEAD; ++n) {
+                    if (h - sub + n * by >= count) break;
+                    float f[4], s[4], r = 1.f;
+                    x[n].get(f, s, w);
+                    if (p.kind == LSTM_NORM_LAYER) {
+                        const float mean = head_sum(sum8(f, s), p.lanes) * per;
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            df[e] = r * (df[e] - mean - f[e] * along);
-                            ds[e] = r * (ds[e] - mean - s[e] * along);
+                            f[e] = w.has(e, 0) ? f[e] - mean : 0.f;
+                            s[e] = w.has(e, 1) ? s[e] - mean : 0.f;
                         }
                     }
+                    if (p.kind != LSTM_NORM_NONE) {
+                        float sf[4], ss[4];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) { f[e] = df[e]; s[e] = ds[e]; }
+                        for (int e = 0; e < 4; ++e) { sf[e] = f[e] * f[e]; ss[e] = s[e] * s[e]; }
+                        r = rsqrtf(head_sum(sum8(sf, ss), p.lanes) * per + p.eps);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) { f[e] *= r; s[e] *= r; }
+                    }
+                    if (!BACK) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float a = f[e] * wf[k][e], b = s[e] * ws[k][e];
+                            f[e] = a * co[e] - b * si[e];
+                            s[e] = fmaf(a, si[e], b * co[e]);
+                        }
+                    } else {
+                        float df[4], ds[4], uf[4], us[4];
+                        y[BACK ? n : 0].get(df, ds, w);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float a = fmaf(df[e], co[e], ds[e] * si[e]), b = ds[e] * co[e] - df[e] * si[e];
+                            gf[k][e] = fmaf(a, f[e], gf[k][e]);
+                            gs[k][e] = fmaf(b, s[e], gs[k][e]);
+                            df[e] = a * wf[k][e];
+                            ds[e] = b * ws[k][e];
+                            uf[e] = df[e] * f[e];
+                            us[e] = ds[e] * s[e];
+                        }
+                        if (p.kind != LSTM_NORM_NONE) {
+                            const float along = head_sum(sum8(uf, us), p.lanes) * per;
+                            const float mean = p.kind == LSTM_NORM_LAYER ? head_sum(sum8(df, ds), p.lanes) * per : 0.f;
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                df[e] = r * (df[e] - mean - f[e] * along);
+                                ds[e] = r * (ds[e] - mean - s[e] * along);
+                            }
+                        }
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) { f[e] = df[e]; s[e] = ds[e]; }
+                    }
+                    if (h + n * by < count && w.on) Pairs<T, VEC>::put(o0, f, s, w);
+                    o0 += os;
                 }
-                if (h < p.heads[k] && w.on) Pairs<T, VEC>::put((T*)p.out[k] + row * p.our[k] + h * p.oh[k], f, s, w);
             }
-        }
+        };
+        heads(std::integral_constant<int, 0>());
+        if (p.heads[1] > 0) heads(std::integral_constant<int, 1>());
     }
     if (BACK && p.part) {
         // the block's sums: lanes of a warp, then its warps in order
@@ -332,8 +356,8 @@ __global__ void __launch_bounds__(256) qk_norm_sums_kernel(const QkArgs p)
 
 int blocks_of(int64_t rows) { return (int)std::min<int64_t>((rows + kWarps - 1) / kWarps, kMaxParts); }
 
-template <typename T, bool VEC>
-lstm_status launch(QkArgs p, bool back, cudaStream_t cs)
+template <typename T, bool VEC, bool HALF>
+lstm_status launch_layout(QkArgs p, bool back, cudaStream_t cs)
 {
     if (!back) {
         // a warp a row; where that leaves warps without one, a row's heads are spread over several
@@ -341,13 +365,19 @@ lstm_status launch(QkArgs p, bool back, cudaStream_t cs)
         while (p.split < passes && p.rows * p.split < 152 * kWarps) p.split *= 2;
         if (p.split > passes) p.split = passes;
         const int64_t blocks = std::min<int64_t>((p.rows * p.split + kWarps - 1) / kWarps, 152 * 6);
-        qk_norm_kernel<T, VEC, false, 4><<<(unsigned)blocks, kWarps * 32, 0, cs>>>(p);
+        qk_norm_kernel<T, VEC, false, HALF><<<(unsigned)blocks, kWarps * 32, 0, cs>>>(p);
     } else {
         p.parts = blocks_of(p.rows);
-        qk_norm_kernel<T, VEC, true, 2><<<p.parts, kWarps * 32, 0, cs>>>(p);
+        qk_norm_kernel<T, VEC, true, HALF><<<p.parts, kWarps * 32, 0, cs>>>(p);
         if (p.part) qk_norm_sums_kernel<<<ceil_div(2 * p.d, 8), 256, 0, cs>>>(p);
     }
     return cudaGetLastError() == cudaSuccess ? LSTM_OK : LSTM_ERR_CUDA;
+}
+
+template <typename T, bool VEC>
+lstm_status launch(const QkArgs& p, bool back, cudaStream_t cs)
+{
+    return p.half ? launch_layout<T, VEC, true>(p, back, cs) : launch_layout<T, VEC, false>(p, back, cs);
 }
 
 // ---------------------------------------------------------------- checks
