@@ -14,7 +14,7 @@ namespace lstm {
 
 namespace {
 
-constexpr int kWarps = 8, kMaxParts = 608, kMaxHead = 256;
+constexpr int kWarps = 8, kMaxParts = 456, kMaxHead = 256;
 
 struct QkArgs {
     // 0: queries, 1: keys
@@ -84,6 +84,7 @@ template <> __device__ __forceinline__ __nv_bfloat16 narrow<__nv_bfloat16>(float
 // values (what is not rotated has no pairs), else two pairs each.  Otherwise every value has a column of its own.
 template <bool VEC, bool HALF> struct Lane {
     int pair, d, turned;                // turned: pairs of halves, `turned` apart
+    int at[VEC ? 1 : 8];                // each value's column, -1: none
     bool on;
     __device__ __forceinline__ void set(const QkArgs& p, int l)
     {
@@ -91,14 +92,20 @@ template <bool VEC, bool HALF> struct Lane {
         d = p.d;
         turned = HALF ? p.rotary / 2 : 0;
         on = 2 * pair < d;
+        if (!VEC) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int k = pair + e / 2, c = HALF && k < turned ? k + e % 2 * turned : 2 * k + e % 2;
+                at[VEC ? 0 : e] = c < d ? c : -1;
+            }
+        }
     }
     __device__ __forceinline__ int col(int e, int which) const
     {
-        const int k = pair + e;
-        if (VEC && HALF) return group(which) + e;
-        return HALF && k < turned ? k + which * turned : 2 * k + which;
+        if (!VEC) return at[VEC ? 0 : 2 * e + which];
+        return HALF ? group(which) + e : 2 * (pair + e) + which;
     }
-    __device__ __forceinline__ bool has(int e, int which) const { return VEC ? on : col(e, which) < d; }
+    __device__ __forceinline__ bool has(int e, int which) const { return VEC ? on : col(e, which) >= 0; }
     __device__ __forceinline__ int group(int which) const { return HALF && pair < turned ? pair + which * turned : 2 * pair + 4 * which; }
 };
 
@@ -173,27 +180,48 @@ __device__ __forceinline__ float head_sum(float v, int lanes)
     return v;
 }
 
-__device__ __forceinline__ float sum8(const float (&f)[4], const float (&s)[4])
+// Two values at once: one instruction of the fp32 pipe.
+struct Two {
+    unsigned long long v;
+    __device__ __forceinline__ Two() {}
+    __device__ __forceinline__ Two(float a, float b) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b)); }
+    __device__ __forceinline__ float sum() const { float a, b; asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); return a + b; }
+    __device__ __forceinline__ void get(float* p) const { asm("mov.b64 {%0, %1}, %2;" : "=f"(p[0]), "=f"(p[1]) : "l"(v)); }
+};
+__device__ __forceinline__ Two operator*(Two a, Two b) { Two r; asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v)); return r; }
+__device__ __forceinline__ Two operator+(Two a, Two b) { Two r; asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v)); return r; }
+__device__ __forceinline__ Two fma2(Two a, Two b, Two c) { Two r; asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v)); return r; }
+__device__ __forceinline__ Two both(float a) { return Two(a, a); }
+
+// Four values.
+struct Quad {
+    Two a, b;
+    __device__ __forceinline__ void set(const float (&f)[4]) { a = Two(f[0], f[1]); b = Two(f[2], f[3]); }
+    __device__ __forceinline__ void get(float (&f)[4]) const { a.get(f); b.get(f + 2); }
+};
+__device__ __forceinline__ Quad operator*(Quad x, Quad y) { return {x.a * y.a, x.b * y.b}; }
+__device__ __forceinline__ Quad operator*(Quad x, Two y) { return {x.a * y, x.b * y}; }
+__device__ __forceinline__ Quad operator+(Quad x, Two y) { return {x.a + y, x.b + y}; }
+__device__ __forceinline__ Quad fma2(Quad x, Quad y, Quad z) { return {fma2(x.a, y.a, z.a), fma2(x.b, y.b, z.b)}; }
+__device__ __forceinline__ Quad fma2(Quad x, Two y, Quad z) { return {fma2(x.a, y, z.a), fma2(x.b, y, z.b)}; }
+// x . x2 + y . y2
+__device__ __forceinline__ float dot(Quad x, Quad x2, Quad y, Quad y2)
 {
-    return ((f[0] + s[0]) + (f[1] + s[1])) + ((f[2] + s[2]) + (f[3] + s[3]));
+    const Quad s = fma2(x, x2, y * y2);
+    return (s.a + s.b).sum();
 }
+__device__ __forceinline__ float total(Quad x, Quad y) { return ((x.a + y.a) + (x.b + y.b)).sum(); }
 
 template <typename T, bool VEC, bool BACK, bool HALF>
-__global__ void __launch_bounds__(kWarps * 32, BACK ? 4 : 4) qk_norm_kernel(const QkArgs p)
+__global__ void __launch_bounds__(kWarps * 32, 3) qk_norm_kernel(const QkArgs p)
 {
-    constexpr int AHEAD = BACK ? 2 : 4;                 // heads of a lane on their way at a time
+    constexpr int AHEAD = BACK ? 1 : 4;                 // heads of a lane on their way at a time
     __shared__ float turns[kWarps][2][kMaxHead / 2];    // cosines and sines of the warp's row
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, l = lane % p.lanes, sub = lane / p.lanes, at_once = 32 / p.lanes;
     Lane<VEC, HALF> w;
     w.set(p, l);
-    float wf[2][4], ws[2][4], gf[2][4] = {}, gs[2][4] = {};
-#pragma unroll
-    for (int k = 0; k < 2; ++k)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            wf[k][e] = w.has(e, 0) ? p.w[k] ? __ldg(p.w[k] + w.col(e, 0)) : 1.f : 0.f;
-            ws[k][e] = w.has(e, 1) ? p.w[k] ? __ldg(p.w[k] + w.col(e, 1)) : 1.f : 0.f;
-        }
+    Quad gf[2], gs[2];
+    for (int k = 0; k < 2; ++k) gf[k].a = gf[k].b = gs[k].a = gs[k].b = Two(0.f, 0.f);
     const int passes0 = (p.heads[0] + at_once - 1) / at_once;
     const float per = 1.f / p.d;
     const int64_t units = p.rows * p.split;
@@ -240,6 +268,25 @@ __global__ void __launch_bounds__(kWarps * 32, BACK ? 4 : 4) qk_norm_kernel(cons
             const T* y0 = BACK ? (const T*)p.dy[k] + row * p.yr[k] + h * p.yh[k] : nullptr;
             T* o0 = (T*)p.out[k] + row * p.our[k] + h * p.oh[k];
             const int64_t xs = by * p.xh[k], ys = by * p.yh[k], os = by * p.oh[k];
+            // the weights, from L1 once a row: registers are what keeps warps off the SM
+            float wf[4], ws[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                wf[e] = w.has(e, 0) ? p.w[k] ? __ldg(p.w[k] + w.col(e, 0)) : 1.f : 0.f;
+                ws[e] = w.has(e, 1) ? p.w[k] ? __ldg(p.w[k] + w.col(e, 1)) : 1.f : 0.f;
+            }
+            // a rotated and weighted pair: first A + second B, first C + second D; backwards the weights come later
+            Quad A, B, C, D, wq, wr;
+            wq.set(wf);
+            wr.set(ws);
+            {
+                const float ni[4] = {-si[0], -si[1], -si[2], -si[3]};
+                A.set(co);
+                C.set(si);
+                D = A;
+                B.set(ni);
+                if (!BACK) { A = wq * A; C = wq * C; B = wr * B; D = wr * D; }
+            }
             for (; h - sub < count; h += AHEAD * by) {
                 Pairs<T, VEC> x[AHEAD], y[BACK ? AHEAD : 1];
 #pragma unroll
@@ -259,53 +306,49 @@ __global__ void __launch_bounds__(kWarps * 32, BACK ? 4 : 4) qk_norm_kernel(cons
                     float f[4], s[4], r = 1.f;
                     x[n].get(f, s, w);
                     if (p.kind == LSTM_NORM_LAYER) {
-                        const float mean = head_sum(sum8(f, s), p.lanes) * per;
+                        const float mean = head_sum(((f[0] + s[0]) + (f[1] + s[1])) + ((f[2] + s[2]) + (f[3] + s[3])), p.lanes) * per;
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             f[e] = w.has(e, 0) ? f[e] - mean : 0.f;
                             s[e] = w.has(e, 1) ? s[e] - mean : 0.f;
                         }
                     }
-                    if (p.kind != LSTM_NORM_NONE) {
-                        float sf[4], ss[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) { sf[e] = f[e] * f[e]; ss[e] = s[e] * s[e]; }
-                        r = rsqrtf(head_sum(sum8(sf, ss), p.lanes) * per + p.eps);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) { f[e] *= r; s[e] *= r; }
-                    }
+                    Quad u, v;
+                    u.set(f);
+                    v.set(s);
+                    if (p.kind != LSTM_NORM_NONE) r = rsqrtf(head_sum(dot(u, u, v, v), p.lanes) * per + p.eps);
                     if (!BACK) {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float a = f[e] * wf[k][e], b = s[e] * ws[k][e];
-                            f[e] = a * co[e] - b * si[e];
-                            s[e] = fmaf(a, si[e], b * co[e]);
-                        }
+                        const Quad first = fma2(u, A, v * B), second = fma2(u, C, v * D);
+                        u = first * both(r);
+                        v = second * both(r);
                     } else {
-                        float df[4], ds[4], uf[4], us[4];
+                        // the error before the rotation, the weights' gradients, the weighted error through the norm
+                        float df[4], ds[4];
                         y[BACK ? n : 0].get(df, ds, w);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float a = fmaf(df[e], co[e], ds[e] * si[e]), b = ds[e] * co[e] - df[e] * si[e];
-                            gf[k][e] = fmaf(a, f[e], gf[k][e]);
-                            gs[k][e] = fmaf(b, s[e], gs[k][e]);
-                            df[e] = a * wf[k][e];
-                            ds[e] = b * ws[k][e];
-                            uf[e] = df[e] * f[e];
-                            us[e] = ds[e] * s[e];
-                        }
+                        Quad g, q;
+                        g.set(df);
+                        q.set(ds);
+                        const Quad a = fma2(g, A, q * C), b = fma2(q, D, g * B);
+                        u = u * both(r);
+                        v = v * both(r);
+                        gf[k] = fma2(a, u, gf[k]);
+                        gs[k] = fma2(b, v, gs[k]);
+                        g = a * wq;
+                        q = b * wr;
                         if (p.kind != LSTM_NORM_NONE) {
-                            const float along = head_sum(sum8(uf, us), p.lanes) * per;
-                            const float mean = p.kind == LSTM_NORM_LAYER ? head_sum(sum8(df, ds), p.lanes) * per : 0.f;
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                df[e] = r * (df[e] - mean - f[e] * along);
-                                ds[e] = r * (ds[e] - mean - s[e] * along);
-                            }
+                            const float along = head_sum(dot(g, u, q, v), p.lanes) * per;
+                            const float mean = p.kind == LSTM_NORM_LAYER ? head_sum(total(g, q), p.lanes) * per : 0.f;
+                            g = fma2(u, both(-along), g) + both(-mean);
+                            q = fma2(v, both(-along), q) + both(-mean);
+                            u = g * both(r);
+                            v = q * both(r);
+                        } else {
+                            u = g;
+                            v = q;
                         }
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) { f[e] = df[e]; s[e] = ds[e]; }
                     }
+                    u.get(f);
+                    v.get(s);
                     if (h + n * by < count && w.on) Pairs<T, VEC>::put(o0, f, s, w);
                     o0 += os;
                 }
@@ -318,10 +361,13 @@ __global__ void __launch_bounds__(kWarps * 32, BACK ? 4 : 4) qk_norm_kernel(cons
         // the block's sums: lanes of a warp, then its warps in order
         __shared__ float sum[kWarps][2][kMaxHead];
 #pragma unroll
-        for (int k = 0; k < 2; ++k)
+        for (int k = 0; k < 2; ++k) {
+            float mf[4], ms[4];
+            gf[k].get(mf);
+            gs[k].get(ms);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                float a = gf[k][e], b = gs[k][e];
+                float a = mf[e], b = ms[e];
                 for (int m = 16; m >= p.lanes; m /= 2) {
                     a += __shfl_xor_sync(0xffffffffu, a, m);
                     b += __shfl_xor_sync(0xffffffffu, b, m);
@@ -331,6 +377,7 @@ __global__ void __launch_bounds__(kWarps * 32, BACK ? 4 : 4) qk_norm_kernel(cons
                     if (w.has(e, 1)) sum[warp][k][w.col(e, 1)] = b;
                 }
             }
+        }
         __syncthreads();
         for (int i = threadIdx.x; i < 2 * p.d; i += blockDim.x) {
             const int k = i >= p.d, c = i - k * p.d;
@@ -364,7 +411,7 @@ lstm_status launch_layout(QkArgs p, bool back, cudaStream_t cs)
         const int at_once = 32 / p.lanes, passes = ceil_div(p.heads[0], at_once) + ceil_div(p.heads[1], at_once);
         while (p.split < passes && p.rows * p.split < 152 * kWarps) p.split *= 2;
         if (p.split > passes) p.split = passes;
-        const int64_t blocks = std::min<int64_t>((p.rows * p.split + kWarps - 1) / kWarps, 152 * 6);
+        const int64_t blocks = std::min<int64_t>((p.rows * p.split + kWarps - 1) / kWarps, 152 * 3);
         qk_norm_kernel<T, VEC, false, HALF><<<(unsigned)blocks, kWarps * 32, 0, cs>>>(p);
     } else {
         p.parts = blocks_of(p.rows);
