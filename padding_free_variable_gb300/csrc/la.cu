@@ -253,19 +253,24 @@ LaArgs plan_args(const ScanPlan& sp, const lstm_la_shape& s, const float* log_de
     return a;
 }
 
+// The walks of `a`; cut sequences' starts are found first, by those of its jobs that have starts of their own.
 lstm_status run_jobs(const LaArgs& a, const lstm_la_shape& s, cudaStream_t cs)
 {
     if ((int64_t)a.count * a.ndir * a.heads * a.jobs > INT32_MAX) return LSTM_ERR_UNSUPPORTED;
     const bool bf16 = s.dtype == LSTM_BF16, tensor = bf16 && la_tensor_fits(a);
-    auto launch = [&](bool states) { return tensor ? launch_la_tensor(a, states, cs) : launch_la_general(a, bf16, states, cs); };
+    auto launch = [&](const LaArgs& b, bool states) { return tensor ? launch_la_tensor(b, states, cs) : launch_la_general(b, bf16, states, cs); };
     if (a.job[0].starts) {
-        const lstm_status st = launch(true);
+        LaArgs first = a;
+        first.jobs = 0;
+        for (int k = 0; k < a.jobs; ++k)
+            if (!a.job[k].flip_starts) first.job[first.jobs++] = a.job[k];
+        const lstm_status st = launch(first, true);
         if (st != LSTM_OK) return st;
-        const dim3 grid((unsigned)(a.B * a.ndir * a.heads), ceil_div(s.key_size * s.value_size, 256), a.jobs);
-        la_starts_kernel<<<grid, 256, 0, cs>>>(a);
+        const dim3 grid((unsigned)(a.B * a.ndir * a.heads), ceil_div(s.key_size * s.value_size, 256), first.jobs);
+        la_starts_kernel<<<grid, 256, 0, cs>>>(first);
         if (cudaGetLastError() != cudaSuccess) return LSTM_ERR_CUDA;
     }
-    return launch(false);
+    return launch(a, false);
 }
 
 lstm_status pass_through(const float* in, float* out, size_t bytes, cudaStream_t cs)
@@ -287,7 +292,7 @@ size_t lstm_la_scratch_bytes(const lstm_plan* plan, const lstm_la_shape* shape)
 {
     if (!plan || check_shape(shape) != LSTM_OK) return 0;
     const ScanPlan& sp = *static_cast<const ScanPlan*>(plan);
-    return std::max(start_bytes(sp, *shape, cut_level(sp, *shape, 1)), 3 * start_bytes(sp, *shape, cut_level(sp, *shape, 3)));
+    return std::max(start_bytes(sp, *shape, cut_level(sp, *shape, 1)), 2 * start_bytes(sp, *shape, cut_level(sp, *shape, 3)));
 }
 
 lstm_status lstm_la_fwd(const lstm_plan* plan, const lstm_la_shape* shape, const lstm_la_inputs* in,
@@ -342,7 +347,6 @@ lstm_status lstm_la_bwd(const lstm_plan* plan, const lstm_la_shape* shape, const
     const LaRows q = rows_of(in->q), k = rows_of(in->k), v = rows_of(in->v), g = dense_rows(dy, s);
     const size_t starts = start_bytes(sp, s, level);
     a.jobs = 3;
-    for (int n = 0; n < 3; ++n) a.job[n].starts = starts ? (float*)((char*)scratch + n * starts) : nullptr;
     LaJob &jv = a.job[0], &jk = a.job[1], &jq = a.job[2];
     jq.q = g; jq.k = v; jq.v = k; jq.out = rows_of(grads->dq);
     jq.a = s.value_size; jq.b = s.key_size; jq.init = s0; jq.flip = 1; jq.early = 1; jq.sP = jq.sI = s.scale; jq.pieces = 2;
@@ -350,6 +354,12 @@ lstm_status lstm_la_bwd(const lstm_plan* plan, const lstm_la_shape* shape, const
     jk.a = s.value_size; jk.b = s.key_size; jk.init = ds_n; jk.flip = 1; jk.back = 1; jk.sP = jk.sK = s.scale; jk.pieces = 2;
     jv.q = k; jv.k = q; jv.v = g; jv.out = rows_of(grads->dv);
     jv.a = s.key_size; jv.b = s.value_size; jv.init = ds_n; jv.back = 1; jv.sP = jv.sK = s.scale; jv.fin = ds0;
+    if (starts) {
+        // the errors in front of dk's pieces are dv's, transposed
+        jv.starts = jk.starts = (float*)scratch;
+        jk.flip_starts = 1;
+        jq.starts = (float*)((char*)scratch + starts);
+    }
     if (!starts && ds0 && ds0 == ds_n) {
         // dk reads the errors that dv's walk overwrites: it goes first (cut sequences read them before either walk)
         LaArgs first = a;

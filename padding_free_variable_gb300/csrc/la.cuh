@@ -27,9 +27,9 @@ struct LaJob {
     int a = 0, b = 0;                   // widths of q and k, of v and out
     const float* init = nullptr;        // [ndir][B][heads][a][b], or [b][a] with `flip`
     float* fin = nullptr;               // [ndir][B][heads][a][b]
-    float* starts = nullptr;            // cut sequences: Y in front of each piece, [entry][ndir * heads][a][b]
+    float* starts = nullptr;            // cut sequences: Y in front of each piece, [entry][ndir * heads][a][b] ([b][a] with `flip_starts`)
     float sP = 1.f, sI = 1.f, sK = 1.f;
-    int flip = 0, back = 0, early = 0;
+    int flip = 0, flip_starts = 0, back = 0, early = 0;
     int pieces = 3;                     // bf16 pieces of a weighted value in Y's products (tensor cores)
 };
 

@@ -107,12 +107,13 @@ __global__ void __launch_bounds__(kThreads) la_general_kernel(const LaArgs p)
     if (tid < kSteps) rows[tid] = row_of(c.begin);
     __syncthreads();
     {
-        const float first = j.early ? W[1] : 1.f;
+        const float first = j.early && !j.starts ? W[1] : 1.f;
+        const bool flip = j.starts ? j.flip_starts : j.flip;
         const float* from = STATES ? nullptr : j.starts ? la_start(p, j, c) : j.init ? j.init + state : nullptr;
         for (int x = warp; x < 4 * a4; x += kThreads / 32)
             for (int y = lane; y < 4 * b4; y += 32) {
                 float v = 0.f;
-                if (from && x < a && y < b) v = j.starts ? from[x * b + y] : first * from[j.flip ? y * a + x : x * b + y];
+                if (from && x < a && y < b) v = first * from[flip ? y * a + x : x * b + y];
                 Y[x * ldb + y] = v;
             }
     }

@@ -73,12 +73,27 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi)
 __device__ __forceinline__ float low(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float high(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
-// Two values less what their first piece holds.
+// Two values at once: one instruction of the fp32 pipe.
+__device__ __forceinline__ void mul2(float& x, float& y, float a, float b)
+{
+    asm("{\n .reg .b64 p, q;\n mov.b64 p, {%0, %1};\n mov.b64 q, {%2, %3};\n mul.rn.f32x2 p, p, q;\n mov.b64 {%0, %1}, p;\n}" : "+f"(x), "+f"(y) : "f"(a), "f"(b));
+}
+__device__ __forceinline__ void add2(float& x, float& y, float a, float b)
+{
+    asm("{\n .reg .b64 p, q;\n mov.b64 p, {%0, %1};\n mov.b64 q, {%2, %3};\n add.rn.f32x2 p, p, q;\n mov.b64 {%0, %1}, p;\n}" : "+f"(x), "+f"(y) : "f"(a), "f"(b));
+}
+// x = s x + a
+__device__ __forceinline__ void fma2(float& x, float& y, float s, float a, float b)
+{
+    asm("{\n .reg .b64 p, q, r;\n mov.b64 p, {%0, %1};\n mov.b64 q, {%2, %3};\n mov.b64 r, {%4, %4};\n fma.rn.f32x2 p, p, r, q;\n mov.b64 {%0, %1}, p;\n}"
+        : "+f"(x), "+f"(y) : "f"(a), "f"(b), "f"(s));
+}
+
+// Two values less what their first piece holds (the piece's sign is turned, so that it can be added).
 __device__ __forceinline__ uint32_t cut(float& x, float& y)
 {
-    const uint32_t w = pack2(x, y);
-    x -= low(w);
-    y -= high(w);
+    const uint32_t w = pack2(x, y), v = w ^ 0x80008000u;
+    add2(x, y, low(v), high(v));
     return w;
 }
 
@@ -222,7 +237,7 @@ __global__ void __launch_bounds__(Layout<A, B>::T, Layout<A, B>::CTAS) la_tensor
             for (int k = 0; k < L::YC; ++k) y[k] = 0.f;
             return false;
         }
-        const bool flip = j.flip && !j.starts;
+        const bool flip = j.starts ? j.flip_starts : j.flip;
         const float first = j.early && !j.starts ? exp2f(l2) : 1.f;
         if (!flip && ((uintptr_t)from & 15) == 0) {
 #pragma unroll
@@ -310,7 +325,9 @@ __global__ void __launch_bounds__(Layout<A, B>::T, Layout<A, B>::CTAS) la_tensor
                 uint4 v = *(const uint4*)(sm + L::V + v0);
                 if (s >= n) v = make_uint4(0, 0, 0, 0);
                 const float w = j.sK * exp2f(max(behind - s, 0) * l2);
-                float f[8] = {low(v.x) * w, high(v.x) * w, low(v.y) * w, high(v.y) * w, low(v.z) * w, high(v.z) * w, low(v.w) * w, high(v.w) * w};
+                float f[8] = {low(v.x), high(v.x), low(v.y), high(v.y), low(v.z), high(v.z), low(v.w), high(v.w)};
+#pragma unroll
+                for (int e = 0; e < 8; e += 2) mul2(f[e], f[e + 1], w, w);
                 uint4 a, b;
                 a.x = cut(f[0], f[1]); a.y = cut(f[2], f[3]); a.z = cut(f[4], f[5]); a.w = cut(f[6], f[7]);
                 *(uint4*)(sm + L::V1 + v0) = a;
@@ -355,22 +372,28 @@ __global__ void __launch_bounds__(Layout<A, B>::T, Layout<A, B>::CTAS) la_tensor
                 } else {
                     float s[32];
                     load_columns(L::S + 32 * b, s);
-                    if (b == quad) {
+                    if (b == quad && l2 < -3.f) {
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            const float s0 = lane >= 2 * e ? s[2 * e] * power[max(lane - 2 * e, 0)] : 0.f;
-                            const float s1 = lane >= 2 * e + 1 ? s[2 * e + 1] * power[max(lane - 2 * e - 1, 0)] : 0.f;
-                            w[e] = pack2(s0, s1);
-                        }
+                        for (int e = 0; e < 16; ++e)
+                            w[e] = pack2(s[2 * e] * power[max(lane - 2 * e, 0)], s[2 * e + 1] * power[max(lane - 2 * e - 1, 0)]);
                     } else {
-                        // lambda^(i-j) in two factors that are at most 1: from the block's last column on, and up to it
+                        // lambda^(i-j) in two factors: from the block's last column on, and up to it; within the diagonal block the
+                        // first is above 1, at most 2^93
                         const float f = exp2f((row - 32 * b - 31) * l2);
 #pragma unroll
                         for (int e = 0; e < 16; e += 2) {
-                            const float4 g = *(const float4*)(power + 32 + 2 * e);
-                            w[e] = pack2(s[2 * e] * (f * g.x), s[2 * e + 1] * (f * g.y));
-                            w[e + 1] = pack2(s[2 * e + 2] * (f * g.z), s[2 * e + 3] * (f * g.w));
+                            float4 g = *(const float4*)(power + 32 + 2 * e);
+                            mul2(g.x, g.y, f, f);
+                            mul2(g.z, g.w, f, f);
+                            mul2(s[2 * e], s[2 * e + 1], g.x, g.y);
+                            mul2(s[2 * e + 2], s[2 * e + 3], g.z, g.w);
+                            w[e] = pack2(s[2 * e], s[2 * e + 1]);
+                            w[e + 1] = pack2(s[2 * e + 2], s[2 * e + 3]);
                         }
+                    }
+                    if (b == quad) {                    // what is later than the row: bits, whatever they say, to zero
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) w[e] &= lane > 2 * e ? 0xffffffffu : lane == 2 * e ? 0xffffu : 0u;
                     }
                 }
                 tc::tmem_st_32x32b_x16(mine + L::S + 32 * b, w);
@@ -379,7 +402,7 @@ __global__ void __launch_bounds__(Layout<A, B>::T, Layout<A, B>::CTAS) la_tensor
                 const float f = j.sI * exp2f(row * l2);
                 load_columns(L::O + o0, o);
 #pragma unroll
-                for (int k = 0; k < L::OC; ++k) o[k] *= f;
+                for (int k = 0; k < L::OC; k += 2) mul2(o[k], o[k + 1], f, f);
             } else {
 #pragma unroll
                 for (int k = 0; k < L::OC; ++k) o[k] = 0.f;
@@ -418,7 +441,7 @@ __global__ void __launch_bounds__(Layout<A, B>::T, Layout<A, B>::CTAS) la_tensor
             float v[L::OC];
             load_columns(L::O + o0, v);
 #pragma unroll
-            for (int k = 0; k < L::OC; ++k) v[k] = fmaf(j.sP, v[k], o[k]);
+            for (int k = 0; k < L::OC; k += 2) fma2(v[k], v[k + 1], j.sP, o[k], o[k + 1]);
 #pragma unroll
             for (int k = 0; k < CPR; ++k)
                 *(uint4*)(stage + lane * 2 * L::OC + ((k ^ ((lane >> 1) & (CPR - 1))) << 4)) =
@@ -446,7 +469,7 @@ __global__ void __launch_bounds__(Layout<A, B>::T, Layout<A, B>::CTAS) la_tensor
             const float keep = exp2f(decay_of(at, u) * l2);
             load_columns(L::Y + y0, v);
 #pragma unroll
-            for (int k = 0; k < L::YC; ++k) y[k] = fmaf(keep, y[k], v[k]);
+            for (int k = 0; k < L::YC; k += 2) fma2(y[k], y[k + 1], keep, v[k], v[k + 1]);
         }
         if (!STATES) __syncthreads();                   // the rows have left the pieces' place
         if (!final) {
