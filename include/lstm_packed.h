@@ -931,9 +931,13 @@ lstm_status lstm_block_norm_bwd(const lstm_block_norm_shape* shape, const lstm_b
  * the values, as operands of a product; states are carried in fp32 and enter
  * products as two or three bf16 pieces.  Every order of summation is fixed by
  * the plan and the shape: repeated calls agree bitwise.  A log_decay above 0
- * counts as 0, one below -138 as -138 (lambda^n = 0 for n > 0 in fp32).  An
- * infinity or NaN in a frame may reach every frame of its head and sequence,
- * earlier ones too, but no other head, direction or sequence.
+ * counts as 0, one below -138 (or NaN) as -138 (lambda^n = 0 for n > 0 in
+ * fp32).  An infinity or NaN in a frame may reach every frame of its head and
+ * sequence, earlier ones too, but no other head, direction or sequence.
+ *
+ * Outputs and gradients must not overlap what the call reads (states may be
+ * carried in place, as said below).  Sequences of more than 2^30 steps are
+ * LSTM_ERR_UNSUPPORTED.
  *
  * Pointers need the alignment of their element type only, scratch 16 bytes.
  * Every device pointer belongs to the current device.  bf16 rows whose

@@ -16,6 +16,7 @@
 namespace lstm {
 
 constexpr int kLaMax = 128;             // largest key or value size
+constexpr int kLaMaxSteps = 1 << 30;    // longest sequence: a step and a chunk more stay within 32 bits
 
 struct LaRows {
     const void* p = nullptr;

@@ -1,8 +1,11 @@
-// la_general.cu -- linear attention on CUDA cores: fp32, and bf16 rows that the tensor cores' loads cannot take.
+// la_general.cu -- linear attention on CUDA cores: fp32, and bf16 rows that la_tensor.cuh's loads cannot take.
 //
 // A CTA walks one head of one sequence (or a piece of it) 64 steps at a time, everything in shared memory in fp32: the
-// products of the chunk's steps with each other (64 x 64), the outputs from them and from the state, then the state.
-// Per step that is 4 a b products for the state and 64 (a + b) between steps.
+// products of the chunk's steps with each other (64 x 64, steps that no row sees left out), the outputs from them and from the
+// state, then the state.  Per step that is 4 a b operations for the state and some 80 (a + b) between steps.  Bound by fp32
+// instructions and shared memory: 29008 steps of 8 heads of 32 + 64 values 164 us (half of the cores' fp32 rate within a
+// chunk), 12364 steps of 2 x 3 heads of 37 + 53 values 80 us.  Three tf32 products on mma.sync in place of each fp32
+// product took 178 us and six times the rounding error (tensor cores cut off sums).
 #include <type_traits>
 
 #include "la.cuh"
@@ -286,7 +289,7 @@ lstm_status launch_la_general(const LaArgs& a, bool bf16, bool states, cudaStrea
         const LaJob& j = a.job[k];
         whole = whole && j.a % 4 == 0 && j.b % 4 == 0;
         for (const LaRows* r : {&j.q, &j.k, &j.v, &j.out})
-            whole = whole && (uintptr_t)r->p % (4 * e) == 0 && r->row % 4 == 0 && (a.ndir == 1 || r->dir % 4 == 0) && (a.heads == 1 || r->head % 4 == 0);
+            whole = whole && (uintptr_t)r->p % (4 * e) == 0 && (a.rows == 1 || r->row % 4 == 0) && (a.ndir == 1 || r->dir % 4 == 0) && (a.heads == 1 || r->head % 4 == 0);
     }
     if (bf16) return whole ? launch<__nv_bfloat16, 4>(a, states, cs) : launch<__nv_bfloat16, 1>(a, states, cs);
     return whole ? launch<float, 4>(a, states, cs) : launch<float, 1>(a, states, cs);

@@ -9,7 +9,7 @@ bool la_tensor_fits(const LaArgs& a)
         const LaJob& j = a.job[k];
         if (j.a % 8 || j.b % 8) return false;
         for (const LaRows* r : {&j.q, &j.k, &j.v, &j.out})
-            if ((uintptr_t)r->p % 16 || r->row % 8 || (a.ndir > 1 && r->dir % 8) || (a.heads > 1 && r->head % 8)) return false;
+            if ((uintptr_t)r->p % 16 || (a.rows > 1 && r->row % 8) || (a.ndir > 1 && r->dir % 8) || (a.heads > 1 && r->head % 8)) return false;
     }
     return true;
 }

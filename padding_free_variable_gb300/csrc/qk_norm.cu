@@ -2,8 +2,11 @@
 //
 // A head lies on 1 to 32 lanes, four pairs of values each: the pairs that are rotated together, so that a rotation needs
 // no other lane, and a norm a few shuffles.  A warp takes a row (or, where rows are few, a part of one) and walks its
-// heads 32 / lanes at a time, several loads ahead: sines and cosines are found once a row.  Bound by memory: every
-// value is read once and written once.
+// heads 32 / lanes at a time, several loads ahead: sines and cosines are found once a row and pair and shared by the warp.
+// Every value is read once and written once; bound by instructions and latency short of memory: 40555 rows of 32 heads of
+// 64 bf16 values, half of each rotated, 79 us forward (62 % of the copy rate) and 147 us backward (50 %); 9564 rows of 7 heads of 74
+// fp32 values, read one by one, 28 and 36 us.  Four lanes' sines each lane for itself, and selects between the layouts, took 125
+// and 194 us.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -14,6 +17,8 @@ namespace lstm {
 
 namespace {
 
+// kMaxParts: the CTAs of the backward pass, three an SM, as many as its registers let the GPU hold; four an SM in two rounds 201 us
+// instead of 151.  A constant, so that the order of the weights' sums depends on the rows alone.
 constexpr int kWarps = 8, kMaxParts = 456, kMaxHead = 256;
 
 struct QkArgs {

@@ -851,22 +851,20 @@ def la_shape(num_heads, key_size, value_size, num_directions: int = 1, bf16: boo
     return s
 
 
-def _la_rows(t, dt, want, name, dev):
-    """(address, row, direction and head stride) of a [rows, ndir, heads, width] view whose values lie next to each other."""
-    if t.dtype is not dt or t.shape != want or t.get_device() != dev:
-        raise ValueError(f"{name}: expected a {dt} tensor of shape {tuple(want)} on cuda:{dev}, got {t.dtype} {tuple(t.shape)} on "
-                         f"{t.device}")
-    r, d, h, one = t.stride()
-    if one != 1 and want[3] > 1:
-        raise ValueError(f"{name}: a head's values have to lie next to each other")
-    # the stride of a single row, direction or head is never stepped over
-    return t.data_ptr(), r if want[0] > 1 else 0, d if want[1] > 1 else 0, h if want[2] > 1 else 0
-
-
 def _la_three(key, q, k, v, rows, names, dev):
+    """lstm_la_inputs of three [rows, ndir, heads, width] views whose heads' values lie next to each other."""
     _, nd, heads, dk, dv, dt = key
-    return _lib.pack_la(*_la_rows(q, dt, (rows, nd, heads, dk), names[0], dev), *_la_rows(k, dt, (rows, nd, heads, dk), names[1], dev),
-                        *_la_rows(v, dt, (rows, nd, heads, dv), names[2], dev))
+    a, b = (rows, nd, heads, dk), (rows, nd, heads, dv)
+    if not (q.dtype is dt and k.dtype is dt and v.dtype is dt and q.shape == a and k.shape == a and v.shape == b and
+            q.get_device() == dev and k.get_device() == dev and v.get_device() == dev):
+        for t, want, name in zip((q, k, v), (a, a, b), names):
+            if t.dtype is not dt or t.shape != want or t.get_device() != dev:
+                raise ValueError(f"{name}: expected a {dt} tensor of shape {want} on cuda:{dev}, got {t.dtype} {tuple(t.shape)} "
+                                 f"on {t.device}")
+    (qr, qd, qh, q1), (kr, kd, kh, k1), (vr, vd, vh, v1) = q.stride(), k.stride(), v.stride()
+    if (dk > 1 and (q1 != 1 or k1 != 1)) or (dv > 1 and v1 != 1):
+        raise ValueError(f"{', '.join(names)}: a head's values have to lie next to each other")
+    return _lib.pack_la(q.data_ptr(), qr, qd, qh, k.data_ptr(), kr, kd, kh, v.data_ptr(), vr, vd, vh)
 
 
 _LA_IN, _LA_GRADS = ("q", "k", "v"), ("dq", "dk", "dv")

@@ -382,6 +382,37 @@ def test_single_frames_captured():
     assert (cache.double() - want).abs().max() < 40 * 2.0 ** -24 * want.abs().max()
 
 
+def test_states_past_32_bits():
+    # a cache of 2.4e9 values: its last slots lie beyond what 32 bits count
+    o, slots = ops(), 73000
+    shape = o.la_shape(2, 128, 128, scale=0.5)
+    q, k, v = (torch.randn(3, 1, 2, 128, device="cuda") for _ in range(3))
+    ld = torch.full((1, 2), -0.3, device="cuda")
+    cache = torch.empty(slots, 2, 128, 128, device="cuda")
+    at = torch.tensor([slots - 1, 65537, 0], dtype=torch.int32, device="cuda")
+    state = torch.randn(3, 2, 128, 128, device="cuda")
+    cache[at.long()] = state
+    y = torch.empty(3, 1, 2, 128, device="cuda")
+    o.la_step(shape, q, k, v, ld, cache, cache, y, at)
+    num = lambda t: t.double().cpu().numpy()  # noqa: E731
+    w = ref.attend([1] * 3, num(q), num(k), num(v), num(ld), np.float32(0.5), num(state)[None])
+    near(y, w["y"], w["~y"], "f32", "y")
+    near(cache[at.long()], w["s_n"][0], w["~s_n"][0], "f32", "state")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_rows_past_32_bits(dtype):
+    # rows 2^28 + 64 values apart: the last one starts beyond 2^31 values
+    c = Case([6, 3, 1], 1, 1, 64, 64, dtype, seed=5)
+    step = 2 ** 28 + 64
+    buf = torch.empty(9 * step + 512, dtype=DT[dtype], device="cuda")
+    wide = [buf.as_strided((10, 1, 1, 64), (step, 64, 64, 1), 64 * m) for m in range(6)]
+    for m in range(3):
+        wide[m].copy_(c.x[m])
+    c.x, c.g = wide[:3], wide[3:]
+    c.check()
+
+
 def test_no_frames_and_bad_arguments():
     o = ops()
     from padding_free_variable_gb300._lib import LSTMError
