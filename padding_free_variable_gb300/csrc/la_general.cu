@@ -2,10 +2,11 @@
 //
 // A CTA walks one head of one sequence (or a piece of it) 64 steps at a time, everything in shared memory in fp32: the
 // products of the chunk's steps with each other (64 x 64, steps that no row sees left out), the outputs from them and from the
-// state, then the state.  Per step that is 4 a b operations for the state and some 80 (a + b) between steps.  Bound by fp32
-// instructions and shared memory: 29008 steps of 8 heads of 32 + 64 values 164 us (half of the cores' fp32 rate within a
-// chunk), 12364 steps of 2 x 3 heads of 37 + 53 values 80 us.  Three tf32 products on mma.sync in place of each fp32
-// product took 178 us and six times the rounding error (tensor cores cut off sums).
+// state, then the state.  Per step that is 4 a b operations for the state and some 80 (a + b) between steps.  Bound by shared
+// memory (three quarters of its wavefronts) and fp32 instructions: 29008 steps of 8 heads of 32 + 64 values, cut into pieces,
+// 226 us, the three gradients 579 us; with registers for two CTAs an SM in place of three 241 and 611.  37 sequences of up to
+// 700 steps of 2 x 3 heads of 37 + 53 values 123 us: the longest one's chunks.  Three tf32 products on mma.sync in place of
+// each fp32 product took a tenth longer and six times the rounding error (tensor cores cut off sums).
 #include <type_traits>
 
 #include "la.cuh"
@@ -76,7 +77,7 @@ __device__ __forceinline__ void fma4(float4& s, float x, const float4& y)
 
 // STATES: only what a piece adds to Y, into `starts` (pieces with one behind them).
 template <typename T, int V, bool STATES>
-__global__ void __launch_bounds__(kThreads) la_general_kernel(const LaArgs p)
+__global__ void __launch_bounds__(kThreads, 3) la_general_kernel(const LaArgs p)
 {
     extern __shared__ __align__(16) float sm[];
     const LaPart c = la_part(p, blockIdx.x);
