@@ -5,7 +5,7 @@
 // heads 32 / lanes at a time, several loads ahead: sines and cosines are found once a row and pair and shared by the warp.
 // Every value is read once and written once; bound by instructions and latency short of memory: 40555 rows of 32 heads of
 // 64 bf16 values, half of each rotated, 79 us forward (62 % of the copy rate) and 147 us backward (50 %); 9564 rows of 7 heads of 74
-// fp32 values, read one by one, 28 and 36 us.  Four lanes' sines each lane for itself, and selects between the layouts, took 125
+// fp32 values, read one by one, 27 and 33 us.  Four lanes' sines each lane for itself, and selects between the layouts, took 125
 // and 194 us.
 #include <algorithm>
 #include <cmath>
@@ -85,26 +85,29 @@ template <typename T> __device__ __forceinline__ T narrow(float v);
 template <> __device__ __forceinline__ float narrow<float>(float v) { return v; }
 template <> __device__ __forceinline__ __nv_bfloat16 narrow<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
-// Where a lane's four pairs (from 4 l on) lie.  VEC: in two groups of four neighbours: with HALF the pairs' first and second
-// values (what is not rotated has no pairs), else two pairs each.  Otherwise every value has a column of its own.
+// Where a lane's four pairs lie.  VEC: pairs 4 l to 4 l + 3, in two groups of four neighbours: with HALF the pairs' first and
+// second values (what is not rotated has no pairs), else two pairs each.  Otherwise every value has a column of its own, and
+// pairs next to each other belong to lanes next to each other, so that a warp's single values share their sectors.
 template <bool VEC, bool HALF> struct Lane {
-    int pair, d, turned;                // turned: pairs of halves, `turned` apart
+    int pair, by, d, turned;            // first pair, distance to the next; turned: pairs of halves, `turned` apart
     int at[VEC ? 1 : 8];                // each value's column, -1: none
     bool on;
     __device__ __forceinline__ void set(const QkArgs& p, int l)
     {
-        pair = 4 * l;
+        pair = VEC ? 4 * l : l;
+        by = VEC ? 1 : p.lanes;
         d = p.d;
         turned = HALF ? p.rotary / 2 : 0;
         on = 2 * pair < d;
         if (!VEC) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const int k = pair + e / 2, c = HALF && k < turned ? k + e % 2 * turned : 2 * k + e % 2;
+                const int k = pair_of(e / 2), c = HALF && k < turned ? k + e % 2 * turned : 2 * k + e % 2;
                 at[VEC ? 0 : e] = c < d ? c : -1;
             }
         }
     }
+    __device__ __forceinline__ int pair_of(int e) const { return pair + e * by; }
     __device__ __forceinline__ int col(int e, int which) const
     {
         if (!VEC) return at[VEC ? 0 : 2 * e + which];
@@ -258,9 +261,9 @@ __global__ void __launch_bounds__(kWarps * 32, 3) qk_norm_kernel(const QkArgs p)
             __syncwarp();
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                if (4 * l + e < p.rotary / 2) {
-                    co[e] = turns[warp][0][4 * l + e];
-                    si[e] = turns[warp][1][4 * l + e];
+                if (w.pair_of(e) < p.rotary / 2) {
+                    co[e] = turns[warp][0][w.pair_of(e)];
+                    si[e] = turns[warp][1][w.pair_of(e)];
                 }
         }
         // the heads of one operand, `at_once` a pass; of a row's passes this warp takes every split-th
