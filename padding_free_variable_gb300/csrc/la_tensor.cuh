@@ -245,11 +245,16 @@ __global__ void __launch_bounds__(Layout<A, B>::T, Layout<A, B>::CTAS) la_tensor
         const bool flip = j.starts ? j.flip_starts : j.flip;
         const float first = j.early && !j.starts ? exp2f(l2) : 1.f;
         if (!flip && ((uintptr_t)from & 15) == 0) {
+            float4 in[A * B / 4 / L::T];        // all reads on their way before the first is stored
 #pragma unroll
-            for (int k = 0; k < A * B / 4 / L::T; ++k) {        // all reads on their way together
+            for (int k = 0; k < A * B / 4 / L::T; ++k) {
                 const int i = k * L::T + tid, r = i / (B / 4), f = i % (B / 4);
-                const bool in = r < j.a && 4 * f < j.b;
-                *(float4*)(sm + whole_at(r, f)) = in ? *(const float4*)(from + r * j.b + 4 * f) : make_float4(0.f, 0.f, 0.f, 0.f);
+                in[k] = r < j.a && 4 * f < j.b ? *(const float4*)(from + r * j.b + 4 * f) : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+#pragma unroll
+            for (int k = 0; k < A * B / 4 / L::T; ++k) {
+                const int i = k * L::T + tid;
+                *(float4*)(sm + whole_at(i / (B / 4), i % (B / 4))) = in[k];
             }
             __syncthreads();
 #pragma unroll
