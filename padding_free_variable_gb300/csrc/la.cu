@@ -226,7 +226,7 @@ LaRows dense_rows(const void* p, const lstm_la_shape& s)
 // The level of the plan's pieces that `jobs` walks of every sequence run over (the last one: uncut).  A sequence is walked
 // chunk by chunk; where the longest one runs far past an even share of all steps for the CTAs that the GPU holds, sequences
 // are cut, and every piece's keys and values are read once more for what it adds to the state.  One sequence of 65536 steps of 8
-// heads of 128 bf16 values: pieces of an eighth of a share or more 401 us, of a quarter 413, of a sixteenth 451, uncut 3424; two
+// heads of 128 bf16 values: pieces of an eighth of a share or more 401 us (390 by now), of a quarter 413, of a sixteenth 451, uncut 3424; two
 // of 29008 steps together, 8 heads of 32 + 64 fp32 values, forward / backward 226 / 579 us, uncut 1880 / 1951.  Just past the rule's
 // edge both are alike or cutting loses: 37 sequences of up to 700 steps, 2 x 3 heads of 37 + 53 fp32 values, 122 and 123 us; 24
 // of 200 to 2400 steps, 8 heads of 64 bf16 values, 112 and 100 us.

@@ -13,7 +13,7 @@
 //
 // Bound by neither memory nor the tensor cores alone but by the chain S, P, O', Y of a chunk: 40555 steps of 2 x 8 heads of
 // 64 values 148 us (38 % of the copy rate; the tensor cores 20 %, issue 45 %), 65536 steps of 8 heads of 128 as one sequence
-// 131 us for the pieces' sums, 29 us for their starts and 240 us for the outputs.  Rows by TMA gathers of four rows took 75 to
+// 130 us for the pieces' sums, 28 us for their starts and 232 us for the outputs.  Rows by TMA gathers of four rows took 75 to
 // 84 cycles an instruction, 218 us instead of 158; the sums for Y in front of S's pass instead of behind it, 179 us.
 //
 // CTAs stay on the GPU and take every so-many-th walk; the next chunk's rows, of the same walk or the next, are on their way
@@ -328,11 +328,14 @@ __global__ void __launch_bounds__(Layout<A, B>::T, Layout<A, B>::CTAS) la_tensor
         uint4 third[L::in_q ? IT : 1];
         if (sum) {
             const int behind = decay_of(at, u);
+            uint4 in[IT];
+#pragma unroll
+            for (int i = 0; i < IT; ++i) in[i] = *(const uint4*)(sm + L::V + tile_at(i * EACH + tid / CH, tid % CH, kPanel));
 #pragma unroll
             for (int i = 0; i < IT; ++i) {
                 const int s = i * EACH + tid / CH;
                 const uint32_t v0 = tile_at(s, tid % CH, kPanel);
-                uint4 v = *(const uint4*)(sm + L::V + v0);
+                uint4 v = in[i];
                 if (s >= n) v = make_uint4(0, 0, 0, 0);
                 const float w = j.sK * exp2f(max(behind - s, 0) * l2);
                 float f[8] = {low(v.x), high(v.x), low(v.y), high(v.y), low(v.z), high(v.z), low(v.w), high(v.w)};
@@ -458,11 +461,16 @@ __global__ void __launch_bounds__(Layout<A, B>::T, Layout<A, B>::CTAS) la_tensor
                     make_uint4(pack2(v[8 * k], v[8 * k + 1]), pack2(v[8 * k + 2], v[8 * k + 3]), pack2(v[8 * k + 4], v[8 * k + 5]),
                                pack2(v[8 * k + 6], v[8 * k + 7]));
             __syncwarp();
+            uint4 w[CPR];
 #pragma unroll
             for (int k = 0; k < CPR; ++k) {
                 const int r = k * RPT + lane / CPR, ch = lane % CPR;
-                const uint4 w = *(const uint4*)(stage + r * 2 * L::OC + ((ch ^ ((r >> 1) & (CPR - 1))) << 4));
-                if (quad * 32 + r < n && o0 + ch * 8 < j.b) *(uint4*)(out + rows_out[k] * j.out.row + ch * 8) = w;
+                w[k] = *(const uint4*)(stage + r * 2 * L::OC + ((ch ^ ((r >> 1) & (CPR - 1))) << 4));
+            }
+#pragma unroll
+            for (int k = 0; k < CPR; ++k) {
+                const int r = k * RPT + lane / CPR, ch = lane % CPR;
+                if (quad * 32 + r < n && o0 + ch * 8 < j.b) *(uint4*)(out + rows_out[k] * j.out.row + ch * 8) = w[k];
             }
         }
         if (sum) {
