@@ -111,9 +111,9 @@ __global__ void __launch_bounds__(Layout<A, B>::T, Layout<A, B>::CTAS) la_tensor
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, quad = warp % 4, part = warp / 4;
     const uint32_t base = tc::smem_u32(sm);
     float* const powers = (float*)(sm + L::POWERS);
-    // S and O, O', the sum for Y are done
+    // S and O, O', the sum for Y are done; everything is, after a wait that ran out
     uint64_t* const bar = (uint64_t*)(sm + L::BARS);
-    enum { DONE_S = 0, DONE_O, DONE_Y, BARRIERS };
+    enum { DONE_S = 0, DONE_O, DONE_Y, DRAINED, BARRIERS };
     uint32_t* const slot_of_tmem = (uint32_t*)(bar + BARRIERS);
     int* const stop = (int*)(slot_of_tmem + 1);
     if (tid == 0) {
@@ -521,6 +521,11 @@ __global__ void __launch_bounds__(Layout<A, B>::T, Layout<A, B>::CTAS) la_tensor
         u = then_u;
         more = next;
     }
+    if (*(volatile int*)stop && tid == 0) {             // products still on their way read shared memory and write tensor memory
+        tc::mma_commit(bar + DRAINED);
+        tc::mbar_wait(bar + DRAINED, 0, 100000000ull);
+    }
+    __syncwarp();
     cp_async_wait();
     tc::tc_fence_before_sync();
     __syncthreads();

@@ -312,6 +312,17 @@ def test_streams_and_graphs(dtype, size, lens):
     d.compare(d.want())
 
 
+def test_a_wait_that_runs_out_leaves_the_device_usable():
+    # a limit that a product may or may not meet: either way the call ends, and the next one is right
+    c = Case([400, 70, 1], 2, 2, 64, 64, "bf16", seed=8)
+    c.plan.set_wait_limit(1)
+    c.forward()
+    c.backward()
+    assert c.plan.poll() in (0, 4)
+    c.plan.set_wait_limit(2000000000)
+    c.check()
+
+
 # ------------------------------------------------------------------ single frames
 
 STEPS = [(1, 1, 1, 1, "f32"), (3, 2, 16, 8, "f32"), (9, 3, 37, 53, "f32"), (9, 3, 37, 53, "bf16"), (40, 8, 64, 64, "bf16"),
